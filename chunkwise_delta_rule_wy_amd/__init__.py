@@ -25,6 +25,8 @@ import torch
 __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_noalloc", "bwd_workspace_bytes", "recurrent_step",
            "longhorn_eps", "longhorn_eps_bwd", "longhorn_fwd", "longhorn_bwd", "prologue", "prologue_bwd",
            "short_conv", "short_conv_bwd", "DeltaRule", "delta_rule", "ShortConv", "short_conv_fn",
+           "ssm_fwd", "ssm_bwd", "ssm_step", "ssm_scan", "SsmScan", "conv_silu", "conv_silu_bwd", "conv_silu_step",
+           "conv_silu_fn", "ConvSilu", "gated_norm", "gated_norm_bwd", "gated_norm_fn", "GatedNorm",
            "load_library", "LIB_PATH", "DnError"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdn.so")
@@ -45,6 +47,12 @@ class _Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _SsmShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+                ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -101,6 +109,26 @@ def load_library():
     lib.dn_short_conv_l2.restype = ctypes.c_int
     lib.dn_short_conv_l2_bwd.argtypes = [ctypes.c_int32] * 7 + [P] * 6 + [P]
     lib.dn_short_conv_l2_bwd.restype = ctypes.c_int
+    I, Z = ctypes.c_int32, ctypes.c_size_t
+    SS = ctypes.POINTER(_SsmShape)
+    lib.dn_ssm_fwd_workspace.argtypes = lib.dn_ssm_bwd_workspace.argtypes = [SS]
+    lib.dn_ssm_fwd_workspace.restype = lib.dn_ssm_bwd_workspace.restype = Z
+    lib.dn_ssm_fwd.argtypes = [SS] + [P] * 9 + [P, P] + [P, Z, P]
+    lib.dn_ssm_bwd.argtypes = [SS] + [P] * 9 + [P, P] + [P] * 8 + [P, Z, P]
+    lib.dn_ssm_step.argtypes = [I] * 6 + [P] * 9 + [P]
+    lib.dn_conv_silu.argtypes = [I] * 7 + [P] * 7 + [P]
+    lib.dn_conv_silu_bwd_workspace.argtypes = [I] * 5
+    lib.dn_conv_silu_bwd_workspace.restype = Z
+    lib.dn_conv_silu_bwd.argtypes = [I] * 7 + [P] * 11 + [P, Z, P]
+    lib.dn_conv_silu_step.argtypes = [I] * 5 + [P] * 5 + [P]
+    lib.dn_gated_norm.argtypes = [ctypes.c_int64, I, I, I] + [P] * 3 + [ctypes.c_float, I] + [P] + [P]
+    lib.dn_gated_norm_bwd_workspace.argtypes = [ctypes.c_int64, I, I]
+    lib.dn_gated_norm_bwd_workspace.restype = Z
+    lib.dn_gated_norm_bwd.argtypes = ([ctypes.c_int64, I, I, I] + [P] * 3 + [ctypes.c_float, I] + [P] * 4
+                                      + [P, Z, P])
+    for name in ("ssm_fwd", "ssm_bwd", "ssm_step", "conv_silu", "conv_silu_bwd", "conv_silu_step", "gated_norm",
+                 "gated_norm_bwd"):
+        getattr(lib, "dn_" + name).restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -565,3 +593,291 @@ def short_conv_fn(x, w, cu_seqlens=None, l2norm=False):
     """Differentiable short convolution (optionally with the per-head L2
     normalisation fused in)."""
     return ShortConv.apply(x, w, cu_seqlens, l2norm)
+
+
+# ------------------------------------------------- the state space mixer
+
+
+def _call(name, dev, *args):
+    """Call a library function on ``dev``'s current stream, with ``dev`` as
+    the current device (kernels start on the current device)."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    _check(name, status)
+
+
+def _gpu(t, name, dims, dtypes):
+    if not isinstance(t, torch.Tensor) or t.dim() not in dims:
+        raise ValueError("%s must be a tensor of %s dimensions" % (name, " or ".join(str(d) for d in dims)))
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    return t.device
+
+
+def _seqs(B, cu_seqlens, dev):
+    """The number of sequences: B, or that of the packed offsets (B == 1)."""
+    if cu_seqlens is None:
+        return B
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a 1-d tensor of at least two offsets")
+    if B != 1:
+        raise ValueError("packed sequences need a batch of one")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+    return cu_seqlens.numel() - 1
+
+
+def _ssm_args(q, k, v, dt, A, dt_bias, skip, dtypes, dims):
+    """(device, leading sizes, H, G, Dk, Dv) of a scan's inputs, checked."""
+    dev = _gpu(v, "v", (dims,), dtypes)
+    _gpu(q, "q", (dims,), (v.dtype,))
+    lead, H, Dv, G, Dk = tuple(v.shape[:-2]), v.shape[-2], v.shape[-1], q.shape[-2], q.shape[-1]
+    if G == 0 or H % G:
+        raise ValueError("q has %d heads, which do not divide v's %d" % (G, H))
+    _need(q, "q", v.dtype, lead + (G, Dk), dev)
+    _need(k, "k", v.dtype, lead + (G, Dk), dev)
+    _need(v, "v", v.dtype, lead + (H, Dv), dev)
+    for t, name, shape in ((dt, "dt", lead + (H,)), (A, "A", (H,))):
+        if t is None:
+            raise TypeError("%s is required" % name)
+        _need(t, name, torch.float32, shape, dev)
+    _need(dt_bias, "dt_bias", torch.float32, (H,), dev)
+    _need(skip, "skip", torch.float32, (H,), dev)
+    return dev, lead, H, G, Dk, Dv
+
+
+def ssm_fwd(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None, output_final_state=True):
+    """Forward pass of the selective state space scan (``dn_ssm_fwd``):
+
+        s_t = softplus(dt_t + dt_bias),  S_t = exp(s_t A) S_{t-1} + s_t v_t k_t^T,
+        o_t = S_t q_t + skip v_t.
+
+    q, k ``[B,T,G,Dk]`` and v ``[B,T,H,Dv]`` bfloat16, G dividing H (head h
+    reads group ``h // (H // G)``); dt ``[B,T,H]``, A, dt_bias, skip ``[H]``
+    float32 (dt_bias, skip None: zero); h0 ``[N,H,Dk,Dv]`` float32 or None;
+    cu_seqlens int32 ``[N+1]`` on the device for packed sequences (B == 1).
+    Returns ``(o, hT)`` (hT None unless output_final_state)."""
+    lib = load_library()
+    dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
+    N = _seqs(B, cu_seqlens, dev)
+    _need(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
+    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
+    o = torch.empty_like(v)
+    hT = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev) if output_final_state else None
+    wsb = lib.dn_ssm_fwd_workspace(s)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_ssm_fwd", dev, s, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(dt_bias), _ptr(skip), _ptr(h0),
+          _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(ws), wsb)
+    return o, hT
+
+
+def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
+    """Backward pass of ``<dO, o> + <dhT, hT>`` of ``ssm_fwd`` (``dn_ssm_bwd``;
+    the states are recomputed).  Returns a dict: dq, dk, dv in bfloat16, ddt,
+    dA, ddt_bias, dskip (None without the parameter) and dh0 in float32."""
+    lib = load_library()
+    dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
+    N = _seqs(B, cu_seqlens, dev)
+    _need(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
+    if dO is None:
+        raise TypeError("dO is required")
+    _need(dO, "dO", v.dtype, tuple(v.shape), dev)
+    _need(dhT, "dhT", torch.float32, (N, H, Dk, Dv), dev)
+    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
+    gr = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), ddt=torch.empty_like(dt),
+              dA=torch.empty_like(A), ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias),
+              dskip=None if skip is None else torch.empty_like(skip),
+              dh0=torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev))
+    wsb = lib.dn_ssm_bwd_workspace(s)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_ssm_bwd", dev, s, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(dt_bias), _ptr(skip), _ptr(h0),
+          _ptr(cu_seqlens), _ptr(dO), _ptr(dhT), *[_ptr(g) for g in gr.values()], _ptr(ws), wsb)
+    return gr
+
+
+def ssm_step(q, k, v, dt, A, dt_bias, skip, state):
+    """One token of every sequence (``dn_ssm_step``): q, k ``[B,G,Dk]``, v
+    ``[B,H,Dv]`` (float32 or bfloat16, one dtype), dt ``[B,H]`` float32, state
+    ``[B,H,Dk,Dv]`` float32 updated in place.  Returns o ``[B,H,Dv]``."""
+    dev, (B,), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, tuple(_DTYPES), 3)
+    if state is None:
+        raise TypeError("state is required")
+    _need(state, "state", torch.float32, (B, H, Dk, Dv), dev)
+    o = torch.empty_like(v)
+    _call("dn_ssm_step", dev, B, H, G, Dk, Dv, _DTYPES[v.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A),
+          _ptr(dt_bias), _ptr(skip), _ptr(state), _ptr(o))
+    return o
+
+
+def _conv_silu_args(x, w, bias, state, cu_seqlens, dims):
+    """(device, leading sizes, H, D, W, sequences), checked; state may be None."""
+    dev = _gpu(x, "x", (dims,), tuple(_DTYPES))
+    lead, (H, D) = tuple(x.shape[:-2]), x.shape[-2:]
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be a [H, D, W] tensor")
+    W = w.shape[2]
+    N = _seqs(lead[0], cu_seqlens, dev)
+    _need(x, "x", x.dtype, tuple(x.shape), dev)
+    _need(w, "w", torch.float32, (H, D, W), dev)
+    _need(bias, "bias", torch.float32, (H, D), dev)
+    _need(state, "state", x.dtype, (N, max(W - 1, 0), H, D), dev)
+    return dev, lead, H, D, W, N
+
+
+def conv_silu(x, w, bias=None, s0=None, cu_seqlens=None):
+    """Depthwise causal short convolution with bias and SiLU (``dn_conv_silu``):
+    y = z sigmoid(z), z[t] = bias + sum_j w[:, :, j] x[t - (W - 1) + j], the
+    inputs before a sequence's first token being s0 (zeros without it).  x
+    ``[B,T,H,D]`` float32 or bfloat16, w ``[H,D,W]`` and bias ``[H,D]`` float32,
+    s0 ``[N,W-1,H,D]`` in x's dtype, cu_seqlens as in ``ssm_fwd``.  Returns
+    ``(y, sT)``, sT the last W - 1 inputs: the s0 of a continuation, or the
+    state of ``conv_silu_step``."""
+    dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
+    y = torch.empty_like(x)
+    sT = torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev)
+    _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(s0),
+          _ptr(cu_seqlens), _ptr(y), _ptr(sT))
+    return y, sT
+
+
+def conv_silu_bwd(x, w, bias, s0, dy, dsT=None, cu_seqlens=None):
+    """Backward of ``conv_silu`` (``dn_conv_silu_bwd``) from dy and dsT in x's
+    dtype (dsT None: 0).  Returns a dict: dx and ds0 in x's dtype, dw and dbias
+    (None without a bias) in float32."""
+    dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
+    if dy is None:
+        raise TypeError("dy is required")
+    _need(dy, "dy", x.dtype, tuple(x.shape), dev)
+    _need(dsT, "dsT", x.dtype, (N, max(W - 1, 0), H, D), dev)
+    gr = dict(dx=torch.empty_like(x), dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
+              ds0=torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev))
+    wsb = load_library().dn_conv_silu_bwd_workspace(B, T, H, D, W)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_conv_silu_bwd", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(s0),
+          _ptr(cu_seqlens), _ptr(dy), _ptr(dsT), *[_ptr(g) for g in gr.values()], _ptr(ws), wsb)
+    return gr
+
+
+def conv_silu_step(x, w, bias, state):
+    """One token of every sequence (``dn_conv_silu_step``): x ``[B,H,D]``, state
+    ``[B,W-1,H,D]`` (x's dtype) holding the last W - 1 inputs, updated in
+    place.  Returns y ``[B,H,D]``."""
+    if state is None:
+        raise TypeError("state is required")
+    dev, (B,), H, D, W, _ = _conv_silu_args(x, w, bias, state, None, 3)
+    y = torch.empty_like(x)
+    _call("dn_conv_silu_step", dev, B, H, D, W, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y))
+    return y
+
+
+def _gated_norm_args(x, z, w):
+    """(device, rows, D, weight rows), checked."""
+    dev = _gpu(x, "x", tuple(range(1, 9)), tuple(_DTYPES))
+    D = x.shape[-1]
+    if not isinstance(w, torch.Tensor) or w.dim() not in (1, 2):
+        raise ValueError("w must be a [D] or [H, D] tensor")
+    if w.dim() == 2 and (x.dim() < 2 or w.shape[0] != x.shape[-2]):
+        raise ValueError("w has shape %s, expected one row for each of x's heads" % (tuple(w.shape),))
+    R = 1 if w.dim() == 1 else w.shape[0]
+    _need(x, "x", x.dtype, tuple(x.shape), dev)
+    _need(z, "z", x.dtype, tuple(x.shape), dev)
+    _need(w, "w", torch.float32, (D,) if w.dim() == 1 else (R, D), dev)
+    return dev, x.numel() // D if D else 0, D, R
+
+
+def gated_norm(x, z, w, eps: float = 1e-5, gate_first: bool = False):
+    """Gated root-mean-square norm over the last dimension (``dn_gated_norm``):
+    ``x / sqrt(mean(x^2) + eps) * w * silu(z)``, or with ``gate_first`` the norm
+    of ``x silu(z)`` times w.  x, z ``[..., D]`` or ``[..., H, D]`` float32 or
+    bfloat16; w float32 ``[D]``, or ``[H, D]`` for a weight per head.  Returns y
+    in x's dtype."""
+    dev, rows, D, R = _gated_norm_args(x, z, w)
+    y = torch.empty_like(x)
+    _call("dn_gated_norm", dev, rows, D, R, _DTYPES[x.dtype], _ptr(x), _ptr(z), _ptr(w), float(eps), int(gate_first),
+          _ptr(y))
+    return y
+
+
+def gated_norm_bwd(x, z, w, dy, eps: float = 1e-5, gate_first: bool = False):
+    """Backward of ``gated_norm`` (``dn_gated_norm_bwd``) from dy in x's dtype:
+    ``(dx, dz, dw)``, dx and dz in x's dtype, dw float32."""
+    dev, rows, D, R = _gated_norm_args(x, z, w)
+    _need(dy, "dy", x.dtype, tuple(x.shape), dev)
+    dx, dz, dw = torch.empty_like(x), torch.empty_like(z), torch.empty_like(w)
+    wsb = load_library().dn_gated_norm_bwd_workspace(rows, D, R)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_gated_norm_bwd", dev, rows, D, R, _DTYPES[x.dtype], _ptr(x), _ptr(z), _ptr(w), float(eps), int(gate_first),
+          _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws), wsb)
+    return dx, dz, dw
+
+
+class SsmScan(torch.autograd.Function):
+    """Autograd wrapper: forward by ``ssm_fwd``, backward by ``ssm_bwd``."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, dt, A, dt_bias, skip, h0, cu_seqlens):
+        o, hT = ssm_fwd(q, k, v, dt, A, dt_bias, skip, h0, cu_seqlens)
+        ctx.save_for_backward(q, k, v, dt, A, dt_bias, skip, h0, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return o, hT
+
+    @staticmethod
+    def backward(ctx, dO, dhT):
+        q, k, v, dt, A, dt_bias, skip, h0, cu = ctx.saved_tensors
+        dO = torch.zeros_like(v) if dO is None else dO.contiguous()
+        gr = ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, None if dhT is None else dhT.contiguous(), cu)
+        return (gr["dq"], gr["dk"], gr["dv"], gr["ddt"], gr["dA"], gr["ddt_bias"], gr["dskip"],
+                None if h0 is None else gr["dh0"], None)
+
+
+def ssm_scan(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None):
+    """Differentiable selective state space scan; returns (o, hT)."""
+    return SsmScan.apply(q, k, v, dt, A, dt_bias, skip, h0, cu_seqlens)
+
+
+class ConvSilu(torch.autograd.Function):
+    """Autograd wrapper: forward by ``conv_silu``, backward by ``conv_silu_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, s0, cu_seqlens):
+        y, sT = conv_silu(x, w, bias, s0, cu_seqlens)
+        ctx.save_for_backward(x, w, bias, s0, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return y, sT
+
+    @staticmethod
+    def backward(ctx, dy, dsT):
+        x, w, bias, s0, cu = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+        gr = conv_silu_bwd(x, w, bias, s0, dy, None if dsT is None else dsT.contiguous(), cu)
+        return gr["dx"], gr["dw"], gr["dbias"], None if s0 is None else gr["ds0"], None
+
+
+def conv_silu_fn(x, w, bias=None, s0=None, cu_seqlens=None):
+    """Differentiable ``conv_silu``; returns (y, sT)."""
+    return ConvSilu.apply(x, w, bias, s0, cu_seqlens)
+
+
+class GatedNorm(torch.autograd.Function):
+    """Autograd wrapper: forward by ``gated_norm``, backward by ``gated_norm_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, z, w, eps, gate_first):
+        ctx.save_for_backward(x, z, w)
+        ctx.eps, ctx.gate_first = eps, gate_first
+        return gated_norm(x, z, w, eps, gate_first)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, z, w = ctx.saved_tensors
+        return (*gated_norm_bwd(x, z, w, dy.contiguous(), ctx.eps, ctx.gate_first), None, None)
+
+
+def gated_norm_fn(x, z, w, eps: float = 1e-5, gate_first: bool = False):
+    """Differentiable ``gated_norm``."""
+    return GatedNorm.apply(x, z, w, eps, gate_first)

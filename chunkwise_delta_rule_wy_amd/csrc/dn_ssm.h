@@ -1,0 +1,272 @@
+// Shared parts of the selective state space scan's kernels (gfx950).
+//
+// Per sequence and head (q, k shared by the H / G heads of a group):
+//
+//   s_t = softplus(dt_t + dt_bias),  a_t = s_t A
+//   h_t = exp(a_t) h_{t-1} + s_t k_t v_t^T      (h = S^T, Dk x Dv)
+//   o_t = h_t^T q_t + skip v_t
+//
+// Over a chunk of 64 tokens, with b = cumsum a, gamma = exp b,
+// Gamma_rj = exp(b_r - b_j) for j <= r and w_j = exp(b_63 - b_j):
+//
+//   O  = ((Q K^T) * Gamma) diag(s) V + diag(gamma) Q h + skip V
+//   h+ = gamma_63 h + K^T diag(w s) V
+//
+// and going back, with dh+ the gradient of the chunk's end state,
+//
+//   dh = gamma_63 dh+ + Q^T diag(gamma) dO.
+//
+// Both are the same sweep S <- gamma_63 S + X^T diag(c) Y, over (k, v, w s)
+// forwards and (q, dO, gamma) backwards.  A sequence is cut into segments of
+// whole chunks, so that few long sequences still fill the device: one sweep
+// from a zero state leaves each segment's own end state, an elementwise pass
+// joins them to the segments' start states, and the segments then run side by
+// side.
+//
+// Precision.  k, v, q and dO are bf16 and enter the matrix products exactly.
+// Everything that feeds a state or an fp32 gradient is an fp32 value split
+// into three bf16 parts (split3: 24 bits), one product each, so that states,
+// ddt and the parameter gradients keep fp32 accuracy; what feeds only bf16
+// outputs is rounded to bf16 once.  Log decays are summed in double and used
+// as differences, so that neither long chunks nor strong decays lose the
+// ratio of two neighbours.
+#pragma once
+
+#include "dn_chunk.h"
+#include "dn_wy.h"
+
+namespace dn {
+
+constexpr int SSM_TILE = 64;  // Dv columns of a workgroup
+
+struct SsmParams {
+  const bf16 *q, *k, *v, *dO;
+  const float *dt, *A, *bias, *skip;  // bias, skip may be null
+  const float *h0, *dhT;              // may be null
+  const int32_t *cu;                  // packed sequences, or null
+  const int32_t *seg_base, *seg_seq;      // packed: segment table
+  const int32_t *chunk_base, *chunk_seq;  // packed: chunk table (backward)
+  bf16 *o;
+  float *hT;                 // may be null
+  float *seg_state[2];       // per segment and head: own end state, then start state (0 forwards, 1 backwards)
+  double *seg_decay;         // per segment and head: sum of the log2 decays
+  float *states, *dstates;   // backward: state entering each chunk, gradient of the state leaving it
+  bf16 *dq, *dk, *dv;
+  float *dq_part, *dk_part;  // fp32 partial sums over sets of heads, or null
+  float *ddt, *dA, *ddt_bias, *dskip, *dh0;  // ddt_bias, dskip, dh0 may be null
+  float *par_part;           // [chunk][H][3]: dA, ddt_bias, dskip
+  int64_t rows;              // B T
+  int T, H, G, DV, N;
+  int ntiles;                // Dv / 64
+  int split;                 // segments are joined through seg_state
+  int NS, segc;              // segments of a sequence (not packed), chunks of a segment
+  int NC;                    // chunks of a sequence (not packed)
+  int nseg, nchunks;         // upper bounds over all sequences
+  int sets, set_heads;       // backward: sets of heads of a group, heads of a set
+};
+
+hipError_t launch_ssm_sweep(const SsmParams &p, int DK, bool store, bool backward, hipStream_t stream);
+hipError_t launch_ssm_join(const SsmParams &p, int DK, bool backward, hipStream_t stream);
+hipError_t launch_ssm_fwd(const SsmParams &p, int DK, hipStream_t stream);
+hipError_t launch_ssm_grad(const SsmParams &p, int DK, hipStream_t stream);
+
+struct SsmStepParams {
+  const void *q, *k, *v;
+  const float *dt, *A, *bias, *skip;
+  float *state;
+  void *o;
+  int B, H, G, DV;
+};
+hipError_t launch_ssm_step(const SsmStepParams &p, int dtype, int DK, hipStream_t stream);
+
+// Workgroups are dealt to the 8 XCDs round robin; this gives each XCD (one L2)
+// a contiguous range of the work items, so that the heads that share a
+// segment's keys and queries meet in one L2.
+__device__ __forceinline__ int xcd_item(int x, int total) {
+  const int q = total >> 3, r = total & 7, xcd = x & 7;
+  return xcd * q + min(xcd, r) + (x >> 3);
+}
+
+// A segment: sequence n, first token row, tokens, place in the sequence.
+struct Segment {
+  int n, len, chunk;  // chunk: its first chunk within the sequence
+  size_t row;
+  bool first, last;
+};
+__device__ __forceinline__ bool segment(const SsmParams &p, int seg, Segment &s) {
+  int start, len;
+  if (p.cu) {
+    s.n = p.seg_seq[seg];
+    if (s.n < 0) return false;
+    const int i = seg - p.seg_base[s.n], t0 = p.cu[s.n];
+    len = p.cu[s.n + 1] - t0;
+    s.chunk = i * p.segc;
+    start = s.chunk * CH;
+    s.row = (size_t)t0 + start;
+  } else {
+    s.n = seg / p.NS;
+    len = p.T;
+    s.chunk = (seg - s.n * p.NS) * p.segc;
+    start = s.chunk * CH;
+    s.row = (size_t)s.n * p.T + start;
+  }
+  s.first = start == 0;
+  s.last = len - start <= p.segc * CH;
+  s.len = s.last ? len - start : p.segc * CH;
+  return true;
+}
+__device__ __forceinline__ int chunk_id(const SsmParams &p, const Segment &s, int c) {
+  return (p.cu ? p.chunk_base[s.n] : s.n * p.NC) + s.chunk + c;
+}
+
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
+
+// the raw step size of one (token, head): dt + dt_bias
+__device__ __forceinline__ float raw_step(const SsmParams &p, size_t row, int h) {
+  return p.dt[row * p.H + h] + (p.bias ? p.bias[h] : 0.f);
+}
+
+// inclusive prefix sum over the 64 lanes of a wave, in double
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp0d(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_incl_scan_d(double x) {
+  x += dpp0d<0x111>(x);
+  x += dpp0d<0x112>(x);
+  x += dpp0d<0x114>(x);
+  x += dpp0d<0x118>(x);
+  x += dpp0d<0x142, 0xa>(x);
+  x += dpp0d<0x143, 0xc>(x);
+  return x;
+}
+// sum over the 16 lanes of each row
+__device__ __forceinline__ double row_sum16_d(double x) {
+  x += dpp0d<0xB1>(x);
+  x += dpp0d<0x4E>(x);
+  x += dpp0d<0x124>(x);
+  x += dpp0d<0x128>(x);
+  return x;
+}
+__device__ __forceinline__ double lane_val_d(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Gate table of one (chunk, head): s, the log2 decays b = bh + bl (two floats
+// hold them to 2^-48), gamma, w, w s; `last` = gamma_63.
+struct GateTab {
+  float s[CH], bh[CH], bl[CH], gam[CH], w[CH], ws[CH];
+  float last, pad[3];
+};
+// One wave fills the table from the raw step sizes of its lanes' tokens (lanes
+// from L on are padding: no decay, no input).  Returns the chunk's log2 decay.
+__device__ __forceinline__ double fill_gates(GateTab &t, float raw, float A, int L) {
+  const int l = lane_id();
+  const float s = l < L ? softplus(raw) : 0.f;
+  const double b = wave_incl_scan_d((double)s * ((double)A * 1.4426950408889634074));
+  const double total = lane_val_d(b, 63);
+  const float bh = (float)b, bl = (float)(b - (double)bh);
+  const float w = wy::fexp2((float)(total - b));
+  t.s[l] = s;
+  t.bh[l] = bh;
+  t.bl[l] = bl;
+  t.gam[l] = wy::fexp2(bh) * (1.f + 0.6931471806f * bl);
+  t.w[l] = w;
+  t.ws[l] = w * s;
+  if (l == 0) {
+    const float th = (float)total;
+    t.last = wy::fexp2(th) * (1.f + 0.6931471806f * (float)(total - (double)th));
+  }
+  return total;
+}
+// Gamma_rj from the table's entries of r and j
+__device__ __forceinline__ float decay_ratio(float bhr, float blr, float bhj, float blj) {
+  return wy::fexp2((bhr - bhj) + (blr - blj));
+}
+
+// x = p0 + p1 + p2 to 24 bits, each part a bf16 operand fragment
+struct Split {
+  bf16x8 p[3];
+};
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ Split split3(const float (&x)[8]) {
+  Split r;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = x[i];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    u32x4 u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = pk_bf16(v[2 * i], v[2 * i + 1]);
+      if (k < 2) {
+        v[2 * i] -= bf_lo(u[i]);
+        v[2 * i + 1] -= bf_hi(u[i]);
+      }
+    }
+    r.p[k] = __builtin_bit_cast(bf16x8, u);
+  }
+  return r;
+}
+// the eight elements of a bf16 fragment as floats
+__device__ __forceinline__ void unpack8(const bf16x8 &f, float (&x)[8]) {
+  const u32x4 u = __builtin_bit_cast(u32x4, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf_lo(u[i]);
+    x[2 * i + 1] = bf_hi(u[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
+// 32-index operand fragment whose rows are the matrix's columns: 16 columns
+// c0 .. of an LDS matrix with `stride` bytes per row, contraction index = its
+// rows r0 + 8 g .. r0 + 8 g + 7 (lane group g)
+__device__ __forceinline__ bf16x8 frag_tr(uint32_t base, int stride, int r0, int c0) {
+  const int l = lane_id(), g = l >> 4, e = (l >> 2) & 3, q = l & 3;
+  const uint32_t a = base + (r0 + 8 * g + e) * stride + 2 * (c0 + 4 * q);
+  return wy::cat(wy::ld_tr(a), wy::ld_tr(a + 4 * stride));
+}
+
+// A rows x COLS bf16 tile staged through registers: each of the workgroup's
+// THR threads holds its share as 16-byte units, zero from row L on.
+template <int ROWS, int COLS, int THR>
+struct Stage {
+  static constexpr int UPR = COLS / 8, NU = ROWS * UPR / THR;
+  static_assert(ROWS * UPR % THR == 0, "whole units per thread");
+  u128 u[NU];
+  // rows of `pitch` elements; src points at the tile's first element
+  __device__ __forceinline__ void load(const bf16 *src, size_t pitch, int L) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int x = threadIdx.x + THR * i, r = x / UPR, c = x % UPR;
+      u[i] = r < L ? ldg128(src + r * pitch + 8 * c) : zero128();
+    }
+  }
+  template <int STRIDE>
+  __device__ __forceinline__ void store(bf16 *lds) const {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int x = threadIdx.x + THR * i, r = x / UPR, c = x % UPR;
+      *reinterpret_cast<u128 *>(lds + r * STRIDE + 8 * c) = u[i];
+    }
+  }
+};
+
+// row-major fragment: 8 elements of row r from column c on
+__device__ __forceinline__ bf16x8 frag_row(const bf16 *lds, int stride, int r, int c) {
+  return *reinterpret_cast<const bf16x8 *>(lds + r * stride + c);
+}
+
+}  // namespace dn

@@ -407,6 +407,137 @@ dn_status dn_short_conv_l2_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32
                                int32_t dtype, const void *x, const float *w, const int32_t *cu_seqlens,
                                const float *dy, float *dx, float *dw, hipStream_t stream);
 
+/*
+ * Selective state space scan (the gated linear recurrence of the Gated
+ * DeltaNet review thread, Table 1, row "Mamba2", S_t = alpha_t S_{t-1} +
+ * v_t k_t^T, with the step size that chooses alpha_t and the input's scale):
+ * per sequence and head,
+ *
+ *     s_t = softplus(dt_t + dt_bias)
+ *     S_t = exp(s_t A) S_{t-1} + s_t v_t k_t^T
+ *     o_t = S_t q_t + skip v_t
+ *
+ * - q, k [B,T,G,Dk], v, o [B,T,H,Dv] bf16; dt [B,T,H] fp32 (before bias and
+ *   softplus); A, dt_bias, skip [H] fp32 (dt_bias, skip NULL: zero); h0, hT
+ *   [N,H,Dk,Dv] fp32, holding h = S^T (h0 NULL: zero; hT NULL: not written).
+ *   G divides H: head h reads the queries and keys of group h / (H / G).
+ *   A <= 0 is the use; a positive A grows and overflows as the formula does.
+ * - Packed sequences by cu_seqlens as dn_chunk_fwd (cu[n_seqs] = T).  A
+ *   sequence without tokens passes h0 through to hT.
+ * - States, step sizes and decays are fp32 or wider throughout, and hT, ddt
+ *   and the parameter gradients have fp32 accuracy; o and the gradients of
+ *   q, k and v are rounded to bf16 once at the end and in at most one product
+ *   operand before it.
+ * - Inputs have to be finite: within a chunk of 64 tokens a value that is not
+ *   reaches the chunk's other outputs, earlier ones included.  It does not
+ *   cross sequences.
+ * - Supported: Dk in {64, 128}; Dv a positive multiple of 64 up to 1024;
+ *   DN_BF16 (dn_ssm_step also DN_F32); pointers of q, k, v, o, states and
+ *   their gradients 16-byte aligned.  Otherwise DN_EUNSUPPORTED or DN_EINVAL.
+ */
+typedef struct {
+    int32_t B, T, H, G, Dk, Dv;
+    int32_t n_seqs;  /* B, or the number of packed sequences */
+    int32_t dtype;   /* dn_dtype of q, k, v, o and their gradients */
+} dn_ssm_shape;
+
+/* Bytes of device workspace (16-byte aligned) of the two passes; they cover
+ * packed input where B == 1. */
+size_t dn_ssm_fwd_workspace(const dn_ssm_shape *s);
+size_t dn_ssm_bwd_workspace(const dn_ssm_shape *s);
+
+dn_status dn_ssm_fwd(const dn_ssm_shape *s, const void *q, const void *k, const void *v,
+                     const float *dt, const float *A, const float *dt_bias, const float *skip,
+                     const float *h0, const int32_t *cu_seqlens, void *o, float *hT,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Backward pass of L = <dO, o> + <dhT, hT> (dO [B,T,H,Dv] bf16, dhT NULL: 0).
+ * Writes dq, dk [B,T,G,Dk] (summed over the heads of a group) and dv in bf16,
+ * ddt [B,T,H], dA, ddt_bias, dskip [H] and dh0 [N,H,Dk,Dv] in fp32; ddt_bias,
+ * dskip and dh0 may be NULL (not written).  The states are recomputed; nothing
+ * is kept from the forward call.  No atomics: results repeat bit for bit.
+ */
+dn_status dn_ssm_bwd(const dn_ssm_shape *s, const void *q, const void *k, const void *v,
+                     const float *dt, const float *A, const float *dt_bias, const float *skip,
+                     const float *h0, const int32_t *cu_seqlens, const void *dO, const float *dhT,
+                     void *dq, void *dk, void *dv, float *ddt, float *dA, float *ddt_bias,
+                     float *dskip, float *dh0,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of B sequences: q, k [B,G,Dk], v, o [B,H,Dv] (dtype), dt [B,H];
+ * state [B,H,Dk,Dv] fp32 holding S^T, read and overwritten.
+ */
+dn_status dn_ssm_step(int32_t B, int32_t H, int32_t G, int32_t Dk, int32_t Dv, int32_t dtype,
+                      const void *q, const void *k, const void *v, const float *dt, const float *A,
+                      const float *dt_bias, const float *skip, float *state, void *o, hipStream_t stream);
+
+/*
+ * Short convolution with bias, SiLU and a carried state: dn_short_conv's
+ * filter with z = bias + conv(x), y = z sigmoid(z), where the W - 1 inputs
+ * before a sequence's first token are s0 instead of zeros.
+ *
+ * x, y [B,T,H,D] and s0, sT [N,W-1,H,D] in the dtype (16-byte aligned), w
+ * [H,D,W] and bias [H,D] fp32; bias and s0 NULL: zero.  sT receives each
+ * sequence's last W - 1 inputs, those of s0 included where the sequence is
+ * shorter, bit for bit (NULL: not written; it may not alias s0).  Packed
+ * sequences by cu_seqlens with B == 1, as dn_short_conv.  D a multiple of 8, W
+ * in 1..4 (DN_EUNSUPPORTED otherwise).
+ */
+dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n_seqs,
+                       int32_t dtype, const void *x, const float *w, const float *bias, const void *s0,
+                       const int32_t *cu_seqlens, void *y, void *sT, hipStream_t stream);
+
+/* Bytes of device workspace of dn_conv_silu_bwd. */
+size_t dn_conv_silu_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W);
+
+/*
+ * Backward of dn_conv_silu from dy [B,T,H,D] and dsT [N,W-1,H,D] (dtype, dsT
+ * NULL: 0): dx [B,T,H,D] and ds0 [N,W-1,H,D] in the dtype, dw [H,D,W] and dbias
+ * [H,D] fp32; dbias and ds0 may be NULL (not written).  z is recomputed from
+ * x.  No atomics: results repeat bit for bit.
+ */
+dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n_seqs,
+                           int32_t dtype, const void *x, const float *w, const float *bias, const void *s0,
+                           const int32_t *cu_seqlens, const void *dy, const void *dsT,
+                           void *dx, float *dw, float *dbias, void *ds0,
+                           void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of B sequences: x, y [B,H,D]; state [B,W-1,H,D] holds the last
+ * W - 1 inputs, is read, and takes x in place of its oldest row.
+ */
+dn_status dn_conv_silu_step(int32_t B, int32_t H, int32_t D, int32_t W, int32_t dtype, const void *x,
+                            const float *w, const float *bias, void *state, void *y, hipStream_t stream);
+
+/*
+ * Gated root-mean-square norm of `rows` rows of D values, the norm behind a
+ * (Gated) DeltaNet or state space mixer: with g = z sigmoid(z) and row i
+ * using weight row i % R (w [R,D] fp32; R = 1 shares one, R = H gives every
+ * head its own; R divides rows),
+ *
+ *     gate_first == 0:  y = x / sqrt(mean(x^2) + eps) * w * g
+ *     gate_first != 0:  y = u / sqrt(mean(u^2) + eps) * w,  u = x g
+ *
+ * x, z, y [rows, D] in the dtype (16-byte aligned); y may alias x or z.  D a
+ * multiple of 8 up to 8192 (DN_EUNSUPPORTED otherwise).
+ */
+dn_status dn_gated_norm(int64_t rows, int32_t D, int32_t R, int32_t dtype, const void *x, const void *z,
+                        const float *w, float eps, int32_t gate_first, void *y, hipStream_t stream);
+
+/* Bytes of device workspace of dn_gated_norm_bwd. */
+size_t dn_gated_norm_bwd_workspace(int64_t rows, int32_t D, int32_t R);
+
+/*
+ * Backward of dn_gated_norm from dy [rows, D] (dtype): dx, dz in the dtype, dw
+ * [R,D] fp32.  No atomics: results repeat bit for bit.
+ */
+dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32_t dtype, const void *x, const void *z,
+                            const float *w, float eps, int32_t gate_first, const void *dy,
+                            void *dx, void *dz, float *dw,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
