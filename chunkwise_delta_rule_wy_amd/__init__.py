@@ -598,16 +598,33 @@ def short_conv_fn(x, w, cu_seqlens=None, l2norm=False):
 # ------------------------------------------------- the state space mixer
 
 
+# Single tokens are bound by what the host does before the launch: the calls
+# below pass raw addresses, test a tensor in one expression (the slow path
+# words the error) and ask for the device and its stream without their objects.
+
+def _adr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _call(name, dev, *args):
     """Call a library function on ``dev``'s current stream, with ``dev`` as
     the current device (kernels start on the current device)."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, _stream(dev))
+    fn = getattr(_lib or load_library(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
-    _check(name, status)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status:
+        _check(name, status)
+
+
+def _is(t, name, dtype, shape, dev):
+    """``_need`` with a quick way through for a tensor that is right."""
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+                     and t.is_contiguous()):
+        return
+    _need(t, name, dtype, shape, dev)
 
 
 def _gpu(t, name, dims, dtypes):
@@ -628,7 +645,7 @@ def _seqs(B, cu_seqlens, dev):
         raise ValueError("cu_seqlens must be a 1-d tensor of at least two offsets")
     if B != 1:
         raise ValueError("packed sequences need a batch of one")
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+    _is(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
     return cu_seqlens.numel() - 1
 
 
@@ -639,15 +656,15 @@ def _ssm_args(q, k, v, dt, A, dt_bias, skip, dtypes, dims):
     lead, H, Dv, G, Dk = tuple(v.shape[:-2]), v.shape[-2], v.shape[-1], q.shape[-2], q.shape[-1]
     if G == 0 or H % G:
         raise ValueError("q has %d heads, which do not divide v's %d" % (G, H))
-    _need(q, "q", v.dtype, lead + (G, Dk), dev)
-    _need(k, "k", v.dtype, lead + (G, Dk), dev)
-    _need(v, "v", v.dtype, lead + (H, Dv), dev)
+    _is(q, "q", v.dtype, lead + (G, Dk), dev)
+    _is(k, "k", v.dtype, lead + (G, Dk), dev)
+    _is(v, "v", v.dtype, lead + (H, Dv), dev)
     for t, name, shape in ((dt, "dt", lead + (H,)), (A, "A", (H,))):
         if t is None:
             raise TypeError("%s is required" % name)
-        _need(t, name, torch.float32, shape, dev)
-    _need(dt_bias, "dt_bias", torch.float32, (H,), dev)
-    _need(skip, "skip", torch.float32, (H,), dev)
+        _is(t, name, torch.float32, shape, dev)
+    _is(dt_bias, "dt_bias", torch.float32, (H,), dev)
+    _is(skip, "skip", torch.float32, (H,), dev)
     return dev, lead, H, G, Dk, Dv
 
 
@@ -665,14 +682,14 @@ def ssm_fwd(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None, o
     lib = load_library()
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
-    _need(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
+    _is(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
     s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
     o = torch.empty_like(v)
     hT = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev) if output_final_state else None
     wsb = lib.dn_ssm_fwd_workspace(s)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_ssm_fwd", dev, s, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(dt_bias), _ptr(skip), _ptr(h0),
-          _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(ws), wsb)
+    _call("dn_ssm_fwd", dev, s, _adr(q), _adr(k), _adr(v), _adr(dt), _adr(A), _adr(dt_bias), _adr(skip), _adr(h0),
+          _adr(cu_seqlens), _adr(o), _adr(hT), _adr(ws), wsb)
     return o, hT
 
 
@@ -683,11 +700,11 @@ def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
     lib = load_library()
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
-    _need(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
+    _is(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
     if dO is None:
         raise TypeError("dO is required")
-    _need(dO, "dO", v.dtype, tuple(v.shape), dev)
-    _need(dhT, "dhT", torch.float32, (N, H, Dk, Dv), dev)
+    _is(dO, "dO", v.dtype, tuple(v.shape), dev)
+    _is(dhT, "dhT", torch.float32, (N, H, Dk, Dv), dev)
     s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
     gr = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), ddt=torch.empty_like(dt),
               dA=torch.empty_like(A), ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias),
@@ -695,8 +712,8 @@ def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
               dh0=torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev))
     wsb = lib.dn_ssm_bwd_workspace(s)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_ssm_bwd", dev, s, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(dt_bias), _ptr(skip), _ptr(h0),
-          _ptr(cu_seqlens), _ptr(dO), _ptr(dhT), *[_ptr(g) for g in gr.values()], _ptr(ws), wsb)
+    _call("dn_ssm_bwd", dev, s, _adr(q), _adr(k), _adr(v), _adr(dt), _adr(A), _adr(dt_bias), _adr(skip), _adr(h0),
+          _adr(cu_seqlens), _adr(dO), _adr(dhT), *[_adr(g) for g in gr.values()], _adr(ws), wsb)
     return gr
 
 
@@ -707,10 +724,10 @@ def ssm_step(q, k, v, dt, A, dt_bias, skip, state):
     dev, (B,), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, tuple(_DTYPES), 3)
     if state is None:
         raise TypeError("state is required")
-    _need(state, "state", torch.float32, (B, H, Dk, Dv), dev)
+    _is(state, "state", torch.float32, (B, H, Dk, Dv), dev)
     o = torch.empty_like(v)
-    _call("dn_ssm_step", dev, B, H, G, Dk, Dv, _DTYPES[v.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A),
-          _ptr(dt_bias), _ptr(skip), _ptr(state), _ptr(o))
+    _call("dn_ssm_step", dev, B, H, G, Dk, Dv, _DTYPES[v.dtype], _adr(q), _adr(k), _adr(v), _adr(dt), _adr(A),
+          _adr(dt_bias), _adr(skip), _adr(state), _adr(o))
     return o
 
 
@@ -722,10 +739,10 @@ def _conv_silu_args(x, w, bias, state, cu_seqlens, dims):
         raise ValueError("w must be a [H, D, W] tensor")
     W = w.shape[2]
     N = _seqs(lead[0], cu_seqlens, dev)
-    _need(x, "x", x.dtype, tuple(x.shape), dev)
-    _need(w, "w", torch.float32, (H, D, W), dev)
-    _need(bias, "bias", torch.float32, (H, D), dev)
-    _need(state, "state", x.dtype, (N, max(W - 1, 0), H, D), dev)
+    _is(x, "x", x.dtype, tuple(x.shape), dev)
+    _is(w, "w", torch.float32, (H, D, W), dev)
+    _is(bias, "bias", torch.float32, (H, D), dev)
+    _is(state, "state", x.dtype, (N, max(W - 1, 0), H, D), dev)
     return dev, lead, H, D, W, N
 
 
@@ -740,8 +757,8 @@ def conv_silu(x, w, bias=None, s0=None, cu_seqlens=None):
     dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
     y = torch.empty_like(x)
     sT = torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev)
-    _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(s0),
-          _ptr(cu_seqlens), _ptr(y), _ptr(sT))
+    _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(s0),
+          _adr(cu_seqlens), _adr(y), _adr(sT))
     return y, sT
 
 
@@ -752,14 +769,14 @@ def conv_silu_bwd(x, w, bias, s0, dy, dsT=None, cu_seqlens=None):
     dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
     if dy is None:
         raise TypeError("dy is required")
-    _need(dy, "dy", x.dtype, tuple(x.shape), dev)
-    _need(dsT, "dsT", x.dtype, (N, max(W - 1, 0), H, D), dev)
+    _is(dy, "dy", x.dtype, tuple(x.shape), dev)
+    _is(dsT, "dsT", x.dtype, (N, max(W - 1, 0), H, D), dev)
     gr = dict(dx=torch.empty_like(x), dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
               ds0=torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev))
     wsb = load_library().dn_conv_silu_bwd_workspace(B, T, H, D, W)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_conv_silu_bwd", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(s0),
-          _ptr(cu_seqlens), _ptr(dy), _ptr(dsT), *[_ptr(g) for g in gr.values()], _ptr(ws), wsb)
+    _call("dn_conv_silu_bwd", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(s0),
+          _adr(cu_seqlens), _adr(dy), _adr(dsT), *[_adr(g) for g in gr.values()], _adr(ws), wsb)
     return gr
 
 
@@ -771,7 +788,7 @@ def conv_silu_step(x, w, bias, state):
         raise TypeError("state is required")
     dev, (B,), H, D, W, _ = _conv_silu_args(x, w, bias, state, None, 3)
     y = torch.empty_like(x)
-    _call("dn_conv_silu_step", dev, B, H, D, W, _DTYPES[x.dtype], _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y))
+    _call("dn_conv_silu_step", dev, B, H, D, W, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(state), _adr(y))
     return y
 
 
@@ -784,9 +801,9 @@ def _gated_norm_args(x, z, w):
     if w.dim() == 2 and (x.dim() < 2 or w.shape[0] != x.shape[-2]):
         raise ValueError("w has shape %s, expected one row for each of x's heads" % (tuple(w.shape),))
     R = 1 if w.dim() == 1 else w.shape[0]
-    _need(x, "x", x.dtype, tuple(x.shape), dev)
-    _need(z, "z", x.dtype, tuple(x.shape), dev)
-    _need(w, "w", torch.float32, (D,) if w.dim() == 1 else (R, D), dev)
+    _is(x, "x", x.dtype, tuple(x.shape), dev)
+    _is(z, "z", x.dtype, tuple(x.shape), dev)
+    _is(w, "w", torch.float32, (D,) if w.dim() == 1 else (R, D), dev)
     return dev, x.numel() // D if D else 0, D, R
 
 
@@ -798,8 +815,8 @@ def gated_norm(x, z, w, eps: float = 1e-5, gate_first: bool = False):
     in x's dtype."""
     dev, rows, D, R = _gated_norm_args(x, z, w)
     y = torch.empty_like(x)
-    _call("dn_gated_norm", dev, rows, D, R, _DTYPES[x.dtype], _ptr(x), _ptr(z), _ptr(w), float(eps), int(gate_first),
-          _ptr(y))
+    _call("dn_gated_norm", dev, rows, D, R, _DTYPES[x.dtype], _adr(x), _adr(z), _adr(w), float(eps), int(gate_first),
+          _adr(y))
     return y
 
 
@@ -807,12 +824,12 @@ def gated_norm_bwd(x, z, w, dy, eps: float = 1e-5, gate_first: bool = False):
     """Backward of ``gated_norm`` (``dn_gated_norm_bwd``) from dy in x's dtype:
     ``(dx, dz, dw)``, dx and dz in x's dtype, dw float32."""
     dev, rows, D, R = _gated_norm_args(x, z, w)
-    _need(dy, "dy", x.dtype, tuple(x.shape), dev)
+    _is(dy, "dy", x.dtype, tuple(x.shape), dev)
     dx, dz, dw = torch.empty_like(x), torch.empty_like(z), torch.empty_like(w)
     wsb = load_library().dn_gated_norm_bwd_workspace(rows, D, R)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_gated_norm_bwd", dev, rows, D, R, _DTYPES[x.dtype], _ptr(x), _ptr(z), _ptr(w), float(eps), int(gate_first),
-          _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws), wsb)
+    _call("dn_gated_norm_bwd", dev, rows, D, R, _DTYPES[x.dtype], _adr(x), _adr(z), _adr(w), float(eps), int(gate_first),
+          _adr(dy), _adr(dx), _adr(dz), _adr(dw), _adr(ws), wsb)
     return dx, dz, dw
 
 

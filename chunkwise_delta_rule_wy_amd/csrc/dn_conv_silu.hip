@@ -10,11 +10,14 @@
 //           the first token, which are ds0
 //   dw[j] = sum_t dz[t] x[t - (W - 1) + j],  dbias = sum_t dz[t]
 //
-// A thread owns eight consecutive channels (16 bytes of bf16) of a run of
-// consecutive tokens and slides the W-token window through registers; a run
-// reads the W - 1 rows beside it again.  Everything else is streamed once:
+// A thread owns four consecutive channels (8 bytes of bf16, 16 of fp32) of a
+// run of consecutive tokens and slides the W-token window through registers; a
+// run reads the W - 1 rows beside it again.  Everything else is streamed once:
 // HBM bounds all three kernels, and rows are loaded a batch ahead of their
-// use.  In the backward pass a thread recomputes z from x.  The weights'
+// use.  Eight channels and batches of eight rows need twice the registers, and
+// the waves that this costs hide less: measured at 4 x 4096 tokens of 4096
+// channels, W = 4, bf16, 53 us forwards (5.1 TB/s, the rate of a large copy)
+// and 102 us backwards against 55 and 150.  In the backward pass a thread recomputes z from x.  The weights'
 // gradients are summed in registers over a run, in LDS over a workgroup's runs
 // and by a second kernel over the workgroups, in a fixed order, so that they
 // repeat bit for bit.
@@ -25,8 +28,8 @@ namespace dn {
 namespace {
 
 constexpr int CS_THREADS = 256;
-constexpr int CS_CH = 8;         // channels of a thread
-constexpr int CS_BATCH = 8;      // rows loaded ahead (forward)
+constexpr int CS_CH = 4;         // channels of a thread
+constexpr int CS_BATCH = 4;      // rows loaded ahead (forward)
 constexpr int CS_BWD_BATCH = 4;  // the same, x and dy
 constexpr int CS_MAX_ROWS = 256; // rows of partial weight gradients
 
@@ -41,47 +44,41 @@ struct ConvSiluParams {
   int runs, rows;
 };
 
+// a row's CS_CH channels as they are in memory
+template <typename E>
+struct Raw {
+  typedef E V __attribute__((ext_vector_type(CS_CH)));
+  V v;
+  __device__ __forceinline__ void load(const E *src, bool valid) {
+    if (valid) v = *reinterpret_cast<const V *>(src);
+    else
+#pragma unroll
+      for (int e = 0; e < CS_CH; ++e) v[e] = to_e<E>(0.f);
+  }
+  __device__ __forceinline__ void get(float (&x)[CS_CH]) const {
+#pragma unroll
+    for (int e = 0; e < CS_CH; ++e) x[e] = to_f<E>(v[e]);
+  }
+};
+
 template <typename E>
 __device__ __forceinline__ void load8(const E *src, float (&x)[CS_CH]) {
-#pragma unroll
-  for (int h = 0; h < CS_CH; h += Vec16<E>::N) {
-    const typename Vec16<E>::type v = *reinterpret_cast<const typename Vec16<E>::type *>(src + h);
-#pragma unroll
-    for (int e = 0; e < Vec16<E>::N; ++e) x[h + e] = to_f<E>(v[e]);
-  }
+  Raw<E> r;
+  r.load(src, true);
+  r.get(x);
 }
 template <typename E>
 __device__ __forceinline__ void store8(E *dst, const float (&x)[CS_CH]) {
+  typedef E V __attribute__((ext_vector_type(CS_CH)));
+  V v;
 #pragma unroll
-  for (int h = 0; h < CS_CH; h += Vec16<E>::N) {
-    typename Vec16<E>::type v;
-#pragma unroll
-    for (int e = 0; e < Vec16<E>::N; ++e) v[e] = to_e<E>(x[h + e]);
-    *reinterpret_cast<typename Vec16<E>::type *>(dst + h) = v;
-  }
+  for (int e = 0; e < CS_CH; ++e) v[e] = to_e<E>(x[e]);
+  *reinterpret_cast<V *>(dst) = v;
 }
 __device__ __forceinline__ void zero8(float (&x)[CS_CH]) {
 #pragma unroll
   for (int e = 0; e < CS_CH; ++e) x[e] = 0.f;
 }
-// rows of eight channels as they are in memory
-template <typename E>
-struct Raw8 {
-  u128 u[CS_CH * sizeof(E) / 16];
-  __device__ __forceinline__ void load(const E *src, bool valid) {
-#pragma unroll
-    for (int i = 0; i < (int)(CS_CH * sizeof(E) / 16); ++i) u[i] = valid ? ldg128(src + i * (16 / sizeof(E))) : zero128();
-  }
-  __device__ __forceinline__ void get(float (&x)[CS_CH]) const {
-    struct alignas(16) V {
-      E e[CS_CH];
-    };
-    const V v = __builtin_bit_cast(V, *this);
-#pragma unroll
-    for (int e = 0; e < CS_CH; ++e) x[e] = to_f<E>(v.e[e]);
-  }
-};
-
 // the sequence [st, nx) around token t, number n
 struct Seq {
   int n;
@@ -105,14 +102,18 @@ struct Seq {
   }
 };
 
-template <typename E, int W>
-__device__ __forceinline__ void load_weights(const ConvSiluParams &p, int c0, float (&w)[W][CS_CH], float (&b)[CS_CH]) {
+// the thread's W x CS_CH weights lie together; w and bias are 16-byte aligned
+template <int W>
+__device__ __forceinline__ void load_weights(const float *wt, const float *bias, int c0, float (&w)[W][CS_CH],
+                                             float (&b)[CS_CH]) {
+  float f[W * CS_CH];
+  load_f32<W * CS_CH>(wt + (size_t)c0 * W, f);
 #pragma unroll
-  for (int e = 0; e < CS_CH; ++e) {
+  for (int e = 0; e < CS_CH; ++e)
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = p.w[(size_t)(c0 + e) * W + j];
-    b[e] = p.bias ? p.bias[c0 + e] : 0.f;
-  }
+    for (int j = 0; j < W; ++j) w[j][e] = f[e * W + j];
+  if (bias) load_f32<CS_CH>(bias + c0, b);
+  else zero8(b);
 }
 
 // the W - 1 inputs before token t of sequence s
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
   const E *x = static_cast<const E *>(p.x);
   E *y = static_cast<E *>(p.y), *sT = static_cast<E *>(p.sT);
   float w[W][CS_CH], bias[CS_CH], h[W > 1 ? W - 1 : 1][CS_CH];
-  load_weights<E, W>(p, c0, w, bias);
+  load_weights<W>(p.w, p.bias, c0, w, bias);
   int64_t t = (int64_t)run * p.run;
   const int64_t t1 = min(t + p.run, p.TT);
   while (t < t1) {
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
     const int64_t end = min(t1, s.nx);
     load_history<E, W>(p, s, t, c0, h);
     for (; t < end; t += CS_BATCH) {
-      Raw8<E> xb[CS_BATCH];
+      Raw<E> xb[CS_BATCH];
 #pragma unroll
       for (int i = 0; i < CS_BATCH; ++i) xb[i].load(x + (t + i) * p.C + c0, t + i < end);
 #pragma unroll
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
   }
 }
 
-// UL units (of eight channels) by CS_THREADS / UL runs per workgroup.  A
+// UL units (of CS_CH channels) by CS_THREADS / UL runs per workgroup.  A
 // thread walks each sequence's part [a, b) of its run: step u computes dz[u]
 // (zero behind the sequence) and emits the input at place u - (W - 1), which
 // all dz up to u complete; a part that starts its sequence also emits the
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_bwd_kernel(ConvSiluParam
     const E *x = static_cast<const E *>(p.x), *dy = static_cast<const E *>(p.dy), *dsT = static_cast<const E *>(p.dsT);
     E *dx = static_cast<E *>(p.dx), *ds0 = static_cast<E *>(p.ds0);
     float w[W][CS_CH], bias[CS_CH], h[W > 1 ? W - 1 : 1][CS_CH], dz[W][CS_CH];
-    load_weights<E, W>(p, c0, w, bias);
+    load_weights<W>(p.w, p.bias, c0, w, bias);
     int64_t a = ((int64_t)blockIdx.y * RUNS + rl) * p.run;
     const int64_t t1 = min(a + p.run, p.TT);
     while (a < t1) {
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_bwd_kernel(ConvSiluParam
 #pragma unroll
       for (int k = 0; k < W; ++k) zero8(dz[k]);
       for (int64_t u0 = a; u0 < b + (W - 1); u0 += CS_BWD_BATCH) {
-        Raw8<E> xb[CS_BWD_BATCH], yb[CS_BWD_BATCH];
+        Raw<E> xb[CS_BWD_BATCH], yb[CS_BWD_BATCH];
 #pragma unroll
         for (int i = 0; i < CS_BWD_BATCH; ++i) {
           const int64_t u = u0 + i;
@@ -322,19 +323,14 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_bwd_kernel(ConvSiluParam
   }
 }
 
-// dw and dbias from the rows of partial sums: 64 entries by four row groups
+// dw and dbias from the rows of partial sums
 __global__ __launch_bounds__(CS_THREADS) void conv_silu_sum_kernel(ConvSiluParams p) {
-  __shared__ float s[4][64];
-  const int n = p.C * (p.W + 1), e = threadIdx.x & 63, r0 = threadIdx.x >> 6, i = blockIdx.x * 64 + e;
-  float a = 0.f;
-  if (i < n)
-    for (int r = r0; r < p.rows; r += 4) a += p.part[(size_t)r * n + i];
-  s[r0][e] = a;
-  __syncthreads();
-  if (r0 != 0 || i >= n) return;
-  a = (s[0][e] + s[1][e]) + (s[2][e] + s[3][e]);
-  const int c = i / (p.W + 1), j = i % (p.W + 1);
-  if (j < p.W) p.dw[(size_t)c * p.W + j] = a;
+  const int64_t n = (int64_t)p.C * (p.W + 1), col0 = (int64_t)blockIdx.x * SUM_COLS, i = col0 + threadIdx.x;
+  const float a = column_sum(p.part, p.rows, n, col0);
+  if (threadIdx.x >= SUM_COLS || i >= n) return;
+  const int64_t c = i / (p.W + 1);
+  const int j = (int)(i - c * (p.W + 1));
+  if (j < p.W) p.dw[c * p.W + j] = a;
   else if (p.dbias) p.dbias[c] = a;
 }
 
@@ -351,10 +347,7 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_step_kernel(const E *x, 
   load8<E>(x + (size_t)n * C + c0, xv);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) load8<E>(st + (size_t)k * C, h[k]);
-  ConvSiluParams p = {};
-  p.w = wt;
-  p.bias = bs;
-  load_weights<E, W>(p, c0, w, bias);
+  load_weights<W>(wt, bs, c0, w, bias);
 #pragma unroll
   for (int e = 0; e < CS_CH; ++e) {
     const float z = conv_at<W>(w, bias, h, xv, e);
@@ -455,7 +448,7 @@ extern "C" dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, in
                                   const int32_t *cu_seqlens, void *y, void *sT, hipStream_t stream) {
   const dn_status st = check(B, T, H, D, W, n_seqs, dtype, w, cu_seqlens);
   if (st != DN_OK) return st;
-  if (!aligned16(s0) || !aligned16(sT)) return DN_EINVAL;
+  if (!aligned16(s0) || !aligned16(sT) || !aligned16(w) || !aligned16(bias)) return DN_EINVAL;
   if (T > 0 && (!x || !y || !aligned16(x) || !aligned16(y))) return DN_EINVAL;
   ConvSiluParams p = {};
   p.x = x;
@@ -497,7 +490,7 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
                                       hipStream_t stream) {
   const dn_status st = check(B, T, H, D, W, n_seqs, dtype, w, cu_seqlens);
   if (st != DN_OK) return st;
-  if (!dw || !aligned16(s0) || !aligned16(dsT) || !aligned16(ds0)) return DN_EINVAL;
+  if (!dw || !aligned16(s0) || !aligned16(dsT) || !aligned16(ds0) || !aligned16(w) || !aligned16(bias)) return DN_EINVAL;
   if (T > 0 && (!x || !dy || !dx || !aligned16(x) || !aligned16(dy) || !aligned16(dx))) return DN_EINVAL;
   ConvSiluParams p = {};
   p.x = x;
@@ -525,7 +518,7 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
   if (dtype == DN_BF16) launch_bwd_e<bf16>(p, stream);
   else launch_bwd_e<float>(p, stream);
   if (hipGetLastError() != hipSuccess) return DN_EHIP;
-  hipLaunchKernelGGL(conv_silu_sum_kernel, dim3((p.C * (W + 1) + 63) / 64), dim3(CS_THREADS), 0, stream, p);
+  hipLaunchKernelGGL(conv_silu_sum_kernel, dim3(((int64_t)p.C * (W + 1) + SUM_COLS - 1) / SUM_COLS), dim3(CS_THREADS), 0, stream, p);
   return hipGetLastError() == hipSuccess ? DN_OK : DN_EHIP;
 }
 
@@ -533,7 +526,9 @@ extern "C" dn_status dn_conv_silu_step(int32_t B, int32_t H, int32_t D, int32_t 
                                        const float *w, const float *bias, void *state, void *y, hipStream_t stream) {
   const dn_status st = check(B, 1, H, D, W, B, dtype, w, nullptr);
   if (st != DN_OK) return st;
-  if (!x || !y || (W > 1 && !state) || !aligned16(x) || !aligned16(y) || !aligned16(state)) return DN_EINVAL;
+  if (!x || !y || (W > 1 && !state) || !aligned16(x) || !aligned16(y) || !aligned16(state) || !aligned16(w) ||
+      !aligned16(bias))
+    return DN_EINVAL;
   const int64_t total = (int64_t)B * (H * D / CS_CH);
   if (total > INT32_MAX) return DN_EUNSUPPORTED;
   if (dtype == DN_BF16) launch_step_e<bf16>(W, x, w, bias, state, y, (uint32_t)total, H * D, stream);

@@ -191,16 +191,11 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_bwd_kernel(GatedNormPar
   }
 }
 
-// dw from the workgroups' partial sums: 64 columns by four groups
+// dw from the workgroups' partial sums
 __global__ __launch_bounds__(GN_THREADS) void gated_norm_sum_kernel(GatedNormParams p) {
-  __shared__ float s[4][64];
-  const int wr = blockIdx.y, e = threadIdx.x & 63, r0 = threadIdx.x >> 6, c = blockIdx.x * 64 + e;
-  float a = 0.f;
-  if (c < p.D)
-    for (int b = r0; b < p.blocks; b += 4) a += p.part[((size_t)wr * p.blocks + b) * p.D + c];
-  s[r0][e] = a;
-  __syncthreads();
-  if (r0 == 0 && c < p.D) p.dw[(size_t)wr * p.D + c] = (s[0][e] + s[1][e]) + (s[2][e] + s[3][e]);
+  const int wr = blockIdx.y, col0 = blockIdx.x * SUM_COLS, c = col0 + threadIdx.x;
+  const float a = column_sum(p.part + (size_t)wr * p.blocks * p.D, p.blocks, p.D, col0);
+  if (threadIdx.x < SUM_COLS && c < p.D) p.dw[(size_t)wr * p.D + c] = a;
 }
 
 // ------------------------------------------------------------------- host
@@ -310,6 +305,6 @@ extern "C" dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32
   if (dtype == DN_BF16) launch_e<bf16>(p, gate_first != 0, true, stream);
   else launch_e<float>(p, gate_first != 0, true, stream);
   if (hipGetLastError() != hipSuccess) return DN_EHIP;
-  hipLaunchKernelGGL(gated_norm_sum_kernel, dim3((D + 63) / 64, R), dim3(GN_THREADS), 0, stream, p);
+  hipLaunchKernelGGL(gated_norm_sum_kernel, dim3((D + SUM_COLS - 1) / SUM_COLS, R), dim3(GN_THREADS), 0, stream, p);
   return hipGetLastError() == hipSuccess ? DN_OK : DN_EHIP;
 }

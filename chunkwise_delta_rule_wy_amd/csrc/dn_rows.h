@@ -59,4 +59,34 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&x)[N]) {
   for (int e = 0; e < N; e += 4) *reinterpret_cast<f32x4 *>(dst + e) = (f32x4){x[e], x[e + 1], x[e + 2], x[e + 3]};
 }
 
+// Sums over the rows of a [rows][n] fp32 matrix (n a multiple of 4), for the
+// second stage of a deterministic reduction: a workgroup of 256 threads takes
+// 16 columns, four lanes of 16 bytes each, and 64 interleaved groups of rows,
+// whose sums meet in LDS, so that even a narrow matrix has enough loads in
+// flight.  Thread t < 16 gets the sum of column 16 blockIdx.x + t.
+constexpr int SUM_COLS = 16;
+__device__ __forceinline__ float column_sum(const float *m, int rows, int64_t n, int64_t col0) {
+  __shared__ float part[64][SUM_COLS];
+  const int q = threadIdx.x & 3, g = threadIdx.x >> 2;
+  const int64_t c = col0 + 4 * q;
+  f32x4 a = zero4();
+  if (c < n) {
+    int r = g;
+    for (; r + 3 * 64 < rows; r += 4 * 64) {
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const f32x4 *>(m + (r + 64 * i) * n + c);
+      a += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; r < rows; r += 64) a += *reinterpret_cast<const f32x4 *>(m + r * n + c);
+  }
+  *reinterpret_cast<f32x4 *>(&part[g][4 * q]) = a;
+  for (int d = 32; d > 0; d >>= 1) {
+    __syncthreads();
+    if (g < d) *reinterpret_cast<f32x4 *>(&part[g][4 * q]) += *reinterpret_cast<const f32x4 *>(&part[g + d][4 * q]);
+  }
+  __syncthreads();
+  return threadIdx.x < SUM_COLS ? part[0][threadIdx.x] : 0.f;
+}
+
 }  // namespace dn

@@ -151,6 +151,15 @@ __device__ __forceinline__ double row_sum16_d(double x) {
   x += dpp0d<0x128>(x);
   return x;
 }
+// over the four rows of 16 lanes: the sum, and the sum of the rows after this one
+__device__ __forceinline__ float row_suffix(float x, int g, float &after) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float pair = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(pair), __float_as_uint(pair), false, false);
+  const float hi = __uint_as_float(b[1]);
+  after = (g & 1 ? 0.f : __uint_as_float(a[1])) + (g & 2 ? 0.f : hi);
+  return __uint_as_float(b[0]) + hi;
+}
 __device__ __forceinline__ double lane_val_d(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
@@ -161,7 +170,8 @@ __device__ __forceinline__ double lane_val_d(double v, int lane) {
 // Gate table of one (chunk, head): s, the log2 decays b = bh + bl (two floats
 // hold them to 2^-48), gamma, w, w s; `last` = gamma_63.
 struct GateTab {
-  float s[CH], bh[CH], bl[CH], gam[CH], w[CH], ws[CH];
+  alignas(16) float s[CH];
+  float bh[CH], bl[CH], gam[CH], w[CH], ws[CH];
   float last, pad[3];
 };
 // One wave fills the table from the raw step sizes of its lanes' tokens (lanes
@@ -185,9 +195,30 @@ __device__ __forceinline__ double fill_gates(GateTab &t, float raw, float A, int
   }
   return total;
 }
-// Gamma_rj from the table's entries of r and j
-__device__ __forceinline__ float decay_ratio(float bhr, float blr, float bhj, float blj) {
-  return wy::fexp2((bhr - bhj) + (blr - blj));
+__device__ __forceinline__ f32x4 lds4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+// Keeps a value's computation where it stands: without it a select between
+// the value and zero becomes a branch around the computation, one for each
+// element.
+__device__ __forceinline__ float computed(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+// A lane-dependent value that the compiler takes for a new one here: what is
+// computed from it is computed where it is used, instead of being held in
+// registers (or spilled) across a loop that needs them all.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+// The decay ratios Gamma of four rows r = r0 .. r0 + 3 to one column, or of one
+// row to four columns j = r0 .. (sign -1), from the table's entries; ratios
+// whose row is before their column come out as anything.
+__device__ __forceinline__ f32x4 decay_ratios(const GateTab &t, int r0, float bh, float bl, float sign) {
+  const f32x4 h = lds4(t.bh + r0), l = lds4(t.bl + r0);
+  f32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = wy::fexp2(sign * ((h[i] - bh) + (l[i] - bl)));
+  return x;
 }
 
 // x = p0 + p1 + p2 to 24 bits, each part a bf16 operand fragment
@@ -226,6 +257,9 @@ __device__ __forceinline__ void unpack8(const bf16x8 &f, float (&x)[8]) {
   }
 }
 
+// the wave's number, as the scalar that it is
+__device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane(wave_id()); }
+
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
@@ -233,34 +267,45 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
 // 32-index operand fragment whose rows are the matrix's columns: 16 columns
 // c0 .. of an LDS matrix with `stride` bytes per row, contraction index = its
 // rows r0 + 8 g .. r0 + 8 g + 7 (lane group g)
-__device__ __forceinline__ bf16x8 frag_tr(uint32_t base, int stride, int r0, int c0) {
-  const int l = lane_id(), g = l >> 4, e = (l >> 2) & 3, q = l & 3;
+__device__ __forceinline__ bf16x8 frag_tr(uint32_t base, int stride, int r0, int c0, int l) {
+  const int g = l >> 4, e = (l >> 2) & 3, q = l & 3;
   const uint32_t a = base + (r0 + 8 * g + e) * stride + 2 * (c0 + 4 * q);
   return wy::cat(wy::ld_tr(a), wy::ld_tr(a + 4 * stride));
 }
 
-// A rows x COLS bf16 tile staged through registers: each of the workgroup's
+// Global accesses of a workgroup go to a uniform base (scalar registers) plus a
+// 32-bit byte offset per lane: the byte span of a chunk's rows, or of a state,
+// stays below 2^31.
+template <typename T>
+__device__ __forceinline__ T ldg(const void *base, uint32_t off) {
+  return *reinterpret_cast<const T *>(static_cast<const char *>(base) + off);
+}
+template <typename T>
+__device__ __forceinline__ void stg(void *base, uint32_t off, const T &x) {
+  *reinterpret_cast<T *>(static_cast<char *>(base) + off) = x;
+}
+
+// A ROWS x COLS bf16 tile staged through registers: each of the workgroup's
 // THR threads holds its share as 16-byte units, zero from row L on.
 template <int ROWS, int COLS, int THR>
 struct Stage {
-  static constexpr int UPR = COLS / 8, NU = ROWS * UPR / THR;
-  static_assert(ROWS * UPR % THR == 0, "whole units per thread");
+  static constexpr int UPR = COLS / 8, NU = ROWS * UPR / THR, RSTEP = THR / UPR;
+  static_assert(ROWS * UPR % THR == 0 && THR % UPR == 0, "whole units and rows per thread");
   u128 u[NU];
-  // rows of `pitch` elements; src points at the tile's first element
-  __device__ __forceinline__ void load(const bf16 *src, size_t pitch, int L) {
+  // rows of `pitch` bytes; base points at the tile's first element
+  __device__ __forceinline__ void load(const bf16 *base, uint32_t pitch, int L) {
+    const int r0 = threadIdx.x / UPR, c = threadIdx.x % UPR;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int x = threadIdx.x + THR * i, r = x / UPR, c = x % UPR;
-      u[i] = r < L ? ldg128(src + r * pitch + 8 * c) : zero128();
+      const int r = r0 + RSTEP * i;
+      u[i] = r < L ? ldg<u128>(base, r * pitch + 16 * c) : zero128();
     }
   }
   template <int STRIDE>
   __device__ __forceinline__ void store(bf16 *lds) const {
+    const int r0 = threadIdx.x / UPR, c = threadIdx.x % UPR;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int x = threadIdx.x + THR * i, r = x / UPR, c = x % UPR;
-      *reinterpret_cast<u128 *>(lds + r * STRIDE + 8 * c) = u[i];
-    }
+    for (int i = 0; i < NU; ++i) *reinterpret_cast<u128 *>(lds + (r0 + RSTEP * i) * STRIDE + 8 * c) = u[i];
   }
 };
 

@@ -24,6 +24,8 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
   if (st != DN_OK) return st;
   if (packed ? s->B != 1 : s->n_seqs != s->B) return DN_EINVAL;
   if (s->dtype != DN_BF16) return DN_EUNSUPPORTED;  // the chunk kernels are bf16
+  // the kernels address a chunk's rows with 32-bit byte offsets
+  if ((int64_t)128 * s->H * s->Dv > INT32_MAX || (int64_t)128 * s->G * s->Dk > INT32_MAX) return DN_EUNSUPPORTED;
   return DN_OK;
 }
 

@@ -18,11 +18,10 @@
 // One workgroup of eight waves owns a chunk of one group and a set of its
 // heads: G, dG, dq and dk stay in registers while the heads pass by, so that
 // the sum over the heads that share a key costs nothing, and dG's products
-// with K and Q are made once for all of them.  dlog's first term is the suffix
-// sum of row sums less column sums of E without its diagonal, which belongs to
-// no t: where the decay is strong the diagonal outweighs all else, and would
-// have to cancel.  The sums are in double, so that what cancels leaves nothing:
-// an error there is the same for all earlier tokens and adds up in dA.  Wave (cb, half) = (w % 4, w / 4)
+// with K and Q are made once for all of them.  dlog's pairs are
+// summed as they stand, suffix sums down the columns and then across, never as
+// a difference of larger sums: with a strong decay E's diagonal, which belongs
+// to no t, outweighs the rest, and an error that all tokens share adds up in dA.  Wave (cb, half) = (w % 4, w / 4)
 // owns token column block cb of the 64 x 64 matrices, of M and dG only the row
 // blocks 2 half, 2 half + 1, and of dv the columns' half; for dq and dk a
 // wave owns 16 of the Dk rows.
@@ -41,10 +40,11 @@ struct GradLds {
   alignas(16) bf16 v[CH * VS];
   alignas(16) bf16 dO[CH * VS];
   alignas(16) bf16 dh[DK * VS];  // dh rounded, for K dh; at the end dG^T
+  alignas(16) bf16 p[CH * VS];   // the head's P^T, zero above the diagonal blocks
   GateTab tabs[2];               // by the head's parity
   struct Sums {
-    double row_x[4][CH], col_x[2][CH], hd[8];
-    float col_e[2][CH], diag_e[CH], qd[NT][CH], kd[NT][CH], diag[4];
+    double hd[8];
+    float pairs[4][CH], col_e[2][CH], diag_e[CH], qd[NT][CH], kd[NT][CH], diag[4];
   } sums[2];
 };
 
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   constexpr int KB = DK / 32, QS = LD::QS, VS = LD::VS, NT = LD::NT;
   constexpr int NTT = NT / 2;  // token tiles of a wave's dq and dk
   __shared__ LD s;
-  const int w = wave_id(), l = lane_id(), g = l >> 4, m = l & 15;
+  const int w = wave_number(), lane = lane_id(), l = lane, g = l >> 4, m = l & 15;
   const int item = xcd_item(blockIdx.x, p.nchunks * p.G * p.sets);
   const int chunk = item / (p.G * p.sets), grp = item % (p.G * p.sets) / p.sets, set = item % p.sets;
   int L;
@@ -76,6 +76,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     row0 += (size_t)c * CH;
     L = min(CH, len - c * CH);
   }
+  // Odd chunks work on -dO and -dh, and their results change sign at the end, so
+  // that the one-sided rounding of the matrix products does not add up in dA.
+  const uint32_t flip = chunk & 1 ? 0x80008000u : 0u;
+  const float sign = chunk & 1 ? -1.f : 1.f;
   const int R = p.H / p.G;
   const int h_first = grp * R + set * p.set_heads;
   const int heads = min(p.set_heads, R - set * p.set_heads);
@@ -86,7 +90,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 
   {
     Stage<CH, DK, GRAD_THREADS> st;
-    const size_t off = (row0 * p.G + grp) * DK, pitch = (size_t)p.G * DK;
+    const size_t off = (row0 * p.G + grp) * DK;
+    const uint32_t pitch = 2 * p.G * DK;
     st.load(p.q + off, pitch, L);
     st.template store<QS>(s.q);
     st.load(p.k + off, pitch, L);
@@ -94,17 +99,25 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   }
   Stage<CH, SSM_TILE, GRAD_THREADS> sv, so;
   f32x4 hr[2][2], dr[2][2];  // the wave's rows of h and dh: [32-column block][half of 8 columns]
-  auto fetch = [&](int h, int tile) {
-    const size_t off = (row0 * p.H + h) * p.DV + tile * SSM_TILE, pitch = (size_t)p.H * p.DV;
+  const uint32_t state_off = 4 * ((n0 + m) * p.DV + 8 * g);
+  auto fetch_rows = [&](int h, int tile) {
+    const size_t off = (row0 * p.H + h) * p.DV + tile * SSM_TILE;
+    const uint32_t pitch = 2 * p.H * p.DV;
     sv.load(p.v + off, pitch, L);
     so.load(p.dO + off, pitch, L);
-    const size_t st = (((size_t)chunk * p.H + h) * DK + n0 + m) * p.DV + tile * SSM_TILE + 8 * g;
+#pragma unroll
+    for (auto &u : so.u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u.w[i] ^= flip;
+  };
+  auto fetch_states = [&](int h, int tile) {
+    const size_t at = ((size_t)chunk * p.H + h) * DK * p.DV + tile * SSM_TILE;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        hr[kb][x] = *reinterpret_cast<const f32x4 *>(p.states + st + 32 * kb + 4 * x);
-        dr[kb][x] = *reinterpret_cast<const f32x4 *>(p.dstates + st + 32 * kb + 4 * x);
+        hr[kb][x] = ldg<f32x4>(p.states + at, state_off + 128 * kb + 16 * x);
+        dr[kb][x] = sign * ldg<f32x4>(p.dstates + at, state_off + 128 * kb + 16 * x);
       }
   };
   auto gates = [&](int hh) {  // one wave
@@ -116,10 +129,9 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     const int h = h_first + hh;
     const GateTab &T = s.tabs[hh & 1];
     const typename LD::Sums &x = s.sums[hh & 1];
-    float qd = 0.f, kd = 0.f;
+    float pairs = 0.f, qd = 0.f, kd = 0.f;
     double hd = 0.;
-    double db = -(x.col_x[0][l] + x.col_x[1][l]);
-    for (int c = 0; c <= (l >> 4); ++c) db += x.row_x[c][l];
+    for (int c = 0; c <= (l >> 4); ++c) pairs += x.pairs[c][l];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       qd += x.qd[t][l];
@@ -129,35 +141,37 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     for (int t = 0; t < 8; ++t) hd += x.hd[t];
     const float st = T.s[l], wu = T.w[l] * kd;
     const float ds = ((x.col_e[0][l] + x.col_e[1][l]) + x.diag_e[l]) + wu;
-    const double su = (double)st * wu;
-    db += (double)(T.gam[l] * qd);
-    const double incl = wave_incl_scan_d(db), before = wave_incl_scan_d(su) - su;
-    const float dlog = (float)((lane_val_d(incl, 63) - incl + db) + before + (double)T.last * hd);
+    // sums over the tokens before t, of all and (t < 32) of E's lower rows, and over those from t on
+    const double su = (double)st * wu, low = (double)st * x.col_e[1][l], z = (double)(T.gam[l] * qd);
+    const double before = wave_incl_scan_d(su) - su, below = wave_incl_scan_d(low) - low;
+    const double incl = wave_incl_scan_d(z);
+    const float dlog =
+        (float)((double)pairs + (l < 32 ? below : 0.) + (lane_val_d(incl, 63) - incl + z) + before + (double)T.last * hd);
     const float ddt = (ds + p.A[h] * dlog) * -expm1f(-st);  // sigmoid(x) = 1 - exp(-softplus(x))
-    if (l < L) p.ddt[(row0 + l) * p.H + h] = ddt;
+    if (l < L) p.ddt[(row0 + l) * p.H + h] = sign * ddt;
     const float dA = wave_sum(st * dlog), db_sum = wave_sum(l < L ? ddt : 0.f);
     if (l == 0) {
       float *out = p.par_part + ((size_t)chunk * p.H + h) * 3;
-      out[0] = dA;
-      out[1] = db_sum;
-      out[2] = (x.diag[0] + x.diag[1]) + (x.diag[2] + x.diag[3]);
+      out[0] = sign * dA;
+      out[1] = sign * db_sum;
+      out[2] = sign * ((x.diag[0] + x.diag[1]) + (x.diag[2] + x.diag[3]));
     }
   };
 
-  fetch(h_first, 0);
+  fetch_rows(h_first, 0);
+  fetch_states(h_first, 0);
   if (w == 3) gates(0);
   __syncthreads();
 
   // G: tiles of rows r (four per lane), column j
-  f32x4 G[4], dG[2], gm[4];
-  bf16x8 kf[KB];  // K row j
+  f32x4 G[2], dG[2];
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb) kf[kb] = frag_row(s.k, QS, j, 32 * kb + 8 * g);
+  for (int x = 0; x < 2; ++x) {
+    G[x] = zero4();
 #pragma unroll
-  for (int rb = 0; rb < 4; ++rb) {
-    G[rb] = zero4();
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) G[rb] = mma32(G[rb], frag_row(s.q, QS, 16 * rb + m, 32 * kb + 8 * g), kf[kb]);
+    for (int kb = 0; kb < KB; ++kb)
+      G[x] = mma32(G[x], frag_row(s.q, QS, 16 * (2 * half + x) + m, 32 * kb + 8 * g), frag_row(s.k, QS, j, 32 * kb + 8 * g));
+    *reinterpret_cast<bf16x4 *>(s.p + j * VS + 16 * (2 * half + x) + 4 * g) = cvt_bf16x4(zero4());
   }
   dG[0] = dG[1] = zero4();
   f32x4 dq[NTT], dk[NTT];
@@ -171,157 +185,170 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     typename LD::Sums &sums = s.sums[hh & 1];
     f32x4 M[2];
     M[0] = M[1] = zero4();
-    bf16x8 pf[2];
-    float sj = 0.f, wsj = 0.f, qd[NTT], kd[NTT];
     double hd = 0.;
-#pragma unroll
-    for (int t = 0; t < NTT; ++t) qd[t] = kd[t] = 0.f;
     const float skip = p.skip ? p.skip[h] : 0.f;
     for (int tile = 0; tile < p.ntiles; ++tile) {
+      // what the next step needs (the last step loads its own again: a load that
+      // may not take place would hold two sets of registers)
+      const bool next_tile = tile + 1 < p.ntiles, more = next_tile || hh + 1 < heads;
+      const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
+      const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
       __syncthreads();
       sv.template store<VS>(s.v);
       so.template store<VS>(s.dO);
-      Split hs[2], ds[2];
-      float dot = 0.f;
+      if (own_rows) {
+        float dot = 0.f;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float x[8], y[8];
+        for (int kb = 0; kb < 2; ++kb) {
+          *reinterpret_cast<bf16x8 *>(s.dh + (n0 + m) * VS + 32 * kb + 8 * g) = bfrag<bf16>(dr[kb][0], dr[kb][1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = hr[kb][i >> 2][i & 3];
-          y[i] = dr[kb][i >> 2][i & 3];
-          dot += x[i] * y[i];
+          for (int i = 0; i < 8; ++i) dot += hr[kb][i >> 2][i & 3] * dr[kb][i >> 2][i & 3];
         }
-        hs[kb] = split3(x);
-        ds[kb] = split3(y);
-        if (own_rows) *reinterpret_cast<bf16x8 *>(s.dh + (n0 + m) * VS + 32 * kb + 8 * g) = ds[kb].p[0];
+        hd += (double)dot;
       }
-      if (own_rows) hd += (double)dot;
-      __syncthreads();
-      if (tile + 1 < p.ntiles) fetch(h, tile + 1);
-      else if (hh + 1 < heads) fetch(h + 1, 0);
-      if (tile == 0) {  // the head's decay ratios and P
-        sj = T.s[j];
-        wsj = T.ws[j];
-        const float bhj = T.bh[j], blj = T.bl[j];
-        f32x4 P[4];
+      if (tile == 0) {
+        const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
 #pragma unroll
-        for (int rb = 0; rb < 4; ++rb) {
+        for (int x = 0; x < 2; ++x) {
+          const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
+          if (rb < cb) continue;
+          const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
+          f32x4 P;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = 16 * rb + 4 * g + i;
-            gm[rb][i] = r >= j ? decay_ratio(T.bh[r], T.bl[r], bhj, blj) : 0.f;
-            P[rb][i] = r >= j ? G[rb][i] * gm[rb][i] * sj : 0.f;
+            const float v = computed(G[x][i] * (gm[i] * sj));
+            P[i] = r0 + i >= j ? v : 0.f;
           }
+          *reinterpret_cast<bf16x4 *>(s.p + j * VS + r0) = cvt_bf16x4(P);
         }
-        pf[0] = bfrag<bf16>(P[0], P[1]);
-        pf[1] = bfrag<bf16>(P[2], P[3]);
       }
+      __syncthreads();
+      fetch_rows(nh, nt);
+      // h dO^T, then dh V^T: the wave's 16 Dk rows.  The states' registers are
+      // free after that for the next ones, which arrive during the rest.
+      auto rows = [&](const f32x4 (&st)[2][2], const bf16 *ly, const bf16 *lx, const float *coef, f32x4 (&acc)[NTT],
+                      float *dots) {
+        f32x4 a[NTT];
+#pragma unroll
+        for (int t = 0; t < NTT; ++t) a[t] = zero4();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          bf16x8 y[NTT];
+#pragma unroll
+          for (int t = 0; t < NTT; ++t) y[t] = frag_row(ly, VS, 16 * (tt0 + t) + m, 32 * kb + 8 * g);
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = st[kb][i >> 2][i & 3];
+          const Split sp = split3(x);
+#pragma unroll
+          for (int k = 2; k >= 0; --k)
+#pragma unroll
+            for (int t = 0; t < NTT; ++t) a[t] = mma32(a[t], sp.p[k], y[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < NTT; ++t) {
+          const int r = 16 * (tt0 + t) + m;
+          const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(lx + r * QS + n0 + 4 * g);
+          const float c = coef[r];
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dot += (float)xv[i] * a[t][i];
+            acc[t][i] += c * a[t][i];
+          }
+          dot = cross_row_sum(dot);
+          if (g == 0) dots[r] = tile == 0 ? dot : dots[r] + dot;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      rows(hr, s.dO, s.q, T.gam, dq, sums.qd[n0 / 16]);
+      rows(dr, s.v, s.k, T.ws, dk, sums.kd[n0 / 16]);
+      fetch_states(nh, nt);
       // M, the wave's row blocks
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rb = 2 * half + x;
+      for (int kb = 0; kb < 2; ++kb) {
+        const bf16x8 vf = frag_row(s.v, VS, j, 32 * kb + 8 * g);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-          M[x] = mma32(M[x], frag_row(s.dO, VS, 16 * rb + m, 32 * kb + 8 * g), frag_row(s.v, VS, j, 32 * kb + 8 * g));
+        for (int x = 0; x < 2; ++x)
+          M[x] = mma32(M[x], frag_row(s.dO, VS, 16 * (2 * half + x) + m, 32 * kb + 8 * g), vf);
       }
-      // h dO^T and dh V^T, the wave's 16 Dk rows
-#pragma unroll
-      for (int t = 0; t < NTT; ++t) {
-        const int r = 16 * (tt0 + t) + m;
-        f32x4 a = zero4(), b = zero4();
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const bf16x8 of = frag_row(s.dO, VS, r, 32 * kb + 8 * g), vf = frag_row(s.v, VS, r, 32 * kb + 8 * g);
-#pragma unroll
-          for (int k = 2; k >= 0; --k) {
-            a = mma32(a, hs[kb].p[k], of);
-            b = mma32(b, ds[kb].p[k], vf);
-          }
-        }
-        const bf16x4 qv = *reinterpret_cast<const bf16x4 *>(s.q + r * QS + n0 + 4 * g);
-        const bf16x4 kv = *reinterpret_cast<const bf16x4 *>(s.k + r * QS + n0 + 4 * g);
-        const float gam = T.gam[r], ws = T.ws[r];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qd[t] += (float)qv[i] * a[i];
-          kd[t] += (float)kv[i] * b[i];
-          dq[t][i] += gam * a[i];
-          dk[t][i] += ws * b[i];
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
       // dv, token j, the wave's two column tiles
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int pt = 2 * half + x;
-        f32x4 a = zero4(), b = zero4();
+      {
+        f32x4 a[2], b[2];
+        a[0] = a[1] = b[0] = b[1] = zero4();
+        const float wsj = T.ws[j];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          const int e = (l >> 2) & 3, q4 = l & 3;
-          const uint32_t at = ao + (32 * kb + 4 * g + e) * 2 * VS + 2 * (16 * pt + 4 * q4);
-          a = mma32(a, wy::cat(wy::ld_tr(at), wy::ld_tr(at + 16 * 2 * VS)), pf[kb]);
+          if (2 * kb + 1 < cb) continue;  // zeros
+          const bf16x8 pf = frag_row(s.p, VS, j, 32 * kb + 8 * g);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) a[x] = mma32(a[x], frag_tr(ao, 2 * VS, 32 * kb, 16 * (2 * half + x), l), pf);
+        }
+        mfma_settle();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const bf16x8 kf = frag_row(s.k, QS, j, 32 * kb + 8 * g);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) b[x] = mma32(b[x], frag_tr(ad, 2 * VS, 32 * kb, 16 * (2 * half + x), l), kf);
         }
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) b = mma32(b, frag_tr(ad, 2 * VS, 32 * kb, 16 * pt), kf[kb]);
-        const bf16x4 ov = *reinterpret_cast<const bf16x4 *>(s.dO + j * VS + 16 * pt + 4 * g);
-        f32x4 o;
+        for (int x = 0; x < 2; ++x) {
+          const int c = 16 * (2 * half + x) + 4 * g;
+          const bf16x4 ov = *reinterpret_cast<const bf16x4 *>(s.dO + j * VS + c);
+          f32x4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = a[i] + wsj * b[i] + skip * (float)ov[i];
-        if (j < L)
-          *reinterpret_cast<bf16x4 *>(p.dv + ((row0 + j) * p.H + h) * p.DV + tile * SSM_TILE + 16 * pt + 4 * g) =
-              cvt_bf16x4(o);
+          for (int i = 0; i < 4; ++i) o[i] = sign * (a[x][i] + wsj * b[x][i] + skip * (float)ov[i]);
+          if (j < L)
+          stg<bf16x4>(p.dv + (row0 * p.H + h) * p.DV + tile * SSM_TILE, 2 * (j * (p.H * p.DV) + c), cvt_bf16x4(o));
+        }
       }
       if (tile == 0 && w == 3) {  // this wave has no blocks of M below
         if (hh > 0) finish(hh - 1);
         if (hh + 1 < heads) gates(hh + 1);
       }
     }
-    // the head's sums over the 64 x 64 matrices
-    float col = 0.f, diag = 0.f, diag_e = 0.f;
-    double col_x = 0.;
+    // the head's sums over the 64 x 64 matrices; `below` sums a column's rows
+    // after the tile
+    const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
+    const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
+    float below = 0.f, diag = 0.f, diag_e = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int rb = 2 * half + x;
+    for (int x = 1; x >= 0; --x) {
+      const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
       if (rb < cb) continue;
-      const f32x4 gmx = half ? gm[2 + x] : gm[x], Gx = half ? G[2 + x] : G[x];
+      const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
+      f32x4 e;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool in = 16 * rb + 4 * g + i >= j;
-        const float mg = in ? M[x][i] * gmx[i] : 0.f;
-        const bool on = rb == cb && 4 * g + i == m;
-        float e = in ? mg * Gx[i] : 0.f;
-        dG[x][i] += mg * sj;
-        if (on) {
-          diag = M[x][i];
-          diag_e = e;
-          e = 0.f;
-        }
-        col += e;
-        const double x64 = (double)(e * sj), row = row_sum16_d(x64);
-        col_x += x64;
-        if (m == 0) sums.row_x[cb][16 * rb + 4 * g + i] = row;
+        const float v = computed(M[x][i] * gm[i]);
+        dG[x][i] += (r0 + i >= j ? v : 0.f) * sj;
+        const float u = computed(v * G[x][i]);
+        e[i] = r0 + i > j ? u : 0.f;
+        diag = r0 + i == j ? M[x][i] : diag;
+        diag_e = r0 + i == j ? u : diag_e;
       }
+      // over the rows from this one on
+      e[2] += e[3];
+      e[1] += e[2];
+      e[0] += e[1];
+      float after;
+      const float sum = row_suffix(e[0], g, after);
+      after += below;
+      below += sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float d = row_sum16(r0 + i > j ? (e[i] + after) * sj : 0.f);
+        if (m == 0) sums.pairs[cb][r0 + i] = d;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    col = cross_row_sum(col);
-    col_x += __shfl_xor(col_x, 16, 64);
-    col_x += __shfl_xor(col_x, 32, 64);
-    if (g == 0) {
-      sums.col_e[half][j] = col;
-      sums.col_x[half][j] = col_x;
-    }
+    if (g == 0) sums.col_e[half][j] = below;
     if (half == cb / 2) {
       diag_e = cross_row_sum(diag_e);
       if (g == 0) sums.diag_e[j] = diag_e;
       diag = wave_sum(diag);
       if (l == 0) sums.diag[cb] = diag;
-    }
-#pragma unroll
-    for (int t = 0; t < NTT; ++t) {
-      const float a = cross_row_sum(qd[t]), b = cross_row_sum(kd[t]);
-      if (g == 0) {
-        sums.qd[n0 / 16][16 * (tt0 + t) + m] = a;
-        sums.kd[n0 / 16][16 * (tt0 + t) + m] = b;
-      }
     }
     hd = row_sum16_d(hd);
     hd += __shfl_xor(hd, 16, 64);
@@ -342,8 +369,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     const int tt = tt0 + t, r = 16 * tt + m;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      dq[t] = mma32(dq[t], frag_tr(ak, 2 * QS, 32 * kb, n0), frag_tr(ad, 2 * VS, 32 * kb, 16 * tt));
-      dk[t] = mma32(dk[t], frag_tr(aq, 2 * QS, 32 * kb, n0), frag_row(s.dh, VS, r, 32 * kb + 8 * g));
+      dq[t] = mma32(dq[t], frag_tr(ak, 2 * QS, 32 * kb, n0, l), frag_tr(ad, 2 * VS, 32 * kb, 16 * tt, l));
+      dk[t] = mma32(dk[t], frag_tr(aq, 2 * QS, 32 * kb, n0, l), frag_row(s.dh, VS, r, 32 * kb + 8 * g));
     }
   }
   mfma_settle();
@@ -351,6 +378,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   for (int t = 0; t < NTT; ++t) {
     const int r = 16 * (tt0 + t) + m;
     if (r >= L) continue;
+    dq[t] *= sign;
+    dk[t] *= sign;
     const size_t at = ((row0 + r) * p.G + grp) * DK + n0 + 4 * g;
     if (p.dq_part) {
       const size_t part = (size_t)set * p.rows * p.G * DK + at;

@@ -17,7 +17,10 @@ namespace {
 // Without STORE the sweep starts from zero and leaves the segment's own end
 // state (`seg_state`) and log decay; with it, it starts from the joined state
 // and stores the state of every chunk before the chunk's update.  REV runs
-// the chunks backwards over (q, dO, gamma).
+// the chunks backwards over (q, dO, gamma).  The accumulators change sign from
+// chunk to chunk: the matrix instructions' sums come out below the exact ones
+// on average (by some 2^-25 of their size), and an error of one sign in the
+// states would add up in dA, where it reached 2e-6 of the result.
 template <int DK>
 struct SweepLds {
   static constexpr int XS = DK + 16, YS = SSM_TILE + 16;  // row strides: 4 rows of a transposed read in separate banks
@@ -35,14 +38,15 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK> &lds, int
   Segment sg;
   if (!segment(p, seg, sg)) return;
   if (!STORE && (REV ? sg.first : sg.last)) return;  // nothing follows it
-  const int w = wave_id(), l = lane_id(), g = l >> 4, m = l & 15;
+  const int w = wave_number(), l = lane_id(), g = l >> 4, m = l & 15;
   const int grp = h / (p.H / p.G);
   const bf16 *X = (REV ? p.q : p.k) + (sg.row * p.G + grp) * DK;
   const bf16 *Y = (REV ? p.dO : p.v) + (sg.row * p.H + h) * p.DV + tile * SSM_TILE;
-  const size_t xp = (size_t)p.G * DK, yp = (size_t)p.H * p.DV;
+  const size_t xp = (size_t)p.G * DK, yp = (size_t)p.H * p.DV;  // elements of a token
   const int nch = (sg.len + CH - 1) / CH;
   const size_t per_state = (size_t)DK * p.DV;
-  const size_t lane_off = tile * SSM_TILE + 16 * w + 4 * g;  // of the lane's four columns
+  // byte offsets of the lane's four columns in the state's row m, and of 16 rows
+  const uint32_t lane_off = 4 * (m * p.DV + tile * SSM_TILE + 16 * w + 4 * g), rows16 = 64 * p.DV;
   const float A = p.A[h];
 
   f32x4 S[NT];
@@ -54,7 +58,7 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK> &lds, int
     if (src) {
       if (!p.split) src += ((size_t)sg.n * p.H + h) * per_state;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(src + (size_t)(16 * t + m) * p.DV + lane_off);
+      for (int t = 0; t < NT; ++t) S[t] = ldg<f32x4>(src, lane_off + t * rows16);
     }
   }
 
@@ -63,10 +67,11 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK> &lds, int
   auto at = [&](int i) { return REV ? nch - 1 - i : i; };
   auto fetch = [&](int c) {
     const int L = min(CH, sg.len - c * CH);
-    sx.load(X + (size_t)c * CH * xp, xp, L);
-    sy.load(Y + (size_t)c * CH * yp, yp, L);
+    sx.load(X + c * (CH * xp), 2 * (uint32_t)xp, L);
+    sy.load(Y + c * (CH * yp), 2 * (uint32_t)yp, L);
   };
   double logd = 0.;
+  float sign = 1.f;  // of the accumulators
   auto gates = [&](int i) {  // one wave
     const int c = at(i), L = min(CH, sg.len - c * CH);
     const float raw = l < L ? raw_step(p, sg.row + (size_t)c * CH + l, h) : 0.f;
@@ -86,25 +91,26 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK> &lds, int
     if (STORE) {
       float *dst = (REV ? p.dstates : p.states) + ((size_t)chunk_id(p, sg, c) * p.H + h) * per_state;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(dst + (size_t)(16 * t + m) * p.DV + lane_off) = S[t];
+      for (int t = 0; t < NT; ++t) stg<f32x4>(dst, lane_off + t * rows16, sign * S[t]);
     }
+    sign = -sign;
     Split ysp[2];
     const float *coef = REV ? T.gam : T.ws;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float y[8];
-      unpack8(frag_tr(ay, 2 * YS, 32 * kb, 16 * w), y);
+      unpack8(frag_tr(ay, 2 * YS, 32 * kb, 16 * w, l), y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= coef[32 * kb + 8 * g + e];
+      for (int e = 0; e < 8; ++e) y[e] *= sign * coef[32 * kb + 8 * g + e];
       ysp[kb] = split3(y);
     }
     const float last = T.last;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      f32x4 acc = S[t] * last;
+      f32x4 acc = S[t] * -last;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const bf16x8 x = frag_tr(ax, 2 * XS, 32 * kb, 16 * t);
+        const bf16x8 x = frag_tr(ax, 2 * XS, 32 * kb, 16 * t, l);
 #pragma unroll
         for (int k = 2; k >= 0; --k) acc = mma32(acc, ysp[kb].p[k], x);
       }
@@ -122,7 +128,7 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK> &lds, int
   if (dst) {
     mfma_settle();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(dst + (size_t)(16 * t + m) * p.DV + lane_off) = S[t];
+    for (int t = 0; t < NT; ++t) stg<f32x4>(dst, lane_off + t * rows16, sign * S[t]);
   }
 }
 
@@ -206,7 +212,7 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
   const int seg = item / per, h = item % per / p.ntiles, tile = item % p.ntiles;
   Segment sg;
   if (!segment(p, seg, sg)) return;
-  const int w = wave_id(), l = lane_id(), g = l >> 4, m = l & 15;
+  const int w = wave_number(), l = lane_id(), g = l >> 4, m = l & 15;
   const int grp = h / (p.H / p.G);
   const bf16 *Q = p.q + (sg.row * p.G + grp) * DK, *K = p.k + (sg.row * p.G + grp) * DK;
   const size_t vo = (sg.row * p.H + h) * p.DV + tile * SSM_TILE;
@@ -224,15 +230,15 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[t][i] = src ? src[(size_t)prow(t, 4 * g + i) * p.DV + col] : 0.f;
+    for (int i = 0; i < 4; ++i) S[t][i] = src ? ldg<float>(src, 4 * (prow(t, 4 * g + i) * p.DV + col)) : 0.f;
 
   Stage<CH, DK, NTHR> sq, sk;
   Stage<CH, SSM_TILE, NTHR> sv;
   auto fetch = [&](int c) {
     const int L = min(CH, sg.len - c * CH);
-    sq.load(Q + (size_t)c * CH * kp, kp, L);
-    sk.load(K + (size_t)c * CH * kp, kp, L);
-    sv.load(V + (size_t)c * CH * vp, vp, L);
+    sq.load(Q + c * (CH * kp), 2 * (uint32_t)kp, L);
+    sk.load(K + c * (CH * kp), 2 * (uint32_t)kp, L);
+    sv.load(V + c * (CH * vp), 2 * (uint32_t)vp, L);
   };
   auto gates = [&](int c) {  // one wave
     const int L = min(CH, sg.len - c * CH);
@@ -267,11 +273,13 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
           for (int kb = 0; kb < KB; ++kb) acc = mma32(acc, frag_row(lk, LD::KS, 16 * jb + m, 32 * kb + 8 * g), qf[kb]);
         }
         mfma_settle();
+        const int j0 = 16 * jb + 4 * g;
+        const f32x4 gm = decay_ratios(T, j0, bhr, blr, -1.f), sj = lds4(T.s + j0);
         f32x4 pr;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int j = 16 * jb + 4 * g + i;
-          pr[i] = j <= r ? acc[i] * decay_ratio(bhr, blr, T.bh[j], T.bl[j]) * T.s[j] : 0.f;
+          const float x = computed(acc[i] * (gm[i] * sj[i]));
+          pr[i] = j0 + i <= r ? x : 0.f;
         }
         *reinterpret_cast<bf16x4 *>(lp + r * LD::PS + 16 * jb + 4 * g) = cvt_bf16x4(pr);
       }
@@ -282,7 +290,7 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
     // O^T tiles: rows the wave's 16 columns, column r
     bf16x8 vf[2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) vf[kb] = frag_tr(av, 2 * LD::VS, 32 * kb, 16 * w);
+    for (int kb = 0; kb < 2; ++kb) vf[kb] = frag_tr(av, 2 * LD::VS, 32 * kb, 16 * w, l);
     bf16x8 sf[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) sf[kb] = bfrag<bf16>(S[2 * kb], S[2 * kb + 1]);
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
       f32x4 o;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = a[i] + gam * b[i] + skip * (float)vr[i];
-      if (r < L) *reinterpret_cast<bf16x4 *>(O + ((size_t)c * CH + r) * vp + 16 * w + 4 * g) = cvt_bf16x4(o);
+      if (r < L) stg<bf16x4>(O + c * (CH * vp), 2 * (r * (uint32_t)vp + 16 * w + 4 * g), cvt_bf16x4(o));
     }
 
     // state update
@@ -334,7 +342,7 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[(size_t)prow(t, 4 * g + i) * p.DV + col] = S[t][i];
+      for (int i = 0; i < 4; ++i) stg<float>(dst, 4 * (prow(t, 4 * g + i) * p.DV + col), S[t][i]);
   }
 }
 
