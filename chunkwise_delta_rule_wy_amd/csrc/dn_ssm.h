@@ -39,6 +39,13 @@ namespace dn {
 
 constexpr int SSM_TILE = 64;  // Dv columns of a workgroup
 
+// A workgroup of the sweeps and the forward pass takes 64 columns, or twice 64
+// that share their keys: two column tiles of one head where Dv is a multiple
+// of 128, else tiles of two heads of one group where it has an even number.
+// Keys and queries are then loaded, and their fragments read from LDS, once for
+// both.
+enum SsmPair { SSM_SINGLE = 0, SSM_TILES = 1, SSM_HEADS = 2 };
+
 struct SsmParams {
   const bf16 *q, *k, *v, *dO;
   const float *dt, *A, *bias, *skip;  // bias, skip may be null
@@ -58,6 +65,7 @@ struct SsmParams {
   int64_t rows;              // B T
   int T, H, G, DV, N;
   int ntiles;                // Dv / 64
+  int pair;                  // columns of a workgroup: see SsmPair
   int split;                 // segments are joined through seg_state
   int NS, segc;              // segments of a sequence (not packed), chunks of a segment
   int NC;                    // chunks of a sequence (not packed)
@@ -119,7 +127,17 @@ __device__ __forceinline__ int chunk_id(const SsmParams &p, const Segment &s, in
   return (p.cu ? p.chunk_base[s.n] : s.n * p.NC) + s.chunk + c;
 }
 
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
+// e^x with the rounding of x log2(e) put back, which would cost |x| 2^-24
+__device__ __forceinline__ float exp_of(float x) {
+  const float t = x * wy::LOG2E, r = __builtin_fmaf(x, wy::LOG2E, -t) + x * 1.925963033e-8f;
+  return wy::fexp2(t) * __builtin_fmaf(r, 0.6931471806f, 1.f);
+}
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|); log1p(y) = y log(u) / (u - 1) with
+// u the rounded 1 + y, whose rounding the quotient takes back
+__device__ __forceinline__ float softplus(float x) {
+  const float y = exp_of(-fabsf(x)), u = 1.f + y, d = u - 1.f;
+  return fmaxf(x, 0.f) + (d == 0.f ? y : __logf(u) * (y * __builtin_amdgcn_rcpf(d)));
+}
 
 // the raw step size of one (token, head): dt + dt_bias
 __device__ __forceinline__ float raw_step(const SsmParams &p, size_t row, int h) {
@@ -170,12 +188,12 @@ __device__ __forceinline__ double lane_val_d(double v, int lane) {
 // Gate table of one (chunk, head): s, the log2 decays b = bh + bl (two floats
 // hold them to 2^-48), gamma, w, w s; `last` = gamma_63.
 struct GateTab {
-  alignas(16) float s[CH];
+  alignas(256) float s[CH];
   float bh[CH], bl[CH], gam[CH], w[CH], ws[CH];
   float last, pad[3];
 };
 // One wave fills the table from the raw step sizes of its lanes' tokens (lanes
-// from L on are padding: no decay, no input).  Returns the chunk's log2 decay.
+// from L on are padding: no decay, no input, gamma 0).  Returns the chunk's log2 decay.
 __device__ __forceinline__ double fill_gates(GateTab &t, float raw, float A, int L) {
   const int l = lane_id();
   const float s = l < L ? softplus(raw) : 0.f;
@@ -186,7 +204,7 @@ __device__ __forceinline__ double fill_gates(GateTab &t, float raw, float A, int
   t.s[l] = s;
   t.bh[l] = bh;
   t.bl[l] = bl;
-  t.gam[l] = wy::fexp2(bh) * (1.f + 0.6931471806f * bl);
+  t.gam[l] = l < L ? wy::fexp2(bh) * (1.f + 0.6931471806f * bl) : 0.f;
   t.w[l] = w;
   t.ws[l] = w * s;
   if (l == 0) {
@@ -206,7 +224,8 @@ __device__ __forceinline__ float computed(float x) {
 // A lane-dependent value that the compiler takes for a new one here: what is
 // computed from it is computed where it is used, instead of being held in
 // registers (or spilled) across a loop that needs them all.
-__device__ __forceinline__ int fresh(int x) {
+template <typename T>
+__device__ __forceinline__ T fresh(T x) {
   asm volatile("" : "+v"(x));
   return x;
 }
@@ -264,6 +283,51 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
+// An LDS matrix of COLS bf16 columns (64 or 128) without padding; the 16-byte
+// unit u of row r sits at unit position u ^ f(r).  With f below, 16 rows of one
+// unit (16-byte row reads), 32 lanes of half units (8-byte row reads) and the
+// four rows by two units of a transposed read all fall into different banks.
+template <int COLS>
+struct Swz {
+  static_assert(COLS == 64 || COLS == 128, "rows of 8 or 16 units");
+  static constexpr int RB = 2 * COLS;  // bytes of a row
+  __device__ static __forceinline__ int f(int r) {
+    return COLS == 128 ? ((r & 3) << 2 | ((r >> 2) & 3)) : ((r & 2) << 1 | ((r >> 2) & 3));
+  }
+  // byte offset of unit u of row r
+  __device__ static __forceinline__ uint32_t off(int r, int u) { return r * RB + ((u ^ f(r)) << 4); }
+  // A lane's address within a tile is one base XOR a constant of the column
+  // block plus an immediate offset of the row block (matrices start at multiples
+  // of 256 bytes, and f repeats every 16 rows).
+  //
+  // 32-index fragments of rows 16 t + m, columns 32 kb + 8 g .. + 7
+  __device__ static __forceinline__ uint32_t row_base(uint32_t base, int l) { return base + off(l & 15, l >> 4); }
+  __device__ static __forceinline__ bf16x8 row(uint32_t b, int t, int kb) {
+    return wy::ld<bf16x8>((b ^ (64 * kb)) + 16 * RB * t);
+  }
+  // four columns 16 c + 4 g .. + 3 of rows 16 t + m
+  __device__ static __forceinline__ uint32_t quad_base(uint32_t base, int l) {
+    return base + off(l & 15, l >> 5) + 8 * ((l >> 4) & 1);
+  }
+  __device__ static __forceinline__ uint32_t quad(uint32_t b, int t, int c) { return (b ^ (32 * c)) + 16 * RB * t; }
+  // rows 16 t + m, columns 32 kb + 4 g .. + 3 and 32 kb + 16 + 4 g .. + 3: the
+  // order of two stacked accumulator tiles
+  __device__ static __forceinline__ bf16x8 row_stacked(uint32_t quad_b, int t, int kb) {
+    return wy::cat(wy::ld<bf16x4>(quad(quad_b, t, 2 * kb)), wy::ld<bf16x4>(quad(quad_b, t, 2 * kb + 1)));
+  }
+  // transposed: columns 16 c + m, contraction over the rows 32 kb + 8 g .. + 7
+  struct Col {
+    uint32_t a, b;
+  };
+  __device__ static __forceinline__ Col col_base(uint32_t base, int l) {
+    const int r = 8 * (l >> 4) + ((l >> 2) & 3), q = l & 3;
+    return {base + off(r, q >> 1) + 8 * (q & 1), base + off(r + 4, q >> 1) + 8 * (q & 1)};
+  }
+  __device__ static __forceinline__ bf16x8 col(const Col &x, int kb, int c) {
+    return wy::cat(wy::ld_tr((x.a ^ (32 * c)) + 32 * RB * kb), wy::ld_tr((x.b ^ (32 * c)) + 32 * RB * kb));
+  }
+};
+
 // 32-index operand fragment whose rows are the matrix's columns: 16 columns
 // c0 .. of an LDS matrix with `stride` bytes per row, contraction index = its
 // rows r0 + 8 g .. r0 + 8 g + 7 (lane group g)
@@ -291,21 +355,35 @@ template <int ROWS, int COLS, int THR>
 struct Stage {
   static constexpr int UPR = COLS / 8, NU = ROWS * UPR / THR, RSTEP = THR / UPR;
   static_assert(ROWS * UPR % THR == 0 && THR % UPR == 0, "whole units and rows per thread");
-  u128 u[NU];
+  u32x4 u[NU];
   // rows of `pitch` bytes; base points at the tile's first element
   __device__ __forceinline__ void load(const bf16 *base, uint32_t pitch, int L) {
     const int r0 = threadIdx.x / UPR, c = threadIdx.x % UPR;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int r = r0 + RSTEP * i;
-      u[i] = r < L ? ldg<u128>(base, r * pitch + 16 * c) : zero128();
+      u[i] = r < L ? ldg<u32x4>(base, r * pitch + 16 * c) : (u32x4)0u;
     }
+  }
+  // the same, but rows from L on repeat row L - 1: for tiles whose coefficients
+  // are zero there
+  __device__ __forceinline__ void load_clamped(const bf16 *base, uint32_t pitch, int L, uint32_t tid) {
+    const uint32_t first = (tid / UPR) * pitch, last = (L - 1) * pitch, c = 16 * (tid % UPR);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) u[i] = ldg<u32x4>(base, min(first + i * (RSTEP * pitch), last) + c);
+  }
+  // into columns c0 .. of a swizzled matrix of WIDTH columns
+  template <int WIDTH>
+  __device__ __forceinline__ void store_swz(uint32_t lds, uint32_t tid, int c0 = 0) const {
+    const int r0 = tid / UPR, c = tid % UPR;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) wy::st(lds + Swz<WIDTH>::off(r0 + RSTEP * i, c0 / 8 + c), u[i]);
   }
   template <int STRIDE>
   __device__ __forceinline__ void store(bf16 *lds) const {
     const int r0 = threadIdx.x / UPR, c = threadIdx.x % UPR;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) *reinterpret_cast<u128 *>(lds + (r0 + RSTEP * i) * STRIDE + 8 * c) = u[i];
+    for (int i = 0; i < NU; ++i) *reinterpret_cast<u32x4 *>(lds + (r0 + RSTEP * i) * STRIDE + 8 * c) = u[i];
   }
 };
 

@@ -39,6 +39,11 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
 // Packed: the lengths are not known on the host, and one long sequence among
 // short ones would set the pass's time, so that packs are always cut, into
 // segments of a length that gives about 1024 workgroups over all tokens.
+int pair_of(const dn_ssm_shape *s) {
+  if (s->Dv % 128 == 0) return dn::SSM_TILES;
+  return (s->H / s->G) % 2 == 0 ? dn::SSM_HEADS : dn::SSM_SINGLE;
+}
+
 struct Plan {
   int split, NS, segc, NC;
   int64_t nseg, nchunks;
@@ -46,7 +51,7 @@ struct Plan {
 
 Plan plan_of(const dn_ssm_shape *s, bool packed) {
   Plan p = {};
-  const int64_t tiles = (int64_t)s->H * (s->Dv / 64), chunks = ((int64_t)s->T + 63) / 64;
+  const int64_t tiles = (int64_t)s->H * (s->Dv / 64) / (pair_of(s) == dn::SSM_SINGLE ? 1 : 2), chunks = ((int64_t)s->T + 63) / 64;
   p.NC = (int)chunks;
   if (packed) {
     const int64_t want = (chunks * tiles + 1023) / 1024;
@@ -150,6 +155,7 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
   p.DV = s->Dv;
   p.N = s->n_seqs;
   p.ntiles = s->Dv / 64;
+  p.pair = pair_of(s);
   p.split = pl.split;
   p.NS = pl.NS;
   p.segc = pl.segc;

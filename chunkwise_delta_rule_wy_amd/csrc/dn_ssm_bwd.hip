@@ -106,9 +106,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     sv.load(p.v + off, pitch, L);
     so.load(p.dO + off, pitch, L);
 #pragma unroll
-    for (auto &u : so.u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u.w[i] ^= flip;
+    for (auto &u : so.u) u ^= flip;
   };
   auto fetch_states = [&](int h, int tile) {
     const size_t at = ((size_t)chunk * p.H + h) * DK * p.DV + tile * SSM_TILE;
