@@ -607,22 +607,27 @@ def _adr(t: Optional[torch.Tensor]):
 
 
 def _call(name, dev, *args):
-    """Call a library function on ``dev``'s current stream, with ``dev`` as
-    the current device (kernels start on the current device)."""
+    """Call a library function on ``dev``'s (a device or its index) current
+    stream, with it as the current device (kernels start on the current device)."""
     fn = getattr(_lib or load_library(), name)
-    if torch._C._cuda_getDevice() == dev.index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    i = dev if type(dev) is int else dev.index
+    if torch._C._cuda_getDevice() == i:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(i):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     if status:
         _check(name, status)
 
 
+def _fits(t, dtype, shape, i):
+    """Whether a tensor is a contiguous one of this type and shape on GPU i."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == i and t.is_contiguous()
+
+
 def _is(t, name, dtype, shape, dev):
     """``_need`` with a quick way through for a tensor that is right."""
-    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-                     and t.is_contiguous()):
+    if t is None or (isinstance(t, torch.Tensor) and _fits(t, dtype, shape, dev.index)):
         return
     _need(t, name, dtype, shape, dev)
 
@@ -721,13 +726,22 @@ def ssm_step(q, k, v, dt, A, dt_bias, skip, state):
     """One token of every sequence (``dn_ssm_step``): q, k ``[B,G,Dk]``, v
     ``[B,H,Dv]`` (float32 or bfloat16, one dtype), dt ``[B,H]`` float32, state
     ``[B,H,Dk,Dv]`` float32 updated in place.  Returns o ``[B,H,Dv]``."""
-    dev, (B,), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, tuple(_DTYPES), 3)
-    if state is None:
-        raise TypeError("state is required")
-    _is(state, "state", torch.float32, (B, H, Dk, Dv), dev)
+    E, i, f32 = v.dtype, v.get_device(), torch.float32
+    qs, vs = q.shape, v.shape
+    H = vs[-2] if len(vs) == 3 else 0
+    # the usual call in one expression; anything else goes through the checks that say what is wrong
+    if not (H and len(qs) == 3 and qs[0] == vs[0] and qs[1] and H % qs[1] == 0 and E in _DTYPES and i >= 0
+            and v.is_contiguous() and _fits(q, E, qs, i) and _fits(k, E, qs, i) and _fits(dt, f32, vs[:2], i)
+            and _fits(A, f32, (H,), i) and (dt_bias is None or _fits(dt_bias, f32, (H,), i))
+            and (skip is None or _fits(skip, f32, (H,), i))
+            and _fits(state, f32, (vs[0], H, qs[2], vs[2]), i)):
+        dev, (B,), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, tuple(_DTYPES), 3)
+        if state is None:
+            raise TypeError("state is required")
+        _is(state, "state", torch.float32, (B, H, Dk, Dv), dev)
     o = torch.empty_like(v)
-    _call("dn_ssm_step", dev, B, H, G, Dk, Dv, _DTYPES[v.dtype], _adr(q), _adr(k), _adr(v), _adr(dt), _adr(A),
-          _adr(dt_bias), _adr(skip), _adr(state), _adr(o))
+    _call("dn_ssm_step", i, vs[0], H, qs[1], qs[2], vs[2], _DTYPES[E], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          dt.data_ptr(), A.data_ptr(), _adr(dt_bias), _adr(skip), state.data_ptr(), o.data_ptr())
     return o
 
 
@@ -784,11 +798,17 @@ def conv_silu_step(x, w, bias, state):
     """One token of every sequence (``dn_conv_silu_step``): x ``[B,H,D]``, state
     ``[B,W-1,H,D]`` (x's dtype) holding the last W - 1 inputs, updated in
     place.  Returns y ``[B,H,D]``."""
-    if state is None:
-        raise TypeError("state is required")
-    dev, (B,), H, D, W, _ = _conv_silu_args(x, w, bias, state, None, 3)
+    E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
+    if not (len(xs) == 3 and len(ws) == 3 and ws[:2] == xs[1:] and ws[2] and E in _DTYPES and i >= 0
+            and x.is_contiguous() and _fits(w, torch.float32, ws, i)
+            and (bias is None or _fits(bias, torch.float32, ws[:2], i))
+            and state is not None and _fits(state, E, (xs[0], ws[2] - 1, xs[1], xs[2]), i)):
+        if state is None:
+            raise TypeError("state is required")
+        _conv_silu_args(x, w, bias, state, None, 3)
     y = torch.empty_like(x)
-    _call("dn_conv_silu_step", dev, B, H, D, W, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(state), _adr(y))
+    _call("dn_conv_silu_step", i, xs[0], xs[1], xs[2], ws[2], _DTYPES[E], x.data_ptr(), w.data_ptr(), _adr(bias),
+          state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -813,10 +833,14 @@ def gated_norm(x, z, w, eps: float = 1e-5, gate_first: bool = False):
     of ``x silu(z)`` times w.  x, z ``[..., D]`` or ``[..., H, D]`` float32 or
     bfloat16; w float32 ``[D]``, or ``[H, D]`` for a weight per head.  Returns y
     in x's dtype."""
-    dev, rows, D, R = _gated_norm_args(x, z, w)
+    E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
+    R = ws[0] if len(ws) == 2 else 1
+    if not (len(xs) > 1 and xs[-1] and ws == xs[-len(ws):] and 0 < len(ws) < 3 and E in _DTYPES and i >= 0
+            and x.is_contiguous() and _fits(z, E, xs, i) and _fits(w, torch.float32, ws, i)):
+        _gated_norm_args(x, z, w)
     y = torch.empty_like(x)
-    _call("dn_gated_norm", dev, rows, D, R, _DTYPES[x.dtype], _adr(x), _adr(z), _adr(w), float(eps), int(gate_first),
-          _adr(y))
+    _call("dn_gated_norm", i, x.numel() // (xs[-1] or 1), xs[-1], R, _DTYPES[E], x.data_ptr(), z.data_ptr(), w.data_ptr(),
+          eps, gate_first, y.data_ptr())
     return y
 
 

@@ -51,7 +51,7 @@ struct SsmParams {
   const float *dt, *A, *bias, *skip;  // bias, skip may be null
   const float *h0, *dhT;              // may be null
   const int32_t *cu;                  // packed sequences, or null
-  const int32_t *seg_base, *seg_seq;      // packed: segment table
+  const int32_t *seg_base, *seg_seq;      // packed and cut: segment table
   const int32_t *chunk_base, *chunk_seq;  // packed: chunk table (backward)
   bf16 *o;
   float *hT;                 // may be null
@@ -95,7 +95,9 @@ __device__ __forceinline__ int xcd_item(int x, int total) {
   return xcd * q + min(xcd, r) + (x >> 3);
 }
 
-// A segment: sequence n, first token row, tokens, place in the sequence.
+// A segment: sequence n, first token row, tokens, place in the sequence.  Where
+// sequences are not cut, every sequence is one segment, also one without
+// tokens.
 struct Segment {
   int n, len, chunk;  // chunk: its first chunk within the sequence
   size_t row;
@@ -104,9 +106,9 @@ struct Segment {
 __device__ __forceinline__ bool segment(const SsmParams &p, int seg, Segment &s) {
   int start, len;
   if (p.cu) {
-    s.n = p.seg_seq[seg];
+    s.n = p.split ? p.seg_seq[seg] : seg;
     if (s.n < 0) return false;
-    const int i = seg - p.seg_base[s.n], t0 = p.cu[s.n];
+    const int i = p.split ? seg - p.seg_base[s.n] : 0, t0 = p.cu[s.n];
     len = p.cu[s.n + 1] - t0;
     s.chunk = i * p.segc;
     start = s.chunk * CH;

@@ -31,44 +31,51 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
 
 // Segments (whole chunks of one sequence) and their tables.
 //
-// Fixed length: the sequences are cut only where the sequences, heads and
-// column tiles alone would leave the device's 256 CUs without two workgroups
-// each, and not below four chunks a segment (a segment costs a sweep over its
-// tokens and a pass over its state).  Measured at 16384 tokens, 16 heads,
-// 128 x 128: see dn_ssm_fwd.hip.
+// A segment costs a sweep over its tokens and passes over its state, so that
+// sequences are cut only where they would leave compute units idle.
+// Up to UNCUT chunks nothing is cut: the chunks' chain is then no longer than
+// the three passes that cutting needs (1357 tokens in 9 sequences, 6 heads,
+// 64 x 128, forwards and backwards: 68 us, cut into segments of 4 chunks 90 us).
+// Fixed length: no cuts from FULL_WGS workgroups on, else about FIXED_WGS, two
+// for each of the 256 CUs, and not below four chunks a segment (16384 tokens,
+// 16 heads, 128 x 128: 124 us, with 384 workgroups 134 us, 1024: 157 us).
 // Packed: the lengths are not known on the host, and one long sequence among
-// short ones would set the pass's time, so that packs are always cut, into
-// segments of a length that gives about 1024 workgroups over all tokens.
+// short ones would set the pass's time, so that longer packs are always cut, so
+// finely that the workgroups' rounds come out even (65536 tokens, 32 heads,
+// 128 x 128: 789 us with PACKED_WGS 2048, 806 us with 1024, 846 us with 4096).
 int pair_of(const dn_ssm_shape *s) {
   if (s->Dv % 128 == 0) return dn::SSM_TILES;
   return (s->H / s->G) % 2 == 0 ? dn::SSM_HEADS : dn::SSM_SINGLE;
 }
+
+constexpr int64_t UNCUT = 32, FULL_WGS = 384, FIXED_WGS = 512, PACKED_WGS = 2048;
 
 struct Plan {
   int split, NS, segc, NC;
   int64_t nseg, nchunks;
 };
 
-Plan plan_of(const dn_ssm_shape *s, bool packed) {
+Plan plan_of(const dn_ssm_shape *s, bool packed, bool backward) {
   Plan p = {};
   const int64_t tiles = (int64_t)s->H * (s->Dv / 64) / (pair_of(s) == dn::SSM_SINGLE ? 1 : 2), chunks = ((int64_t)s->T + 63) / 64;
   p.NC = (int)chunks;
   if (packed) {
-    const int64_t want = (chunks * tiles + 1023) / 1024;
+    const int64_t want = (chunks * tiles + PACKED_WGS - 1) / PACKED_WGS;
     p.segc = (int)(want < 4 ? 4 : want > 1 << 20 ? 1 << 20 : want);
-    p.split = 1;
-    p.nseg = (int64_t)s->T / (64 * (int64_t)p.segc) + s->n_seqs;
+    if (chunks <= UNCUT) p.segc = (int)(chunks < 1 ? 1 : chunks);
+    p.split = p.segc < chunks;
+    p.nseg = (p.split ? (int64_t)s->T / (64 * (int64_t)p.segc) : 0) + s->n_seqs;
     p.nchunks = (int64_t)s->T / 64 + s->n_seqs;
     return p;
   }
-  const int64_t streams = tiles * s->n_seqs;
-  int64_t ns = streams >= 384 ? 1 : (512 + streams - 1) / streams;
+  const int64_t streams = tiles * s->n_seqs * (backward ? 2 : 1);  // the backward pass sweeps both ways at once
+  int64_t ns = streams >= FULL_WGS || chunks <= UNCUT ? 1 : (FIXED_WGS + streams - 1) / streams;
   if (ns > chunks / 4) ns = chunks / 4;
   if (ns < 1) ns = 1;
   p.segc = (int)((chunks + ns - 1) / ns);
   if (p.segc < 1) p.segc = 1;
-  p.NS = (int)((chunks + p.segc - 1) / p.segc);
-  p.split = p.NS != 1;  // a sequence without tokens has no segment: its state passes through the join
+  p.NS = chunks > 0 ? (int)((chunks + p.segc - 1) / p.segc) : 1;
+  p.split = p.NS > 1;
   p.nseg = (int64_t)p.NS * s->n_seqs;
   p.nchunks = chunks * s->n_seqs;
   return p;
@@ -98,7 +105,8 @@ Layout layout_of(const dn_ssm_shape *s, const Plan &pl, bool packed, bool backwa
   };
   const size_t st = (size_t)s->H * s->Dk * s->Dv * 4;
   if (packed)
-    L.tables = take(4 * ((size_t)s->n_seqs + 1 + pl.nseg + (backward ? (size_t)s->n_seqs + 1 + pl.nchunks : 0)));
+    L.tables = take(4 * ((pl.split ? (size_t)s->n_seqs + 1 + pl.nseg : 0) +
+                         (backward ? (size_t)s->n_seqs + 1 + pl.nchunks : 0)));
   if (pl.split) {
     L.decay = take(8 * (size_t)pl.nseg * s->H);
     for (int i = 0; i < (backward ? 2 : 1); ++i) L.seg[i] = take((size_t)pl.nseg * st);
@@ -125,9 +133,9 @@ size_t workspace(const dn_ssm_shape *s, bool backward) {
   if (!s || s->B <= 0 || s->T < 0 || s->n_seqs <= 0) return 0;
   if (check_dims(s->H, s->G, s->Dk, s->Dv, s->dtype) != DN_OK) return 0;
   size_t n = 0;
-  if (s->n_seqs == s->B) n = layout_of(s, plan_of(s, false), false, backward).total;
+  if (s->n_seqs == s->B) n = layout_of(s, plan_of(s, false, backward), false, backward).total;
   if (s->B == 1) {
-    const size_t m = layout_of(s, plan_of(s, true), true, backward).total;
+    const size_t m = layout_of(s, plan_of(s, true, backward), true, backward).total;
     if (m > n) n = m;
   }
   return n;
@@ -138,7 +146,7 @@ size_t workspace(const dn_ssm_shape *s, bool backward) {
 dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *ws, size_t ws_bytes, dn::SsmParams &p,
                 hipStream_t stream) {
   const bool packed = cu != nullptr;
-  const Plan pl = plan_of(s, packed);
+  const Plan pl = plan_of(s, packed, backward);
   const int64_t top = INT32_MAX;
   sets_of(s, pl, p.sets, p.set_heads);
   if (pl.nseg * s->H * (s->Dv / 64) > top || pl.nchunks * s->H > top || pl.nchunks * s->G * p.sets > top ||
@@ -177,12 +185,14 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
   }
   if (packed) {
     int32_t *t = reinterpret_cast<int32_t *>(base + L.tables);
-    p.seg_base = t;
-    p.seg_seq = t + s->n_seqs + 1;
-    if (dn::launch_chunk_table(cu, s->n_seqs, t, t + s->n_seqs + 1, p.nseg, 64 * p.segc, stream) != hipSuccess)
-      return DN_EHIP;
-    if (backward) {
+    if (pl.split) {
+      p.seg_base = t;
+      p.seg_seq = t + s->n_seqs + 1;
+      if (dn::launch_chunk_table(cu, s->n_seqs, t, t + s->n_seqs + 1, p.nseg, 64 * p.segc, stream) != hipSuccess)
+        return DN_EHIP;
       t += s->n_seqs + 1 + pl.nseg;
+    }
+    if (backward) {
       p.chunk_base = t;
       p.chunk_seq = t + s->n_seqs + 1;
       if (dn::launch_chunk_table(cu, s->n_seqs, t, t + s->n_seqs + 1, p.nchunks, 64, stream) != hipSuccess)

@@ -109,10 +109,10 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
     return l < min(CH, sg.len - c * CH) ? raw_step(p, sg.row + (size_t)c * CH + l, gh) : 0.f;
   };
   auto gates = [&](int i, float raw) { logd += fill_gates(lds.tabs[i & 1][w], raw, A, min(CH, sg.len - at(i) * CH)); };
-  fetch(at(0));
+  if (nch > 0) fetch(at(0));
   float sign = 1.f;  // of the accumulators
   float raw = 0.f;
-  if (w < TABS) {
+  if (w < TABS && nch > 0) {
     gates(0, load_raw(0));
     if (nch > 1) raw = load_raw(1);
   }
@@ -189,7 +189,8 @@ __global__ __launch_bounds__(Work<PAIR>::THREADS, 4) void ssm_sweep_kernel(SsmPa
 //
 // Start states of a sequence's segments from their own end states and decays,
 // in place, four state elements per thread; a sequence without tokens hands
-// its initial state on.  Bound by the segment states' traffic.
+// its initial state on.  Bound by the segment states' traffic, of which four
+// segments are on their way at a time.
 constexpr int JOIN_THREADS = 256;
 
 __global__ __launch_bounds__(JOIN_THREADS) void ssm_join_kernel(SsmParams p, int dk) {
@@ -210,17 +211,29 @@ __global__ __launch_bounds__(JOIN_THREADS) void ssm_join_kernel(SsmParams p, int
   const float *init = rev ? p.dhT : p.h0;
   f32x4 cur = init ? *reinterpret_cast<const f32x4 *>(init + (size_t)nh * per + e) : zero4();
   float *st = p.seg_state[rev];
-  for (int i = 0; i < cnt; ++i) {
-    const size_t at = (size_t)(rev ? s0 + cnt - 1 - i : s0 + i) * p.H + h;
-    f32x4 *x = reinterpret_cast<f32x4 *>(st + at * per + e);
-    if (i + 1 == cnt) {  // no sweep has filled this one
-      *x = cur;
-      break;
+  constexpr int AHEAD = 4;
+  for (int i = 0; i < cnt; i += AHEAD) {
+    f32x4 *x[AHEAD], own[AHEAD];
+    double d[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int j = min(i + k, cnt - 1);
+      const size_t at = (size_t)(rev ? s0 + cnt - 1 - j : s0 + j) * p.H + h;
+      x[k] = reinterpret_cast<f32x4 *>(st + at * per + e);
+      if (i + k + 1 < cnt) {  // no sweep has filled the last one
+        own[k] = *x[k];
+        d[k] = p.seg_decay[at];
+      } else {
+        own[k] = zero4();
+        d[k] = 0.;
+      }
     }
-    const f32x4 own = *x;
-    *x = cur;
-    const float d = (float)exp2(p.seg_decay[at]);
-    cur = cur * d + own;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (i + k >= cnt) break;
+      *x[k] = cur;
+      cur = cur * (float)exp2(d[k]) + own[k];
+    }
   }
   float *out = rev ? p.dh0 : p.hT;
   if (cnt == 0 && out) *reinterpret_cast<f32x4 *>(out + (size_t)nh * per + e) = cur;
@@ -298,9 +311,9 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
     return l < min(CH, sg.len - c * CH) ? raw_step(p, sg.row + (size_t)c * CH + l, gh) : 0.f;
   };
   auto gates = [&](int c, float raw) { fill_gates(lds.tabs[c & 1][w], raw, A, min(CH, sg.len - c * CH)); };
-  fetch(0);
+  if (nch > 0) fetch(0);
   float raw = 0.f;
-  if (w < TABS) {
+  if (w < TABS && nch > 0) {
     gates(0, load_raw(0));
     if (nch > 1) raw = load_raw(1);
   }
