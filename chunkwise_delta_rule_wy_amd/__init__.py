@@ -770,7 +770,7 @@ def conv_silu(x, w, bias=None, s0=None, cu_seqlens=None):
     state of ``conv_silu_step``."""
     dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
     y = torch.empty_like(x)
-    sT = torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev)
+    sT = x.new_empty((N, max(W - 1, 0), H, D)) if s0 is None else torch.empty_like(s0)
     _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(s0),
           _adr(cu_seqlens), _adr(y), _adr(sT))
     return y, sT

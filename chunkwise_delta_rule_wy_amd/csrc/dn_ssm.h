@@ -298,14 +298,15 @@ struct Swz {
   }
   // byte offset of unit u of row r
   __device__ static __forceinline__ uint32_t off(int r, int u) { return r * RB + ((u ^ f(r)) << 4); }
+  // `o`: a constant to add, for matrices that share a base.
   // A lane's address within a tile is one base XOR a constant of the column
   // block plus an immediate offset of the row block (matrices start at multiples
   // of 256 bytes, and f repeats every 16 rows).
   //
   // 32-index fragments of rows 16 t + m, columns 32 kb + 8 g .. + 7
   __device__ static __forceinline__ uint32_t row_base(uint32_t base, int l) { return base + off(l & 15, l >> 4); }
-  __device__ static __forceinline__ bf16x8 row(uint32_t b, int t, int kb) {
-    return wy::ld<bf16x8>((b ^ (64 * kb)) + 16 * RB * t);
+  __device__ static __forceinline__ bf16x8 row(uint32_t b, int t, int kb, uint32_t o = 0) {
+    return wy::ld<bf16x8>((b ^ (64 * kb)) + 16 * RB * t + o);
   }
   // four columns 16 c + 4 g .. + 3 of rows 16 t + m
   __device__ static __forceinline__ uint32_t quad_base(uint32_t base, int l) {
@@ -325,8 +326,8 @@ struct Swz {
     const int r = 8 * (l >> 4) + ((l >> 2) & 3), q = l & 3;
     return {base + off(r, q >> 1) + 8 * (q & 1), base + off(r + 4, q >> 1) + 8 * (q & 1)};
   }
-  __device__ static __forceinline__ bf16x8 col(const Col &x, int kb, int c) {
-    return wy::cat(wy::ld_tr((x.a ^ (32 * c)) + 32 * RB * kb), wy::ld_tr((x.b ^ (32 * c)) + 32 * RB * kb));
+  __device__ static __forceinline__ bf16x8 col(const Col &x, int kb, int c, uint32_t o = 0) {
+    return wy::cat(wy::ld_tr((x.a ^ (32 * c)) + 32 * RB * kb + o), wy::ld_tr((x.b ^ (32 * c)) + 32 * RB * kb + o));
   }
 };
 

@@ -29,6 +29,13 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
   return DN_OK;
 }
 
+// Two column tiles share a workgroup where Dv has them, else two heads that
+// share their keys (SsmPair).
+int pair_of(const dn_ssm_shape *s) {
+  if (s->Dv % 128 == 0) return dn::SSM_TILES;
+  return (s->H / s->G) % 2 == 0 ? dn::SSM_HEADS : dn::SSM_SINGLE;
+}
+
 // Segments (whole chunks of one sequence) and their tables.
 //
 // A segment costs a sweep over its tokens and passes over its state, so that
@@ -43,11 +50,6 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
 // short ones would set the pass's time, so that longer packs are always cut, so
 // finely that the workgroups' rounds come out even (65536 tokens, 32 heads,
 // 128 x 128: 789 us with PACKED_WGS 2048, 806 us with 1024, 846 us with 4096).
-int pair_of(const dn_ssm_shape *s) {
-  if (s->Dv % 128 == 0) return dn::SSM_TILES;
-  return (s->H / s->G) % 2 == 0 ? dn::SSM_HEADS : dn::SSM_SINGLE;
-}
-
 constexpr int64_t UNCUT = 32, FULL_WGS = 384, FIXED_WGS = 512, PACKED_WGS = 2048;
 
 struct Plan {
@@ -81,11 +83,13 @@ Plan plan_of(const dn_ssm_shape *s, bool packed, bool backward) {
   return p;
 }
 
-// Sets of a group's heads for the gradient kernel: about four workgroups per
-// CU, as even as the heads allow.
+// Sets of a group's heads for the gradient kernel: one workgroup per CU where
+// the heads give as many, since every set costs a start and a share of fp32
+// partial sums (4 x 4096 tokens, 32 heads: 285 us with one set, 330 us with
+// four, their sums included).
 void sets_of(const dn_ssm_shape *s, const Plan &pl, int &sets, int &heads) {
   const int64_t R = s->H / s->G, wgs = pl.nchunks * s->G;
-  int64_t n = wgs > 0 ? (1024 + wgs - 1) / wgs : 1;
+  int64_t n = wgs > 0 ? (256 + wgs - 1) / wgs : 1;
   if (n > R) n = R;
   heads = (int)((R + n - 1) / n);
   sets = (int)((R + heads - 1) / heads);

@@ -41,7 +41,7 @@ struct GradLds {
   alignas(16) bf16 dO[CH * VS];
   alignas(16) bf16 dh[DK * VS];  // dh rounded, for K dh; at the end dG^T
   alignas(16) bf16 p[CH * VS];   // the head's P^T, zero above the diagonal blocks
-  GateTab tabs[2];               // by the head's parity
+  GateTab tabs[3];               // of a head and its neighbours
   struct Sums {
     double hd[8];
     float pairs[4][CH], col_e[2][CH], diag_e[CH], qd[NT][CH], kd[NT][CH], diag[4];
@@ -118,14 +118,15 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
         dr[kb][x] = sign * ldg<f32x4>(p.dstates + at, state_off + 128 * kb + 16 * x);
       }
   };
-  auto gates = [&](int hh) {  // one wave
-    const int h = h_first + hh;
-    fill_gates(s.tabs[hh & 1], l < L ? raw_step(p, row0 + l, h) : 0.f, p.A[h], L);
-  };
+  // one wave fills the gate tables; the raw steps are loaded a head ahead and
+  // before the head's other loads, for which the wave would else have to wait
+  float raw = 0.f;
+  auto load_raw = [&](int hh) { raw = l < L ? raw_step(p, row0 + l, h_first + min(hh, heads - 1)) : 0.f; };
+  auto gates = [&](int hh) { fill_gates(s.tabs[hh % 3], raw, p.A[h_first + hh], L); };
   // the head's sums over the waves and its scalar gradients, by one wave
   auto finish = [&](int hh) {
     const int h = h_first + hh;
-    const GateTab &T = s.tabs[hh & 1];
+    const GateTab &T = s.tabs[hh % 3];
     const typename LD::Sums &x = s.sums[hh & 1];
     float pairs = 0.f, qd = 0.f, kd = 0.f;
     double hd = 0.;
@@ -156,9 +157,13 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     }
   };
 
+  if (w == 2) {
+    load_raw(0);
+    gates(0);
+    load_raw(1);
+  }
   fetch_rows(h_first, 0);
   fetch_states(h_first, 0);
-  if (w == 3) gates(0);
   __syncthreads();
 
   // G: tiles of rows r (four per lane), column j
@@ -179,7 +184,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h_first + hh;
-    const GateTab &T = s.tabs[hh & 1];
+    const GateTab &T = s.tabs[hh % 3];
     typename LD::Sums &sums = s.sums[hh & 1];
     f32x4 M[2];
     M[0] = M[1] = zero4();
@@ -221,6 +226,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
         }
       }
       __syncthreads();
+      if (tile == 0 && w == 2 && hh + 1 < heads) {
+        gates(hh + 1);
+        load_raw(hh + 2);
+      }
       fetch_rows(nh, nt);
       // h dO^T, then dh V^T: the wave's 16 Dk rows.  The states' registers are
       // free after that for the next ones, which arrive during the rest.
@@ -301,9 +310,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
           stg<bf16x4>(p.dv + (row0 * p.H + h) * p.DV + tile * SSM_TILE, 2 * (j * (p.H * p.DV) + c), cvt_bf16x4(o));
         }
       }
-      if (tile == 0 && w == 3) {  // this wave has no blocks of M below
-        if (hh > 0) finish(hh - 1);
-        if (hh + 1 < heads) gates(hh + 1);
+      if (tile == 0) {  // by waves without blocks of M
+        if (w == 3 && hh > 0) finish(hh - 1);
       }
     }
     // the head's sums over the 64 x 64 matrices; `below` sums a column's rows

@@ -60,8 +60,11 @@ SHAPES = [
     (2, 64, 4, 2, 128, 64, None, True),
     (1, 65, 3, 1, 64, 192, None, True),
     (3, 130, 4, 1, 128, 128, None, False),
-    (1, 577, 2, 1, 128, 64, None, True),   # few streams: cut into segments
+    (1, 577, 2, 1, 128, 64, None, True),
     (2, 512, 1, 1, 64, 64, None, True),
+    (1, 2117, 2, 1, 64, 64, None, True),   # more than 32 chunks and few streams: cut into segments
+    (1, 2112, 1, 1, 128, 64, None, False),
+    (1, 2300, 2, 2, 64, 64, [0, 2200, 37, 0, 63, 0], True),
     (1, 300, 4, 2, 64, 64, [0, 1, 63, 64, 0, 65, 107, 0], True),
     (1, 700, 2, 1, 128, 128, [1, 1, 600, 98], False),
     (1, 5, 6, 3, 64, 64, [0, 0, 5], True),

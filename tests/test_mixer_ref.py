@@ -128,10 +128,11 @@ def test_scan_refuses_pointers_and_workspaces(lib):
     assert need >= 2 * 4 * 4 * 64 * 64 * 4
     assert ssm_bwd(lib, s, wsb=need - 1) == ENOWS and ssm_bwd(lib, s, ws=None) == ENOWS
     assert ssm_bwd(lib, s, ws=FAKE + 8) == ENOWS
-    packed = ssm_shape(B=1, n_seqs=5)
+    packed = ssm_shape(B=1, T=4096, n_seqs=5)  # cut into segments, whose states take memory
     need = lib.dn_ssm_fwd_workspace(ctypes.byref(packed))
     assert need > 0 and ssm_fwd(lib, packed, cu=FAKE, wsb=need - 1) == ENOWS
-    assert lib.dn_ssm_fwd_workspace(ctypes.byref(ssm_shape(H=400, G=400))) == 0  # streams enough: not cut
+    assert lib.dn_ssm_fwd_workspace(ctypes.byref(ssm_shape(T=10 ** 5, H=400, G=400))) == 0  # streams enough: not cut
+    assert lib.dn_ssm_fwd_workspace(ctypes.byref(ssm_shape(B=1, T=2048, n_seqs=9))) == 0  # 32 chunks: not cut
 
 
 @pytest.mark.parametrize("H,G,Dk,Dv,dtype,state,code", [
