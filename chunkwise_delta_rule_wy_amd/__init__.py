@@ -602,6 +602,9 @@ def short_conv_fn(x, w, cu_seqlens=None, l2norm=False):
 # below pass raw addresses, test a tensor in one expression (the slow path
 # words the error) and ask for the device and its stream without their objects.
 
+_MAX_SIZE = 2 ** 31 - 1  # the library's sizes are 32-bit
+
+
 def _adr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -633,13 +636,22 @@ def _is(t, name, dtype, shape, dev):
 
 
 def _gpu(t, name, dims, dtypes):
+    """The device of a required tensor of these numbers of dimensions and types."""
     if not isinstance(t, torch.Tensor) or t.dim() not in dims:
         raise ValueError("%s must be a tensor of %s dimensions" % (name, " or ".join(str(d) for d in dims)))
     if t.dtype not in dtypes:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
     if t.device.type != "cuda":
         raise ValueError("tensors must be on a GPU")
+    if any(n > _MAX_SIZE for n in t.shape):
+        raise ValueError("%s has a size of 2^31 or more" % name)
     return t.device
+
+
+def _given(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise TypeError("%s is required" % name)
 
 
 def _seqs(B, cu_seqlens, dev):
@@ -661,13 +673,12 @@ def _ssm_args(q, k, v, dt, A, dt_bias, skip, dtypes, dims):
     lead, H, Dv, G, Dk = tuple(v.shape[:-2]), v.shape[-2], v.shape[-1], q.shape[-2], q.shape[-1]
     if G == 0 or H % G:
         raise ValueError("q has %d heads, which do not divide v's %d" % (G, H))
+    _given(k=k, dt=dt, A=A)
     _is(q, "q", v.dtype, lead + (G, Dk), dev)
     _is(k, "k", v.dtype, lead + (G, Dk), dev)
     _is(v, "v", v.dtype, lead + (H, Dv), dev)
-    for t, name, shape in ((dt, "dt", lead + (H,)), (A, "A", (H,))):
-        if t is None:
-            raise TypeError("%s is required" % name)
-        _is(t, name, torch.float32, shape, dev)
+    _is(dt, "dt", torch.float32, lead + (H,), dev)
+    _is(A, "A", torch.float32, (H,), dev)
     _is(dt_bias, "dt_bias", torch.float32, (H,), dev)
     _is(skip, "skip", torch.float32, (H,), dev)
     return dev, lead, H, G, Dk, Dv
@@ -682,8 +693,10 @@ def ssm_fwd(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None, o
     q, k ``[B,T,G,Dk]`` and v ``[B,T,H,Dv]`` bfloat16, G dividing H (head h
     reads group ``h // (H // G)``); dt ``[B,T,H]``, A, dt_bias, skip ``[H]``
     float32 (dt_bias, skip None: zero); h0 ``[N,H,Dk,Dv]`` float32 or None;
-    cu_seqlens int32 ``[N+1]`` on the device for packed sequences (B == 1).
-    Returns ``(o, hT)`` (hT None unless output_final_state)."""
+    cu_seqlens int32 ``[N+1]`` on the device for packed sequences (B == 1),
+    from 0 to T; where it ends before T, the rows behind it are not used, and
+    theirs in the results are not set.  Returns ``(o, hT)`` (hT None unless
+    output_final_state)."""
     lib = load_library()
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
@@ -706,8 +719,7 @@ def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
     _is(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
-    if dO is None:
-        raise TypeError("dO is required")
+    _given(dO=dO)
     _is(dO, "dO", v.dtype, tuple(v.shape), dev)
     _is(dhT, "dhT", torch.float32, (N, H, Dk, Dv), dev)
     s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
@@ -726,18 +738,19 @@ def ssm_step(q, k, v, dt, A, dt_bias, skip, state):
     """One token of every sequence (``dn_ssm_step``): q, k ``[B,G,Dk]``, v
     ``[B,H,Dv]`` (float32 or bfloat16, one dtype), dt ``[B,H]`` float32, state
     ``[B,H,Dk,Dv]`` float32 updated in place.  Returns o ``[B,H,Dv]``."""
-    E, i, f32 = v.dtype, v.get_device(), torch.float32
-    qs, vs = q.shape, v.shape
-    H = vs[-2] if len(vs) == 3 else 0
-    # the usual call in one expression; anything else goes through the checks that say what is wrong
-    if not (H and len(qs) == 3 and qs[0] == vs[0] and qs[1] and H % qs[1] == 0 and E in _DTYPES and i >= 0
-            and v.is_contiguous() and _fits(q, E, qs, i) and _fits(k, E, qs, i) and _fits(dt, f32, vs[:2], i)
-            and _fits(A, f32, (H,), i) and (dt_bias is None or _fits(dt_bias, f32, (H,), i))
-            and (skip is None or _fits(skip, f32, (H,), i))
-            and _fits(state, f32, (vs[0], H, qs[2], vs[2]), i)):
+    try:  # the usual call in one expression; anything else goes through the checks that say what is wrong
+        E, i, f32, qs, vs = v.dtype, v.get_device(), torch.float32, q.shape, v.shape
+        H = vs[-2] if len(vs) == 3 else 0
+        fits = (H and len(qs) == 3 and qs[0] == vs[0] <= _MAX_SIZE and qs[1] and H % qs[1] == 0 and E in _DTYPES and i >= 0
+                and v.is_contiguous() and _fits(q, E, qs, i) and _fits(k, E, qs, i) and _fits(dt, f32, vs[:2], i)
+                and _fits(A, f32, (H,), i) and (dt_bias is None or _fits(dt_bias, f32, (H,), i))
+                and (skip is None or _fits(skip, f32, (H,), i))
+                and _fits(state, f32, (vs[0], H, qs[2], vs[2]), i))
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
         dev, (B,), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, tuple(_DTYPES), 3)
-        if state is None:
-            raise TypeError("state is required")
+        _given(state=state)
         _is(state, "state", torch.float32, (B, H, Dk, Dv), dev)
     o = torch.empty_like(v)
     _call("dn_ssm_step", i, vs[0], H, qs[1], qs[2], vs[2], _DTYPES[E], q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -781,8 +794,7 @@ def conv_silu_bwd(x, w, bias, s0, dy, dsT=None, cu_seqlens=None):
     dtype (dsT None: 0).  Returns a dict: dx and ds0 in x's dtype, dw and dbias
     (None without a bias) in float32."""
     dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
-    if dy is None:
-        raise TypeError("dy is required")
+    _given(dy=dy)
     _is(dy, "dy", x.dtype, tuple(x.shape), dev)
     _is(dsT, "dsT", x.dtype, (N, max(W - 1, 0), H, D), dev)
     gr = dict(dx=torch.empty_like(x), dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
@@ -798,13 +810,16 @@ def conv_silu_step(x, w, bias, state):
     """One token of every sequence (``dn_conv_silu_step``): x ``[B,H,D]``, state
     ``[B,W-1,H,D]`` (x's dtype) holding the last W - 1 inputs, updated in
     place.  Returns y ``[B,H,D]``."""
-    E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
-    if not (len(xs) == 3 and len(ws) == 3 and ws[:2] == xs[1:] and ws[2] and E in _DTYPES and i >= 0
-            and x.is_contiguous() and _fits(w, torch.float32, ws, i)
-            and (bias is None or _fits(bias, torch.float32, ws[:2], i))
-            and state is not None and _fits(state, E, (xs[0], ws[2] - 1, xs[1], xs[2]), i)):
-        if state is None:
-            raise TypeError("state is required")
+    try:
+        E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
+        fits = (len(xs) == 3 and len(ws) == 3 and ws[:2] == xs[1:] and ws[2] and E in _DTYPES and i >= 0
+                and max(xs) <= _MAX_SIZE and x.is_contiguous() and _fits(w, torch.float32, ws, i)
+                and (bias is None or _fits(bias, torch.float32, ws[:2], i))
+                and _fits(state, E, (xs[0], ws[2] - 1, xs[1], xs[2]), i))
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _given(state=state)
         _conv_silu_args(x, w, bias, state, None, 3)
     y = torch.empty_like(x)
     _call("dn_conv_silu_step", i, xs[0], xs[1], xs[2], ws[2], _DTYPES[E], x.data_ptr(), w.data_ptr(), _adr(bias),
@@ -815,6 +830,7 @@ def conv_silu_step(x, w, bias, state):
 def _gated_norm_args(x, z, w):
     """(device, rows, D, weight rows), checked."""
     dev = _gpu(x, "x", tuple(range(1, 9)), tuple(_DTYPES))
+    _given(z=z)
     D = x.shape[-1]
     if not isinstance(w, torch.Tensor) or w.dim() not in (1, 2):
         raise ValueError("w must be a [D] or [H, D] tensor")
@@ -833,10 +849,14 @@ def gated_norm(x, z, w, eps: float = 1e-5, gate_first: bool = False):
     of ``x silu(z)`` times w.  x, z ``[..., D]`` or ``[..., H, D]`` float32 or
     bfloat16; w float32 ``[D]``, or ``[H, D]`` for a weight per head.  Returns y
     in x's dtype."""
-    E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
-    R = ws[0] if len(ws) == 2 else 1
-    if not (len(xs) > 1 and xs[-1] and ws == xs[-len(ws):] and 0 < len(ws) < 3 and E in _DTYPES and i >= 0
-            and x.is_contiguous() and _fits(z, E, xs, i) and _fits(w, torch.float32, ws, i)):
+    try:
+        E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
+        R = ws[0] if len(ws) == 2 else 1
+        fits = (len(xs) > 1 and 0 < xs[-1] <= _MAX_SIZE and ws == xs[-len(ws):] and 0 < len(ws) < 3 and E in _DTYPES
+                and i >= 0 and x.is_contiguous() and _fits(z, E, xs, i) and _fits(w, torch.float32, ws, i))
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
         _gated_norm_args(x, z, w)
     y = torch.empty_like(x)
     _call("dn_gated_norm", i, x.numel() // (xs[-1] or 1), xs[-1], R, _DTYPES[E], x.data_ptr(), z.data_ptr(), w.data_ptr(),
@@ -848,6 +868,7 @@ def gated_norm_bwd(x, z, w, dy, eps: float = 1e-5, gate_first: bool = False):
     """Backward of ``gated_norm`` (``dn_gated_norm_bwd``) from dy in x's dtype:
     ``(dx, dz, dw)``, dx and dz in x's dtype, dw float32."""
     dev, rows, D, R = _gated_norm_args(x, z, w)
+    _given(dy=dy)
     _is(dy, "dy", x.dtype, tuple(x.shape), dev)
     dx, dz, dw = torch.empty_like(x), torch.empty_like(z), torch.empty_like(w)
     wsb = load_library().dn_gated_norm_bwd_workspace(rows, D, R)
@@ -868,6 +889,7 @@ class SsmScan(torch.autograd.Function):
         return o, hT
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dhT):
         q, k, v, dt, A, dt_bias, skip, h0, cu = ctx.saved_tensors
         dO = torch.zeros_like(v) if dO is None else dO.contiguous()
@@ -892,6 +914,7 @@ class ConvSilu(torch.autograd.Function):
         return y, sT
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dsT):
         x, w, bias, s0, cu = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else dy.contiguous()
@@ -914,6 +937,7 @@ class GatedNorm(torch.autograd.Function):
         return gated_norm(x, z, w, eps, gate_first)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, z, w = ctx.saved_tensors
         return (*gated_norm_bwd(x, z, w, dy.contiguous(), ctx.eps, ctx.gate_first), None, None)

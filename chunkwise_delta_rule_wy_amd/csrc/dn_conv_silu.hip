@@ -477,7 +477,7 @@ extern "C" dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, in
 }
 
 extern "C" size_t dn_conv_silu_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W) {
-  if (B <= 0 || T <= 0 || H <= 0 || D <= 0 || W < 1 || W > 4) return 0;
+  if (B <= 0 || T <= 0 || H <= 0 || D <= 0 || W < 1 || W > 4 || (int64_t)H * D * (W + 1) > INT32_MAX) return 0;
   int run, rows;
   bwd_plan((int64_t)B * T, H * D, run, rows);
   return 4 * (size_t)rows * H * D * (W + 1);

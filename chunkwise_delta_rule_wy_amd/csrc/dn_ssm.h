@@ -135,10 +135,12 @@ __device__ __forceinline__ float exp_of(float x) {
   return wy::fexp2(t) * __builtin_fmaf(r, 0.6931471806f, 1.f);
 }
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|); log1p(y) = y log(u) / (u - 1) with
-// u the rounded 1 + y, whose rounding the quotient takes back
+// u the rounded 1 + y, whose rounding the quotient takes back.  The largest
+// negative steps, minus infinity among them, give 0; NaN stays NaN.
 __device__ __forceinline__ float softplus(float x) {
-  const float y = exp_of(-fabsf(x)), u = 1.f + y, d = u - 1.f;
-  return fmaxf(x, 0.f) + (d == 0.f ? y : __logf(u) * (y * __builtin_amdgcn_rcpf(d)));
+  const float n = -fabsf(x);
+  const float y = exp_of(n < -200.f ? -200.f : n), u = 1.f + y, d = u - 1.f;
+  return (x < 0.f ? 0.f : x) + (d == 0.f ? y : __logf(u) * (y * __builtin_amdgcn_rcpf(d)));
 }
 
 // the raw step size of one (token, head): dt + dt_bias
@@ -199,7 +201,9 @@ struct GateTab {
 __device__ __forceinline__ double fill_gates(GateTab &t, float raw, float A, int L) {
   const int l = lane_id();
   const float s = l < L ? softplus(raw) : 0.f;
-  const double b = wave_incl_scan_d((double)s * ((double)A * 1.4426950408889634074));
+  // a decay past 1e30 is zero as well, and sums of 64 stay within the floats' range
+  const double a = (double)s * ((double)A * 1.4426950408889634074);
+  const double b = wave_incl_scan_d(a < -1e30 ? -1e30 : a);
   const double total = lane_val_d(b, 63);
   const float bh = (float)b, bl = (float)(b - (double)bh);
   const float w = wy::fexp2((float)(total - b));
@@ -298,15 +302,14 @@ struct Swz {
   }
   // byte offset of unit u of row r
   __device__ static __forceinline__ uint32_t off(int r, int u) { return r * RB + ((u ^ f(r)) << 4); }
-  // `o`: a constant to add, for matrices that share a base.
   // A lane's address within a tile is one base XOR a constant of the column
   // block plus an immediate offset of the row block (matrices start at multiples
   // of 256 bytes, and f repeats every 16 rows).
   //
   // 32-index fragments of rows 16 t + m, columns 32 kb + 8 g .. + 7
   __device__ static __forceinline__ uint32_t row_base(uint32_t base, int l) { return base + off(l & 15, l >> 4); }
-  __device__ static __forceinline__ bf16x8 row(uint32_t b, int t, int kb, uint32_t o = 0) {
-    return wy::ld<bf16x8>((b ^ (64 * kb)) + 16 * RB * t + o);
+  __device__ static __forceinline__ bf16x8 row(uint32_t b, int t, int kb) {
+    return wy::ld<bf16x8>((b ^ (64 * kb)) + 16 * RB * t);
   }
   // four columns 16 c + 4 g .. + 3 of rows 16 t + m
   __device__ static __forceinline__ uint32_t quad_base(uint32_t base, int l) {
@@ -326,8 +329,8 @@ struct Swz {
     const int r = 8 * (l >> 4) + ((l >> 2) & 3), q = l & 3;
     return {base + off(r, q >> 1) + 8 * (q & 1), base + off(r + 4, q >> 1) + 8 * (q & 1)};
   }
-  __device__ static __forceinline__ bf16x8 col(const Col &x, int kb, int c, uint32_t o = 0) {
-    return wy::cat(wy::ld_tr((x.a ^ (32 * c)) + 32 * RB * kb + o), wy::ld_tr((x.b ^ (32 * c)) + 32 * RB * kb + o));
+  __device__ static __forceinline__ bf16x8 col(const Col &x, int kb, int c) {
+    return wy::cat(wy::ld_tr((x.a ^ (32 * c)) + 32 * RB * kb), wy::ld_tr((x.b ^ (32 * c)) + 32 * RB * kb));
   }
 };
 

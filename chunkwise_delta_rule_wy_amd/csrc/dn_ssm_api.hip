@@ -151,10 +151,10 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
                 hipStream_t stream) {
   const bool packed = cu != nullptr;
   const Plan pl = plan_of(s, packed, backward);
-  const int64_t top = INT32_MAX;
+  const int64_t top = UINT32_MAX / 512;  // a grid has fewer than 2^32 threads, in workgroups of up to 512
   sets_of(s, pl, p.sets, p.set_heads);
   if (pl.nseg * s->H * (s->Dv / 64) > top || pl.nchunks * s->H > top || pl.nchunks * s->G * p.sets > top ||
-      (int64_t)s->n_seqs * s->H * s->Dk * s->Dv / 1024 > top)
+      (int64_t)s->n_seqs * s->H * (s->Dk * s->Dv / 1024) > top)
     return DN_EUNSUPPORTED;
   const Layout L = layout_of(s, pl, packed, backward);
   if (L.total > 0 && (ws_bytes < L.total || !ws || !aligned16(ws))) return DN_ENOWS;
@@ -291,7 +291,7 @@ extern "C" dn_status dn_ssm_step(int32_t B, int32_t H, int32_t G, int32_t Dk, in
   const dn_status st = check_dims(H, G, Dk, Dv, dtype);
   if (st != DN_OK) return st;
   if (!q || !k || !v || !dt || !A || !state || !o || !all16({q, k, v, state, o})) return DN_EINVAL;
-  if ((int64_t)B * H * (Dv / 64) > INT32_MAX) return DN_EUNSUPPORTED;
+  if ((int64_t)B * H * (Dv / 64) > UINT32_MAX / 512) return DN_EUNSUPPORTED;
   dn::SsmStepParams p = {};
   p.q = q;
   p.k = k;

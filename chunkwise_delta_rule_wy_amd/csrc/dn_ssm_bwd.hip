@@ -398,12 +398,13 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   }
 }
 
-// Sums over the sets of heads, four elements per thread (blockIdx.y: dq, dk).
+// Sums over the sets of heads, four elements per thread (blockIdx.y: dq, dk);
+// rows behind the last packed sequence have none.
 constexpr int SUM_THREADS = 256;
 
 __global__ __launch_bounds__(SUM_THREADS) void ssm_set_sum_kernel(SsmParams p, int64_t n4, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * SUM_THREADS + threadIdx.x;
-  if (i >= n4) return;
+  if (i >= (p.cu ? n4 / p.rows * p.cu[p.N] : n4)) return;
   const float *src = (blockIdx.y ? p.dk_part : p.dq_part) + 4 * i;
   f32x4 a = *reinterpret_cast<const f32x4 *>(src);
   for (int k = 1; k < p.sets; ++k) a += *reinterpret_cast<const f32x4 *>(src + k * n);
@@ -444,7 +445,7 @@ hipError_t launch_ssm_grad(const SsmParams &p, int DK, hipStream_t stream) {
     else hipLaunchKernelGGL((ssm_grad_kernel<128>), dim3(grid), dim3(GRAD_THREADS), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.dq_part) {
+    if (p.dq_part && p.rows > 0) {
       const int64_t n = p.rows * p.G * DK, n4 = n / 4;
       hipLaunchKernelGGL(ssm_set_sum_kernel, dim3((unsigned)((n4 + SUM_THREADS - 1) / SUM_THREADS), 2),
                          dim3(SUM_THREADS), 0, stream, p, n4, n);

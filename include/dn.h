@@ -422,18 +422,23 @@ dn_status dn_short_conv_l2_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32
  *   [N,H,Dk,Dv] fp32, holding h = S^T (h0 NULL: zero; hT NULL: not written).
  *   G divides H: head h reads the queries and keys of group h / (H / G).
  *   A <= 0 is the use; a positive A grows and overflows as the formula does.
- * - Packed sequences by cu_seqlens as dn_chunk_fwd (cu[n_seqs] = T).  A
- *   sequence without tokens passes h0 through to hT.
+ * - Packed sequences by cu_seqlens as dn_chunk_fwd, except that cu[n_seqs] may
+ *   be less than T: rows behind the last sequence are not used, and theirs in
+ *   o and the gradients are left as they were.  A sequence without tokens
+ *   passes h0 through to hT.
  * - States, step sizes and decays are fp32 or wider throughout, and hT, ddt
  *   and the parameter gradients have fp32 accuracy; o and the gradients of
  *   q, k and v are rounded to bf16 once at the end and in at most one product
  *   operand before it.
- * - Inputs have to be finite: within a chunk of 64 tokens a value that is not
+ * - The step may be minus infinity or the type's lowest value: s = 0 then, and
+ *   the token leaves the state as it is.  All else has to be finite: within a chunk of 64 tokens a value that is not
  *   reaches the chunk's other outputs, earlier ones included.  It does not
  *   cross sequences.
  * - Supported: Dk in {64, 128}; Dv a positive multiple of 64 up to 1024;
  *   DN_BF16 (dn_ssm_step also DN_F32); pointers of q, k, v, o, states and
- *   their gradients 16-byte aligned.  Otherwise DN_EUNSUPPORTED or DN_EINVAL.
+ *   their gradients 16-byte aligned; 128 H Dv and 128 G Dk below 2^31; fewer
+ *   than 2^23 workgroups a launch (one per sequence, head and 64 columns at
+ *   the most).  Otherwise DN_EUNSUPPORTED or DN_EINVAL.
  */
 typedef struct {
     int32_t B, T, H, G, Dk, Dv;
@@ -478,12 +483,14 @@ dn_status dn_ssm_step(int32_t B, int32_t H, int32_t G, int32_t Dk, int32_t Dv, i
  * filter with z = bias + conv(x), y = z sigmoid(z), where the W - 1 inputs
  * before a sequence's first token are s0 instead of zeros.
  *
- * x, y [B,T,H,D] and s0, sT [N,W-1,H,D] in the dtype (16-byte aligned), w
- * [H,D,W] and bias [H,D] fp32; bias and s0 NULL: zero.  sT receives each
- * sequence's last W - 1 inputs, those of s0 included where the sequence is
- * shorter, bit for bit (NULL: not written; it may not alias s0).  Packed
- * sequences by cu_seqlens with B == 1, as dn_short_conv.  D a multiple of 8, W
- * in 1..4 (DN_EUNSUPPORTED otherwise).
+ * x, y [B,T,H,D] and s0, sT [N,W-1,H,D] in the dtype, w [H,D,W] and bias [H,D]
+ * fp32, all of them 16-byte aligned (DN_EINVAL otherwise); y may not alias x; bias
+ * and s0 NULL: zero.  sT receives each sequence's last W - 1 inputs, those of
+ * s0 included where the sequence is shorter, bit for bit (NULL: not written;
+ * it may not alias s0).  Packed sequences by cu_seqlens with
+ * B == 1, as dn_short_conv, with cu[n_seqs] <= T as in dn_ssm_fwd.  D a
+ * multiple of 8, W in 1..4, H D (W + 1) below 2^31, and fewer than 2^31
+ * quadruples of channels times runs of 32 tokens (DN_EUNSUPPORTED otherwise).
  */
 dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n_seqs,
                        int32_t dtype, const void *x, const float *w, const float *bias, const void *s0,
@@ -521,7 +528,7 @@ dn_status dn_conv_silu_step(int32_t B, int32_t H, int32_t D, int32_t W, int32_t 
  *     gate_first != 0:  y = u / sqrt(mean(u^2) + eps) * w,  u = x g
  *
  * x, z, y [rows, D] in the dtype (16-byte aligned); y may alias x or z.  D a
- * multiple of 8 up to 8192 (DN_EUNSUPPORTED otherwise).
+ * multiple of 8 up to 8192, rows below 2^31 (DN_EUNSUPPORTED otherwise).
  */
 dn_status dn_gated_norm(int64_t rows, int32_t D, int32_t R, int32_t dtype, const void *x, const void *z,
                         const float *w, float eps, int32_t gate_first, void *y, hipStream_t stream);

@@ -2,6 +2,8 @@
 convolution, gated norm) with the 64-bit reference, within the bounds that
 their roundings allow, and the ways a program uses them: continued prompts,
 single tokens, streams, graphs, autograd, the three together."""
+import ctypes
+
 import pytest
 import torch
 
@@ -464,6 +466,190 @@ def test_other_stream_and_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(out2[0], eager[0])
         assert torch.equal(step_state, after[0]) and torch.equal(step_conv, after[1])
+
+
+def test_scan_masked_steps_and_vanishing_decays():
+    """Steps of minus infinity or the type's lowest value leave the state as it is, on the very
+    first and last token too; decays past the float range clear it."""
+    x, dO, dhT, ls = scan_inputs(1, 150, 2, 1, 64, 64)
+    low = torch.finfo(F32).min
+    for t, v in ((0, low), (1, -float("inf")), (63, low), (64, low), (65, -float("inf")), (100, -200.0), (149, low)):
+        x["dt"][0, t] = v
+    far = dict(x, dt=x["dt"].clamp_min(-1e5))  # softplus is 0 there in 64 bits as well
+    val, bound = reference(far, ls, dO, dhT)
+    d = cuda(x)
+    args = (d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"])
+    o, hT = dn.ssm_fwd(*args)
+    gr = dn.ssm_bwd(*args, dO.cuda(), dhT.cuda())
+    check(dict(gr, o=o, hT=hT), val, {k: b + 1e-37 for k, b in bound.items()}, list(val))
+    state = d["h0"].clone()
+    o1 = dn.ssm_step(d["q"][:, 1], d["k"][:, 1], d["v"][:, 1], d["dt"][:, 1], *args[4:7], state)
+    assert torch.equal(state, d["h0"]) and torch.isfinite(o1).all()
+    d["dt"].fill_(-float("inf"))
+    o, hT = dn.ssm_fwd(*args)
+    assert torch.equal(hT, d["h0"]) and torch.isfinite(o).all()
+    d["dt"][0, 70, 1] = float("nan")
+    _, hT = dn.ssm_fwd(*args)
+    assert torch.isnan(hT[:, 1]).all() and torch.equal(hT[:, 0], d["h0"][:, 0])
+    x, dO, dhT, ls = scan_inputs(1, 70, 2, 1, 64, 64, A=-3e38)
+    val, bound = reference(x, ls, dO, dhT)
+    d = cuda(x)
+    args = (d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"])
+    o, hT = dn.ssm_fwd(*args)
+    gr = dn.ssm_bwd(*args, dO.cuda(), dhT.cuda())
+    check(dict(gr, o=o, hT=hT), val, {k: b + 1e-37 for k, b in bound.items()}, list(val))
+
+
+def test_scan_of_a_pack_without_tokens():
+    x, _, dhT, _ = scan_inputs(1, 0, 6, 2, 64, 128, lens=[0, 0, 0])
+    d, cu = cuda(x), cu_of([0, 0, 0])
+    o, hT = dn.ssm_fwd(**d, cu_seqlens=cu)
+    assert o.numel() == 0 and torch.equal(hT, d["h0"])
+    gr = dn.ssm_bwd(d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"], d["v"], dhT.cuda(), cu)
+    assert torch.equal(gr["dh0"].cpu(), dhT) and not gr["dA"].any() and not gr["dskip"].any()
+
+
+@pytest.mark.parametrize("lens,tail", [([70, 0, 33], 97), ([2200, 5], 100), ([0, 0], 40)])
+def test_rows_behind_the_last_sequence_stay(lens, tail):
+    """Offsets that end before the rows do, called through the library itself, with NaN behind
+    the last sequence and marked outputs."""
+    H, G, dk, dv, n = 4, 1, 64, 64, sum(lens)
+    x, dO, dhT, ls = scan_inputs(1, n, H, G, dk, dv, lens)
+    val, bound = reference(x, ls, dO, dhT)
+    pad = lambda t: torch.cat([t, torch.full((1, tail, *t.shape[2:]), float("nan"), dtype=t.dtype)], 1)  # noqa: E731
+    d = {k: (pad(t) if k in ("q", "k", "v", "dt") else t).cuda() for k, t in x.items()}
+    g, gT, cu = pad(dO).cuda(), dhT.cuda(), cu_of(lens)
+    lib, T = dn.load_library(), n + tail
+    s = ctypes.byref(dn._SsmShape(1, T, H, G, dk, dv, len(lens), 1))
+    mark = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+    out = dict(o=mark(d["v"]), hT=mark(d["h0"]))
+    gr = dict(dq=mark(d["q"]), dk=mark(d["k"]), dv=mark(d["v"]), ddt=mark(d["dt"]), dA=mark(d["A"]),
+              ddt_bias=mark(d["A"]), dskip=mark(d["A"]), dh0=mark(d["h0"]))
+    ws = torch.empty(max(lib.dn_ssm_fwd_workspace(s), lib.dn_ssm_bwd_workspace(s)), dtype=torch.uint8, device="cuda")
+    p = lambda *ts: [t.data_ptr() for t in ts]  # noqa: E731
+    ins = p(d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"], cu)
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.dn_ssm_fwd(s, *ins, *p(*out.values()), ws.data_ptr(), ws.numel(), st) == 0
+    assert lib.dn_ssm_bwd(s, *ins, *p(g, gT, *gr.values()), ws.data_ptr(), ws.numel(), st) == 0
+    for name, t in dict(gr, **out).items():
+        if t.shape[:2] == (1, T):
+            assert (t[:, n:] == 7).all(), name
+    cut = {k: t[:, :n] if t.shape[:2] == (1, T) else t for k, t in dict(gr, **out).items()}
+    check(cut, val, bound, list(val))
+    xc, w, b = d["v"], randn(H, dv, 4, seed=2).cuda(), randn(H, dv, seed=3).cuda()
+    y, sT, dx = mark(xc), xc.new_empty(len(lens), 3, H, dv), mark(xc)
+    dw, db = torch.empty_like(w), torch.empty_like(b)
+    assert lib.dn_conv_silu(1, T, H, dv, 4, len(lens), 1, *p(xc, w, b), None, *p(cu, y, sT), st) == 0
+    wsb = lib.dn_conv_silu_bwd_workspace(1, T, H, dv, 4)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    assert lib.dn_conv_silu_bwd(1, T, H, dv, 4, len(lens), 1, *p(xc, w, b), None, *p(cu, g), None, *p(dx, dw, db), None,
+                                ws.data_ptr(), wsb, st) == 0
+    assert (y[:, n:] == 7).all() and (dx[:, n:] == 7).all()
+    y0, s0 = dn.conv_silu(xc[:, :n].contiguous(), w, b, None, cu)
+    g0 = dn.conv_silu_bwd(xc[:, :n].contiguous(), w, b, None, g[:, :n].contiguous(), None, cu)
+    assert torch.equal(y[:, :n], y0) and torch.equal(sT, s0) and torch.equal(dx[:, :n], g0["dx"])
+    assert torch.isfinite(dw).all() and torch.isfinite(db).all()
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows against the same rows by themselves."""
+    n, d = (1 << 31) // 4096 + 70, 4096
+    x = torch.zeros(n, d, dtype=BF, device="cuda")
+    end = randn(300, d, seed=1, dtype=BF).cuda()
+    x[-300:] = end
+    w = randn(d, seed=2).cuda()
+    y = dn.gated_norm(x, x, w)
+    assert torch.equal(y[-300:], dn.gated_norm(end, end, w)) and not y[:1000].any()
+    dx, _, dw = dn.gated_norm_bwd(x, x, w, x)
+    dx0, _, dw0 = dn.gated_norm_bwd(end, end, w, end)
+    assert torch.equal(dx[-300:], dx0)
+    # the same 300 terms |dy n g| <= r |x|^3, r < 1.2, added in two orders
+    assert ((dw - dw0).abs() <= 2 * 300 * ref.U32 * 1.2 * (end.float().abs() ** 3).sum(0)).all()
+    del y, dx
+    wc, b = randn(32, 128, 4, seed=3).cuda(), randn(32, 128, seed=4).cuda()
+    yc, sT = dn.conv_silu(x.view(1, n, 32, 128), wc, b)
+    s0 = torch.zeros(1, 3, 32, 128, dtype=BF, device="cuda")
+    y0, sT0 = dn.conv_silu(end.view(1, 300, 32, 128), wc, b, s0)
+    assert torch.equal(yc[:, -300:], y0) and torch.equal(sT, sT0)
+    gr = dn.conv_silu_bwd(x.view(1, n, 32, 128), wc, b, None, x.view(1, n, 32, 128))
+    g0 = dn.conv_silu_bwd(end.view(1, 300, 32, 128), wc, b, s0, end.view(1, 300, 32, 128))
+    assert torch.equal(gr["dx"][:, -300:], g0["dx"])
+    del yc, gr
+    # a long sequence and a short one behind it, whose results do not depend on the first
+    sx, dO, dhT, _ = scan_inputs(1, 300, 32, 1, 64, 128, state=False, seed=5)
+    val, bound = reference(sx, [300], dO)
+    q = torch.zeros(1, n, 1, 64, dtype=BF, device="cuda")
+    k, dt = torch.zeros_like(q), torch.zeros(1, n, 32, device="cuda")
+    for t, name in ((q, "q"), (k, "k"), (dt, "dt")):
+        t[:, -300:] = sx[name].cuda()
+    x = x.view(1, n, 32, 128)
+    x[:, -300:] = sx["v"].cuda()
+    par = [sx[i].cuda() for i in ("A", "dt_bias", "skip")]
+    cu = cu_of([n - 300, 300])
+    o, hT = dn.ssm_fwd(q, k, x, dt, *par, None, cu)
+    check(dict(o=o[:, -300:], hT=hT[1:]), val, bound, ["o", "hT"])
+    assert not o[:, :1000].any() and not hT[0].any()
+    o.zero_()
+    o[:, -300:] = dO.cuda()
+    gr = dn.ssm_bwd(q, k, x, dt, *par, None, o, None, cu)
+    last = {i: g[:, -300:] if g.dim() > 1 else g for i, g in gr.items() if i != "dh0"}
+    check(last, val, bound, list(last))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams side by side, each with its own tensors and workspaces."""
+    sets = [scan_inputs(1, 2500, 4, 2, 64, 64, seed=10 * i) for i in range(2)]
+    sets = [(cuda(x), dO.cuda(), dhT.cuda()) for x, dO, dhT, _ in sets]
+
+    def go(d, dO, dhT):
+        args = (d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"])
+        o, hT = dn.ssm_fwd(*args)
+        return [o, hT, *dn.ssm_bwd(*args, dO, dhT).values()]
+
+    want = [go(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(go(*s))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+def test_autograd_pass_in_a_graph_and_no_second_derivatives():
+    x, dO, _, _ = scan_inputs(1, 130, 2, 1, 64, 64, state=False)
+    d, dO = cuda(x), dO.cuda()
+    w, wn = randn(2, 64, 4, seed=1).cuda(), randn(64, seed=2).cuda()
+    leaves = [d["q"], d["k"], d["v"], d["dt"], d["A"], w, wn]
+
+    def train():
+        q, k, v, dt, A, w, wn = (t.detach().requires_grad_() for t in leaves)
+        c, _ = dn.conv_silu_fn(v, w)
+        o, _ = dn.ssm_scan(q, k, c, dt, A, d["dt_bias"], d["skip"])
+        y = dn.gated_norm_fn(o, v, wn)
+        return [y.detach(), *torch.autograd.grad(y, (q, k, v, dt, A, w, wn), dO)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        train()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = train()
+    for i in range(3):
+        d["v"].copy_(randn(1, 130, 2, 64, seed=70 + i, dtype=BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, train()))
+    z = randn(2, 64, seed=3).cuda().requires_grad_()
+    y = dn.gated_norm_fn(z, z, wn)
+    (g,) = torch.autograd.grad(y.sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
 
 
 def test_refusals_on_the_device():

@@ -190,3 +190,37 @@ def test_python_refuses_host_tensors_and_types():
         dn.ssm_fwd(x, x, x, torch.zeros(1, 4, 2), -torch.ones(2))  # float32 chunks are not there
     with pytest.raises(ValueError):
         dn.ssm_step(x[0], x[0], x[0], torch.zeros(4, 2), -torch.ones(2), None, None, torch.zeros(4, 2, 64, 64))
+
+
+def test_python_refuses_what_is_no_tensor():
+    x, w = torch.zeros(2, 2, 64), torch.zeros(2, 64, 4)
+    for call in (lambda: dn.ssm_step(None, x, x, x, x, None, None, x), lambda: dn.ssm_step(x, x, None, x, x, None, None, x),
+                 lambda: dn.conv_silu_step(None, w, None, x), lambda: dn.conv_silu_step(x, None, None, x),
+                 lambda: dn.conv_silu_step(x, w, None, None), lambda: dn.gated_norm(None, x, x),
+                 lambda: dn.gated_norm(x, x, None), lambda: dn.gated_norm_bwd(x, None, x, x),
+                 lambda: dn.ssm_fwd(None, x, x, x, x), lambda: dn.conv_silu(None, w)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+
+
+def test_launches_that_are_too_large_are_refused(lib):
+    # 2^20 sequences of 64 heads: 2^26 workgroups of 256 threads are more than a grid has
+    assert lib.dn_ssm_step(1 << 20, 64, 1, 64, 64, 1, P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, None, P(FAKE),
+                           P(FAKE), None) == EUNSUPPORTED
+    s = ssm_shape(B=1 << 18, n_seqs=1 << 18, H=64, G=1)
+    assert ssm_fwd(lib, s) == EUNSUPPORTED and ssm_bwd(lib, s) == EUNSUPPORTED
+    assert ssm_fwd(lib, ssm_shape(H=1 << 18, G=1 << 18, Dv=1024)) == EUNSUPPORTED  # 2^31 bytes between 64 rows
+    # 2^27 channels of 16 weights and a bias, and 2^31 channel quadruples times runs
+    assert lib.dn_conv_silu(1, 1, 1 << 20, 1 << 9, 4, 1, 1, P(FAKE), P(FAKE), None, None, None, P(FAKE), None,
+                            None) == EUNSUPPORTED
+    assert lib.dn_conv_silu_bwd_workspace(1, 1, 1 << 20, 1 << 9, 4) == 0
+    assert lib.dn_conv_silu(1 << 15, 1 << 15, 8, 64, 4, 1 << 15, 1, P(FAKE), P(FAKE), None, None, None, P(FAKE), None,
+                            None) == EUNSUPPORTED
+
+
+def test_conv_silu_refuses_unaligned_weights(lib):
+    for w, b in ((FAKE + 4, FAKE), (FAKE, FAKE + 8)):
+        assert lib.dn_conv_silu(1, 4, 1, 8, 4, 1, 1, P(FAKE), P(w), P(b), None, None, P(FAKE), None, None) == EINVAL
+        assert lib.dn_conv_silu_step(1, 1, 8, 4, 1, P(FAKE), P(w), P(b), P(FAKE), P(FAKE), None) == EINVAL
+        assert lib.dn_conv_silu_bwd(1, 4, 1, 8, 4, 1, 1, P(FAKE), P(w), P(b), None, None, P(FAKE), None, P(FAKE), P(FAKE),
+                                    None, None, P(FAKE), 1 << 30, None) == EINVAL
