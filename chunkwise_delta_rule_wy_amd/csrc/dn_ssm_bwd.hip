@@ -99,7 +99,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   }
   Stage<CH, SSM_TILE, GRAD_THREADS> sv, so;
   f32x4 hr[2][2], dr[2][2];  // the wave's rows of h and dh: [32-column block][half of 8 columns]
-  const uint32_t state_off = 4 * ((n0 + m) * p.DV + 8 * g);
+  const uint32_t state_off = chunk_state_unit<DK>(n0 / 16, g >> 1, m, 2 * (g & 1));
   auto fetch_rows = [&](int h, int tile) {
     const size_t off = (row0 * p.H + h) * p.DV + tile * SSM_TILE;
     const uint32_t pitch = 2 * p.H * p.DV;
@@ -109,13 +109,14 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     for (auto &u : so.u) u ^= flip;
   };
   auto fetch_states = [&](int h, int tile) {
-    const size_t at = ((size_t)chunk * p.H + h) * DK * p.DV + tile * SSM_TILE;
+    const size_t at = ((size_t)chunk * p.H + h) * DK * p.DV + tile * (SSM_TILE * DK);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        hr[kb][x] = ldg<f32x4>(p.states + at, state_off + 128 * kb + 16 * x);
-        dr[kb][x] = sign * ldg<f32x4>(p.dstates + at, state_off + 128 * kb + 16 * x);
+        const uint32_t off = state_off + chunk_state_unit<DK>(0, 2 * kb, 0, x);
+        hr[kb][x] = ldg<f32x4>(p.states + at, off);
+        dr[kb][x] = sign * ldg<f32x4>(p.dstates + at, off);
       }
   };
   // one wave fills the gate tables; the raw steps are loaded a head ahead and

@@ -130,9 +130,9 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
     fetch(at(min(i + 1, nch - 1)));  // without a branch, which would hold two sets of registers
     const typename XT::Col bx = {fresh(cx.a), fresh(cx.b)};
     if (STORE) {
-      float *dst = (REV ? p.dstates : p.states) + ((size_t)chunk_id(p, sg, c) * p.H + head) * per_state + col;
+      float *dst = (REV ? p.dstates : p.states) + ((size_t)chunk_id(p, sg, c) * p.H + head) * per_state + col * DK;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) stg<f32x4>(dst, lane_off + t * rows16, sign * S[t]);
+      for (int t = 0; t < NT; ++t) stg<f32x4>(dst, chunk_state_unit<DK>(t, 0, m, g), sign * S[t]);
     }
     sign = -sign;
     const GateTab &T = lds.tabs[i & 1][TABS == 2 ? sub : 0];
