@@ -31,6 +31,11 @@ namespace dn {
 namespace {
 
 constexpr int GRAD_THREADS = 512;
+// Heads between two rounds in which every wave turns one head's sums into its
+// scalar gradients and fills one of the next heads' gate tables.  (4 x 4096
+// tokens, 32 heads, 128 x 64: XX us, with one wave for each of the two tasks
+// beside every head's products 250 us.)
+constexpr int ROUND = GRAD_THREADS / 64;
 
 template <int DK>
 struct GradLds {
@@ -41,11 +46,11 @@ struct GradLds {
   alignas(16) bf16 dO[CH * VS];
   alignas(16) bf16 dh[DK * VS];  // dh rounded, for K dh; at the end dG^T
   alignas(16) bf16 p[CH * VS];   // the head's P^T, zero above the diagonal blocks
-  GateTab tabs[3];               // of a head and its neighbours
+  GateTab tabs[ROUND];
   struct Sums {
     double hd[8];
     float pairs[4][CH], col_e[2][CH], diag_e[CH], qd[NT][CH], kd[NT][CH], diag[4];
-  } sums[2];
+  } sums[ROUND];
 };
 
 template <int DK>
@@ -83,7 +88,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   const int R = p.H / p.G;
   const int h_first = grp * R + set * p.set_heads;
   const int heads = min(p.set_heads, R - set * p.set_heads);
-  const int cb = w & 3, half = w >> 2;
+  const int half = w >> 2, cb = half ? 3 - (w & 3) : w & 3;  // so that the lower blocks are spread over the SIMDs
   const int n0 = DK == 128 ? 16 * w : 16 * cb, tt0 = DK == 128 ? 0 : 2 * half;
   const bool own_rows = DK == 128 || half == 0;  // one wave per 16 rows of h and dh for their dot product
   const int j = 16 * cb + m;                     // the lane's token column
@@ -103,32 +108,26 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   auto fetch_rows = [&](int h, int tile) {
     const size_t off = (row0 * p.H + h) * p.DV + tile * SSM_TILE;
     const uint32_t pitch = 2 * p.H * p.DV;
-    sv.load(p.v + off, pitch, L);
-    so.load(p.dO + off, pitch, L);
-#pragma unroll
-    for (auto &u : so.u) u ^= flip;
+    sv.load_clamped(p.v + off, pitch, L, threadIdx.x);
+    so.load_clamped(p.dO + off, pitch, L, threadIdx.x);
   };
-  auto fetch_states = [&](int h, int tile) {
+  auto fetch_state = [&](const float *states, int h, int tile, f32x4 (&x)[2][2]) {
     const size_t at = ((size_t)chunk * p.H + h) * DK * p.DV + tile * (SSM_TILE * DK);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t off = state_off + chunk_state_unit<DK>(0, 2 * kb, 0, x);
-        hr[kb][x] = ldg<f32x4>(p.states + at, off);
-        dr[kb][x] = sign * ldg<f32x4>(p.dstates + at, off);
-      }
+      for (int i = 0; i < 2; ++i)
+        x[kb][i] = ldg<f32x4>(states + at, state_off + chunk_state_unit<DK>(0, 2 * kb, 0, i));
   };
-  // one wave fills the gate tables; the raw steps are loaded a head ahead and
-  // before the head's other loads, for which the wave would else have to wait
+  // the raw steps are loaded a round ahead
   float raw = 0.f;
   auto load_raw = [&](int hh) { raw = l < L ? raw_step(p, row0 + l, h_first + min(hh, heads - 1)) : 0.f; };
-  auto gates = [&](int hh) { fill_gates(s.tabs[hh % 3], raw, p.A[h_first + hh], L); };
-  // the head's sums over the waves and its scalar gradients, by one wave
+  auto gates = [&](int hh) { fill_gates(s.tabs[hh % ROUND], raw, p.A[h_first + hh], L); };
+  // a head's sums over the waves and its scalar gradients
   auto finish = [&](int hh) {
     const int h = h_first + hh;
-    const GateTab &T = s.tabs[hh % 3];
-    const typename LD::Sums &x = s.sums[hh & 1];
+    const GateTab &T = s.tabs[hh % ROUND];
+    const typename LD::Sums &x = s.sums[hh % ROUND];
     float pairs = 0.f, qd = 0.f, kd = 0.f;
     double hd = 0.;
     for (int c = 0; c <= (l >> 4); ++c) pairs += x.pairs[c][l];
@@ -158,13 +157,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     }
   };
 
-  if (w == 2) {
-    load_raw(0);
-    gates(0);
-    load_raw(1);
-  }
+  load_raw(w);
+  if (w < heads) gates(w);
   fetch_rows(h_first, 0);
-  fetch_states(h_first, 0);
+  fetch_state(p.states, h_first, 0, hr);
+  fetch_state(p.dstates, h_first, 0, dr);
   __syncthreads();
 
   // G: tiles of rows r (four per lane), column j
@@ -185,8 +182,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h_first + hh;
-    const GateTab &T = s.tabs[hh % 3];
-    typename LD::Sums &sums = s.sums[hh & 1];
+    const int place = hh % ROUND;
+    const GateTab &T = s.tabs[place];
+    typename LD::Sums &sums = s.sums[place];
+    if (place == 0) load_raw(hh + ROUND + w);
     f32x4 M[2];
     M[0] = M[1] = zero4();
     double hd = 0.;
@@ -198,6 +197,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
       const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
       const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
       __syncthreads();
+      // dO is zero behind the sequence; v's rows there meet gates of zero
+      static_assert(decltype(so)::NU == 1, "one unit a thread");
+      so.u[0] = (int)threadIdx.x / decltype(so)::UPR < L ? so.u[0] ^ flip : (u32x4)0u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) dr[x >> 1][x & 1] *= sign;
       sv.template store<VS>(s.v);
       so.template store<VS>(s.dO);
       if (own_rows) {
@@ -227,13 +231,9 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
         }
       }
       __syncthreads();
-      if (tile == 0 && w == 2 && hh + 1 < heads) {
-        gates(hh + 1);
-        load_raw(hh + 2);
-      }
       fetch_rows(nh, nt);
-      // h dO^T, then dh V^T: the wave's 16 Dk rows.  The states' registers are
-      // free after that for the next ones, which arrive during the rest.
+      // h dO^T, then dh V^T: the wave's 16 Dk rows.  A state's registers are
+      // free after that for the next one, which arrives during the rest.
       auto rows = [&](const f32x4 (&st)[2][2], const bf16 *ly, const bf16 *lx, const float *coef, f32x4 (&acc)[NTT],
                       float *dots) {
         f32x4 a[NTT];
@@ -270,8 +270,9 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
         __builtin_amdgcn_sched_barrier(0);
       };
       rows(hr, s.dO, s.q, T.gam, dq, sums.qd[n0 / 16]);
+      fetch_state(p.states, nh, nt, hr);
       rows(dr, s.v, s.k, T.ws, dk, sums.kd[n0 / 16]);
-      fetch_states(nh, nt);
+      fetch_state(p.dstates, nh, nt, dr);
       // M, the wave's row blocks
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
@@ -310,9 +311,6 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
           if (j < L)
           stg<bf16x4>(p.dv + (row0 * p.H + h) * p.DV + tile * SSM_TILE, 2 * (j * (p.H * p.DV) + c), cvt_bf16x4(o));
         }
-      }
-      if (tile == 0) {  // by waves without blocks of M
-        if (w == 3 && hh > 0) finish(hh - 1);
       }
     }
     // the head's sums over the 64 x 64 matrices; `below` sums a column's rows
@@ -361,9 +359,12 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     hd += __shfl_xor(hd, 16, 64);
     hd += __shfl_xor(hd, 32, 64);
     if (l == 0) sums.hd[w] = hd;
+    if (place == ROUND - 1 || hh + 1 == heads) {
+      __syncthreads();
+      if (w <= place) finish(hh - place + w);
+      if (hh + 1 + w < heads) gates(hh + 1 + w);
+    }
   }
-  __syncthreads();
-  if (w == 3) finish(heads - 1);
 
   // dG^T into LDS (rows j, row blocks above the diagonal zero), then its
   // products with K and Q
