@@ -193,6 +193,28 @@ __device__ __forceinline__ float row_suffix(float x, int g, float &after) {
   after = (g & 1 ? 0.f : __uint_as_float(a[1])) + (g & 2 ? 0.f : hi);
   return __uint_as_float(b[0]) + hi;
 }
+// sums over the four rows of 16 lanes of N = 2 or 4 values at once: row g gets
+// that of x[g % N]
+template <int N>
+__device__ __forceinline__ float rows_sums(const float (&x)[N]) {
+  static_assert(N == 2 || N == 4, "a value for every row, or for every other");
+  auto halves = [](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  const float a = halves(x[0], x[N - 2]), b = halves(x[1], x[N - 1]);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// sums over the 16 lanes of a row of four values at once: lane m gets that of x[m % 4]
+__device__ __forceinline__ float row_sums16(const f32x4 &x, int m) {
+  const bool b0 = m & 1, b1 = m & 2;
+  const float a = (b0 ? x[1] : x[0]) + dpp0<0xB1>(b0 ? x[0] : x[1]);
+  const float b = (b0 ? x[3] : x[2]) + dpp0<0xB1>(b0 ? x[2] : x[3]);
+  float c = (b1 ? b : a) + dpp0<0x4E>(b1 ? a : b);
+  c += dpp0<0x124>(c);
+  return c + dpp0<0x128>(c);
+}
 __device__ __forceinline__ double lane_val_d(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);

@@ -253,19 +253,23 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 #pragma unroll
             for (int t = 0; t < NTT; ++t) a[t] = mma32(a[t], sp.p[k], y[t]);
         }
+        float dot[NTT];
 #pragma unroll
         for (int t = 0; t < NTT; ++t) {
           const int r = 16 * (tt0 + t) + m;
           const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(lx + r * QS + n0 + 4 * g);
           const float c = coef[r];
-          float dot = 0.f;
+          dot[t] = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            dot += (float)xv[i] * a[t][i];
+            dot[t] += (float)xv[i] * a[t][i];
             acc[t][i] += c * a[t][i];
           }
-          dot = cross_row_sum(dot);
-          if (g == 0) dots[r] = tile == 0 ? dot : dots[r] + dot;
+        }
+        const float sum = rows_sums(dot);
+        if (g < NTT) {
+          float *d = dots + 16 * (tt0 + g) + m;
+          *d = tile == 0 ? sum : *d + sum;
         }
         __builtin_amdgcn_sched_barrier(0);
       };
@@ -341,11 +345,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
       const float sum = row_suffix(e[0], g, after);
       after += below;
       below += sum;
+      f32x4 d;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float d = row_sum16(r0 + i > j ? (e[i] + after) * sj : 0.f);
-        if (m == 0) sums.pairs[cb][r0 + i] = d;
-      }
+      for (int i = 0; i < 4; ++i) d[i] = r0 + i > j ? (e[i] + after) * sj : 0.f;
+      const float sums_m = row_sums16(d, m);
+      if (m < 4) sums.pairs[cb][r0 + m] = sums_m;
       __builtin_amdgcn_sched_barrier(0);
     }
     if (g == 0) sums.col_e[half][j] = below;
