@@ -813,7 +813,7 @@ def conv_silu_step(x, w, bias, state):
     try:
         E, i, xs, ws = x.dtype, x.get_device(), x.shape, w.shape
         fits = (len(xs) == 3 and len(ws) == 3 and ws[:2] == xs[1:] and ws[2] and E in _DTYPES and i >= 0
-                and max(xs) <= _MAX_SIZE and x.is_contiguous() and _fits(w, torch.float32, ws, i)
+                and xs.numel() <= _MAX_SIZE and x.is_contiguous() and _fits(w, torch.float32, ws, i)
                 and (bias is None or _fits(bias, torch.float32, ws[:2], i))
                 and _fits(state, E, (xs[0], ws[2] - 1, xs[1], xs[2]), i))
     except AttributeError:  # not a tensor

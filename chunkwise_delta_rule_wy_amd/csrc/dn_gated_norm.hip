@@ -10,7 +10,11 @@
 //
 // with g'(z) = sigmoid(z) (1 + z (1 - sigmoid(z))).  A row sits in registers
 // of a group of LPR lanes (one wave's part, or the whole workgroup for wide
-// rows), K units of 16 bytes per lane, so that every tensor crosses HBM once.
+// rows), K units of 16 bytes per lane, so that every tensor crosses HBM once,
+// which bounds both passes: 262144 rows of 256 values in bf16 take 80 us
+// forwards (403 MB, 5.0 TB/s) and 117 us backwards (671 MB, 5.7 TB/s), the rates
+// of large copies.  Two, four or eight rows per lane group with all loads first
+// are slower (91, 119, 167 us forwards: fewer waves).
 // The weights' gradient is summed in registers over the rows that a workgroup
 // takes (all of one weight row), in LDS over its lane groups and by a second
 // kernel over the workgroups, in a fixed order.

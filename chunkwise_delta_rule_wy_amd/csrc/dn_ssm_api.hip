@@ -42,14 +42,14 @@ int pair_of(const dn_ssm_shape *s) {
 // sequences are cut only where they would leave compute units idle.
 // Up to UNCUT chunks nothing is cut: the chunks' chain is then no longer than
 // the three passes that cutting needs (1357 tokens in 9 sequences, 6 heads,
-// 64 x 128, forwards and backwards: 68 us, cut into segments of 4 chunks 90 us).
+// 64 x 128, forwards and backwards: 65 us, cut into segments of 4 chunks 80 us).
 // Fixed length: no cuts from FULL_WGS workgroups on, else about FIXED_WGS, two
 // for each of the 256 CUs, and not below four chunks a segment (16384 tokens,
-// 16 heads, 128 x 128: 124 us, with 384 workgroups 134 us, 1024: 157 us).
+// 16 heads, 128 x 128: 125 us, with 384 workgroups 142 us, 1024: 149 us).
 // Packed: the lengths are not known on the host, and one long sequence among
 // short ones would set the pass's time, so that longer packs are always cut, so
 // finely that the workgroups' rounds come out even (65536 tokens, 32 heads,
-// 128 x 128: 789 us with PACKED_WGS 2048, 806 us with 1024, 846 us with 4096).
+// 128 x 128: 833 us with PACKED_WGS 2048, 906 us with 1024, 882 us with 4096).
 constexpr int64_t UNCUT = 32, FULL_WGS = 384, FIXED_WGS = 512, PACKED_WGS = 2048;
 
 struct Plan {
@@ -85,7 +85,7 @@ Plan plan_of(const dn_ssm_shape *s, bool packed, bool backward) {
 
 // Sets of a group's heads for the gradient kernel: one workgroup per CU where
 // the heads give as many, since every set costs a start and a share of fp32
-// partial sums (4 x 4096 tokens, 32 heads: 285 us with one set, 330 us with
+// partial sums (4 x 4096 tokens, 32 heads: 214 us with one set, 252 us with
 // four, their sums included).
 void sets_of(const dn_ssm_shape *s, const Plan &pl, int &sets, int &heads) {
   const int64_t R = s->H / s->G, wgs = pl.nchunks * s->G;

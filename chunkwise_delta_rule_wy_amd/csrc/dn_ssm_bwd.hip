@@ -21,10 +21,17 @@
 // with K and Q are made once for all of them.  dlog's pairs are
 // summed as they stand, suffix sums down the columns and then across, never as
 // a difference of larger sums: with a strong decay E's diagonal, which belongs
-// to no t, outweighs the rest, and an error that all tokens share adds up in dA.  Wave (cb, half) = (w % 4, w / 4)
-// owns token column block cb of the 64 x 64 matrices, of M and dG only the row
-// blocks 2 half, 2 half + 1, and of dv the columns' half; for dq and dk a
-// wave owns 16 of the Dk rows.
+// to no t, outweighs the rest, and an error that all tokens share adds up in
+// dA.  Wave (cb, half) owns token column block cb of the 64 x 64 matrices, of M
+// and dG only the row blocks 2 half, 2 half + 1, and of dv the columns' half;
+// for dq and dk a wave owns 16 of the Dk rows.
+//
+// 245 registers allow two waves on a SIMD, one workgroup on a CU, so that what
+// the next head needs is loaded as soon as its registers are free and without
+// a branch.  4 x 4096 tokens, 32 heads of 128 x 64 (256 workgroups): 214 us.
+// The states (537 MB) and v, dO, dv (201 MB) pass at 3.4 TB/s; without the loads
+// the rest takes 177 us, without most of the products the loads take 192 us,
+// so that neither hides the other entirely.
 #include "dn_ssm.h"
 
 namespace dn {
@@ -32,9 +39,10 @@ namespace {
 
 constexpr int GRAD_THREADS = 512;
 // Heads between two rounds in which every wave turns one head's sums into its
-// scalar gradients and fills one of the next heads' gate tables.  (4 x 4096
-// tokens, 32 heads, 128 x 64: XX us, with one wave for each of the two tasks
-// beside every head's products 250 us.)
+// scalar gradients and fills one of the next heads' gate tables: both are
+// long chains of a few lanes' work, which one wave for each of the two tasks
+// beside every head's products would make the kernel's pace (241 against 250
+// us, and 183 against 254 us without the loads, before the loads came early).
 constexpr int ROUND = GRAD_THREADS / 64;
 
 template <int DK>
