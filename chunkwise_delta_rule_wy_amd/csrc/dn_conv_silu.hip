@@ -19,10 +19,9 @@
 // channels, W = 4, bf16, 53 us forwards (5.1 TB/s, the rate of a large copy)
 // and 102 us backwards (3.9 TB/s; runs of 16 or 64 tokens and batches of 8
 // are slower) against 55 and 150.  In the backward pass a thread recomputes z
-// from x.  The weights'
-// gradients are summed in registers over a run, in LDS over a workgroup's runs
-// and by a second kernel over the workgroups, in a fixed order, so that they
-// repeat bit for bit.
+// from x.  The weights' gradients are summed in registers over a run, in LDS
+// over a workgroup's runs and by a second kernel over the workgroups, in a
+// fixed order, so that they repeat bit for bit.
 #include "dn.h"
 #include "dn_rows.h"
 

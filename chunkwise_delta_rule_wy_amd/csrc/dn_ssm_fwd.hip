@@ -47,10 +47,10 @@ int work_items(const SsmParams &p) {
 // on average (by some 2^-25 of their size), and an error of one sign in the
 // states would add up in dA, where it reached 2e-6 of the result.
 //
-// Measured at 4 x 4096 tokens, 32 heads of 128 x 64, cut into 16 segments: without
-// STORE 38 us forwards and 62 us both ways, bound by issue (a SIMD issues
-// matrix and vector instructions by turns: 260 vector ones a chunk, half of
-// them split3, beside 48 products); with STORE both ways 140 us, 537 MB of
+// Measured at 4 x 4096 tokens, 32 heads of 128 x 64: without STORE 38 us
+// forwards (8 segments a sequence) and 62 us both ways (4 segments), bound by
+// issue (a SIMD issues matrix and vector instructions by turns: 260 vector
+// ones a chunk, half of them split3, beside 48 products); with STORE both ways 140 us, 537 MB of
 // states and 150 MB of inputs at 4.9 TB/s.
 template <int DK, int PAIR>
 struct SweepLds {
@@ -196,8 +196,8 @@ __global__ __launch_bounds__(Work<PAIR>::THREADS, 4) void ssm_sweep_kernel(SsmPa
 // Start states of a sequence's segments from their own end states and decays,
 // in place, four state elements per thread; a sequence without tokens hands
 // its initial state on.  Bound by the latency of the segment states' loads, of
-// which four segments are on their way at a time (64 segments of 32 heads of
-// 128 x 64: 11 us for 67 MB, which the caches still hold).
+// which four segments are on their way at a time (32 segments of 32 heads of
+// 128 x 64: 11 us for the 34 MB of states, read and written).
 constexpr int JOIN_THREADS = 256;
 
 __global__ __launch_bounds__(JOIN_THREADS) void ssm_join_kernel(SsmParams p, int dk) {
