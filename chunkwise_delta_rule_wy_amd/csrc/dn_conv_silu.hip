@@ -13,15 +13,16 @@
 // A thread owns four consecutive channels (8 bytes of bf16, 16 of fp32) of a
 // run of consecutive tokens and slides the W-token window through registers; a
 // run reads the W - 1 rows beside it again.  Everything else is streamed once:
-// HBM bounds all three kernels, and rows are loaded a batch ahead of their
-// use.  Eight channels and batches of eight rows need twice the registers, and
-// the waves that this costs hide less: measured at 4 x 4096 tokens of 4096
-// channels, W = 4, bf16, 53 us forwards (5.1 TB/s, the rate of a large copy)
-// and 102 us backwards (3.9 TB/s; runs of 16 or 64 tokens and batches of 8
-// are slower) against 55 and 150.  In the backward pass a thread recomputes z
-// from x.  The weights' gradients are summed in registers over a run, in LDS
-// over a workgroup's runs and by a second kernel over the workgroups, in a
-// fixed order, so that they repeat bit for bit.
+// HBM bounds the forward pass and the step, HBM and some 35 vector instructions
+// an element the backward pass, in which a thread recomputes z from x.  Rows are
+// loaded in batches, in the backward pass a batch ahead of their use.  Measured
+// at 4 x 4096 tokens of 4096 channels, W = 4, bf16: 53 us forwards (5.1 TB/s,
+// the rate of a large copy; with eight channels and eight rows 55 us) and 90 us
+// backwards (4.5 TB/s; batches of one row 93 us, of four, which leave three waves
+// on a SIMD, 97 us, of four without the early loads 93 us).  The weights'
+// gradients are summed in registers over a run, in LDS over a workgroup's runs
+// and by a second kernel over the workgroups, in a fixed order, so that they
+// repeat bit for bit.
 #include "dn.h"
 #include "dn_rows.h"
 
@@ -31,7 +32,7 @@ namespace {
 constexpr int CS_THREADS = 256;
 constexpr int CS_CH = 4;         // channels of a thread
 constexpr int CS_BATCH = 4;      // rows loaded ahead (forward)
-constexpr int CS_BWD_BATCH = 4;  // the same, x and dy
+constexpr int CS_BWD_BATCH = 2;  // the same of x and dy, a batch ahead of their use
 constexpr int CS_MAX_ROWS = 256; // rows of partial weight gradients
 
 struct ConvSiluParams {
@@ -217,10 +218,13 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
 // all dz up to u complete; a part that starts its sequence also emits the
 // places before it, ds0.
 template <typename E, int W, int UL>
-__global__ __launch_bounds__(CS_THREADS) void conv_silu_bwd_kernel(ConvSiluParams p) {
+__global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_kernel(ConvSiluParams p) {
   constexpr int RUNS = CS_THREADS / UL, PER = UL * CS_CH * (W + 1);
   __shared__ float part[RUNS][PER];
-  const int units = p.C / CS_CH, ul = threadIdx.x % UL, rl = threadIdx.x / UL;
+  const int units = p.C / CS_CH, ul = threadIdx.x % UL;
+  // a wave's lanes share their run where UL is a wave: its place, and all
+  // branches on it, are then scalar
+  const int rl = UL == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / UL) : threadIdx.x / UL;
   const int unit = blockIdx.x * UL + ul, c0 = unit * CS_CH;
   const bool act = unit < units;
   float dw[W][CS_CH], db[CS_CH];
@@ -247,15 +251,25 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_bwd_kernel(ConvSiluParam
       load_history<E, W>(p, s, a, c0, h);
 #pragma unroll
       for (int k = 0; k < W; ++k) zero8(dz[k]);
+      const int64_t lim = min(b + (W - 1), s.nx);  // rows behind it are not used
+      Raw<E> xn[CS_BWD_BATCH], yn[CS_BWD_BATCH];
+      auto fetch = [&](int64_t u0) {
+#pragma unroll
+        for (int i = 0; i < CS_BWD_BATCH; ++i) {
+          const int64_t at = min(u0 + i, lim - 1) * p.C;
+          xn[i].load(x + at + c0, true);
+          yn[i].load(dy + at + c0, true);
+        }
+      };
+      fetch(a);
       for (int64_t u0 = a; u0 < b + (W - 1); u0 += CS_BWD_BATCH) {
         Raw<E> xb[CS_BWD_BATCH], yb[CS_BWD_BATCH];
 #pragma unroll
         for (int i = 0; i < CS_BWD_BATCH; ++i) {
-          const int64_t u = u0 + i;
-          const bool in = u < s.nx && u < b + (W - 1);
-          xb[i].load(x + u * p.C + c0, in);
-          yb[i].load(dy + u * p.C + c0, in);
+          xb[i] = xn[i];
+          yb[i] = yn[i];
         }
+        fetch(u0 + CS_BWD_BATCH);
 #pragma unroll
         for (int i = 0; i < CS_BWD_BATCH; ++i) {
           const int64_t u = u0 + i;
@@ -380,12 +394,13 @@ dn_status check(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n
 // 16, so that short rows do not leave most lanes idle.
 int unit_lanes(int C) { return C / CS_CH >= 64 ? 64 : 16; }
 
-// Tokens of a run and rows of partial sums in the backward pass: 32 tokens
-// while that gives at most CS_MAX_ROWS rows, longer ones beyond.
+// Tokens of a run and rows of partial sums in the backward pass: 64 tokens where
+// that gives each SIMD its four waves (4 x 4096 tokens of 4096 channels: 90 us,
+// with 32 tokens 95 us), else 32, and longer ones beyond CS_MAX_ROWS rows.
 void bwd_plan(int64_t TT, int C, int &run, int &rows) {
-  const int64_t per = CS_THREADS / unit_lanes(C);
+  const int64_t per = CS_THREADS / unit_lanes(C), least = TT / 64 * (C / CS_CH) >= 4 * 1024 * 64 ? 64 : 32;
   int64_t r = (TT + CS_MAX_ROWS * per - 1) / (CS_MAX_ROWS * per);
-  r = r < 32 ? 32 : (r + 3) / 4 * 4;
+  r = r < least ? least : (r + 3) / 4 * 4;
   run = (int)r;
   rows = (int)((TT + r * per - 1) / (r * per));
 }
