@@ -180,6 +180,27 @@ def test_scan_repeats_bit_for_bit():
         assert all(torch.equal(gr[n], g2[n]) for n in gr)
 
 
+@pytest.mark.parametrize("B,T,H,G,dk,dv,lens", [
+    (4, 4096, 32, 1, 128, 64, None), (1, 16384, 16, 4, 64, 128, None), (2, 4096, 5, 5, 128, 192, None),
+    (1, 20000, 16, 2, 128, 128, [9000, 1, 64, 10000, 935])])
+def test_scan_repeats_at_full_size(B, T, H, G, dk, dv, lens):
+    """A matrix result read too early, or a missing barrier, shows as values that change between
+    runs of a full device."""
+    torch.manual_seed(7)
+    r = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    args = (r(B, T, G, dk).to(BF), r(B, T, G, dk).to(BF), r(B, T, H, dv).to(BF), r(B, T, H) - 3, -4 * torch.rand(H).cuda(),
+            r(H), r(H), r(len(lens) if lens else B, H, dk, dv))
+    dO, dhT, cu = r(B, T, H, dv).to(BF), torch.randn_like(args[-1]), cu_of(lens) if lens else None
+    first = None
+    for _ in range(8):
+        o, hT = dn.ssm_fwd(*args, cu)
+        out = dict(dn.ssm_bwd(*args, dO, dhT, cu), o=o, hT=hT)
+        first = first or out
+        for n in out:
+            assert torch.equal(out[n], first[n]), n
+    assert all(torch.isfinite(t).all() for t in first.values())
+
+
 # ------------------------------------------------------------ convolution
 
 CONVS = [
