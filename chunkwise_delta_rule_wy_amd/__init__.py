@@ -878,6 +878,13 @@ def gated_norm_bwd(x, z, w, dy, eps: float = 1e-5, gate_first: bool = False):
     return dx, dz, dw
 
 
+def _grad(t):
+    """An incoming gradient as the kernels take it: autograd may hand on any
+    view, also a contiguous slice that starts between 16-byte units."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class SsmScan(torch.autograd.Function):
     """Autograd wrapper: forward by ``ssm_fwd``, backward by ``ssm_bwd``."""
 
@@ -892,8 +899,8 @@ class SsmScan(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dhT):
         q, k, v, dt, A, dt_bias, skip, h0, cu = ctx.saved_tensors
-        dO = torch.zeros_like(v) if dO is None else dO.contiguous()
-        gr = ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, None if dhT is None else dhT.contiguous(), cu)
+        dO = torch.zeros_like(v) if dO is None else _grad(dO)
+        gr = ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, None if dhT is None else _grad(dhT), cu)
         return (gr["dq"], gr["dk"], gr["dv"], gr["ddt"], gr["dA"], gr["ddt_bias"], gr["dskip"],
                 None if h0 is None else gr["dh0"], None)
 
@@ -917,8 +924,8 @@ class ConvSilu(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dsT):
         x, w, bias, s0, cu = ctx.saved_tensors
-        dy = torch.zeros_like(x) if dy is None else dy.contiguous()
-        gr = conv_silu_bwd(x, w, bias, s0, dy, None if dsT is None else dsT.contiguous(), cu)
+        dy = torch.zeros_like(x) if dy is None else _grad(dy)
+        gr = conv_silu_bwd(x, w, bias, s0, dy, None if dsT is None else _grad(dsT), cu)
         return gr["dx"], gr["dw"], gr["dbias"], None if s0 is None else gr["ds0"], None
 
 
@@ -940,7 +947,7 @@ class GatedNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, z, w = ctx.saved_tensors
-        return (*gated_norm_bwd(x, z, w, dy.contiguous(), ctx.eps, ctx.gate_first), None, None)
+        return (*gated_norm_bwd(x, z, w, _grad(dy), ctx.eps, ctx.gate_first), None, None)
 
 
 def gated_norm_fn(x, z, w, eps: float = 1e-5, gate_first: bool = False):

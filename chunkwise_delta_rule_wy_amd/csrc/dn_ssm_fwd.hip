@@ -195,9 +195,9 @@ __global__ __launch_bounds__(Work<PAIR>::THREADS, 4) void ssm_sweep_kernel(SsmPa
 //
 // Start states of a sequence's segments from their own end states and decays,
 // in place, four state elements per thread; a sequence without tokens hands
-// its initial state on.  Bound by the latency of the segment states' loads, of
-// which four segments are on their way at a time (32 segments of 32 heads of
-// 128 x 64: 11 us for the 34 MB of states, read and written).
+// its initial state on.  Bound by the segment states' traffic, of which four
+// segments are on their way at a time (32 segments of 32 heads of 128 x 64: 34
+// MB read and written in 11 us, 6 TB/s; eight at a time take as long).
 constexpr int JOIN_THREADS = 256;
 
 __global__ __launch_bounds__(JOIN_THREADS) void ssm_join_kernel(SsmParams p, int dk) {

@@ -87,6 +87,17 @@ def test_scan_and_gradients(B, T, H, G, dk, dv, lens, state):
     check(dict(gr, o=o, hT=hT), val, bound, list(val))
 
 
+@pytest.mark.parametrize("B,T,H,G,dk,dv", [(256, 2, 12, 1, 64, 64), (130, 3, 22, 2, 128, 64), (86, 65, 9, 3, 64, 64)])
+def test_scan_many_heads_of_a_key(B, T, H, G, dk, dv):
+    # chunks enough that one workgroup passes through all heads of a group, in rounds of eight
+    x, dO, dhT, ls = scan_inputs(B, T, H, G, dk, dv, state=T < 60)
+    val, bound = reference(x, ls, dO, dhT)
+    d = cuda(x)
+    gr = dn.ssm_bwd(d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"], dO.cuda(),
+                    None if dhT is None else dhT.cuda())
+    check(gr, val, bound, [n for n in gr if n in val])
+
+
 @pytest.mark.parametrize("A,shift", [(0.0, 0.0), (-1e-4, 0.0), (-40.0, 3.0), (-1.0, -30.0), (-2000.0, 5.0)])
 def test_scan_extreme_decays(A, shift):
     # no decay, hardly any, one token's memory, vanishing steps, decays that underflow at once
@@ -433,6 +444,27 @@ def test_gradients_of_states_through_autograd():
     up = randn(1, 3, 1, 8, seed=3).cuda()
     sT.backward(up)
     assert torch.equal(xc.grad[0], up[0, 1:]) and torch.equal(s0.grad[0, 2], up[0, 0]) and not s0.grad[0, :2].any()
+
+
+def test_gradients_that_start_between_units():
+    # torch.cat hands its parts slices of one gradient, here an odd number of elements in
+    x, _, _, _ = scan_inputs(1, 70, 2, 1, 64, 64, state=False)
+    d = cuda(x)
+    leaves = [d[n].requires_grad_() for n in ("q", "k", "v", "dt", "A")]
+    w, wn = randn(2, 64, 4, seed=1).cuda(), randn(64, seed=2).cuda()
+    extra = torch.zeros(3, dtype=BF, device="cuda", requires_grad=True)
+    up = randn(70 * 128 + 3, seed=3, dtype=BF).cuda()
+
+    def outputs():
+        o, _ = dn.ssm_scan(*leaves, d["dt_bias"], d["skip"])
+        c, _ = dn.conv_silu_fn(leaves[2], w)
+        return o, c, dn.gated_norm_fn(leaves[2], leaves[2], wn)
+
+    for i in range(3):
+        got = torch.autograd.grad(torch.cat([extra, outputs()[i].flatten()]), leaves, up, allow_unused=True)
+        want = torch.autograd.grad(outputs()[i], leaves, up[3:].clone().view(1, 70, 2, 64), allow_unused=True)
+        assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(got, want))
+        assert got[2] is not None
 
 
 def test_other_stream_and_graph_replays():
