@@ -38,12 +38,12 @@ namespace dn {
 namespace {
 
 constexpr int GRAD_THREADS = 512;
-// Heads between two rounds in which every wave turns one head's sums into its
+// Heads between two pauses in which every wave turns one head's sums into its
 // scalar gradients and fills one of the next heads' gate tables: both are
 // long chains of a few lanes' work, which one wave for each of the two tasks
 // beside every head's products would make the kernel's pace (241 against 250
 // us, and 183 against 254 us without the loads, before the loads came early).
-constexpr int ROUND = GRAD_THREADS / 64;
+constexpr int BATCH = GRAD_THREADS / 64;
 
 template <int DK>
 struct GradLds {
@@ -54,11 +54,11 @@ struct GradLds {
   alignas(16) bf16 dO[CH * VS];
   alignas(16) bf16 dh[DK * VS];  // dh rounded, for K dh; at the end dG^T
   alignas(16) bf16 p[CH * VS];   // the head's P^T, zero above the diagonal blocks
-  GateTab tabs[ROUND];
+  GateTab tabs[BATCH];
   struct Sums {
     double hd[8];
     float pairs[4][CH], col_e[2][CH], diag_e[CH], qd[NT][CH], kd[NT][CH], diag[4];
-  } sums[ROUND];
+  } sums[BATCH];
 };
 
 template <int DK>
@@ -127,15 +127,15 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
       for (int i = 0; i < 2; ++i)
         x[kb][i] = ldg<f32x4>(states + at, state_off + chunk_state_unit<DK>(0, 2 * kb, 0, i));
   };
-  // the raw steps are loaded a round ahead
+  // the raw steps are loaded a batch of heads ahead
   float raw = 0.f;
   auto load_raw = [&](int hh) { raw = l < L ? raw_step(p, row0 + l, h_first + min(hh, heads - 1)) : 0.f; };
-  auto gates = [&](int hh) { fill_gates(s.tabs[hh % ROUND], raw, p.A[h_first + hh], L); };
+  auto gates = [&](int hh) { fill_gates(s.tabs[hh % BATCH], raw, p.A[h_first + hh], L); };
   // a head's sums over the waves and its scalar gradients
   auto finish = [&](int hh) {
     const int h = h_first + hh;
-    const GateTab &T = s.tabs[hh % ROUND];
-    const typename LD::Sums &x = s.sums[hh % ROUND];
+    const GateTab &T = s.tabs[hh % BATCH];
+    const typename LD::Sums &x = s.sums[hh % BATCH];
     float pairs = 0.f, qd = 0.f, kd = 0.f;
     double hd = 0.;
     for (int c = 0; c <= (l >> 4); ++c) pairs += x.pairs[c][l];
@@ -190,10 +190,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h_first + hh;
-    const int place = hh % ROUND;
+    const int place = hh % BATCH;
     const GateTab &T = s.tabs[place];
     typename LD::Sums &sums = s.sums[place];
-    if (place == 0) load_raw(hh + ROUND + w);
+    if (place == 0) load_raw(hh + BATCH + w);
     f32x4 M[2];
     M[0] = M[1] = zero4();
     double hd = 0.;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     hd += __shfl_xor(hd, 16, 64);
     hd += __shfl_xor(hd, 32, 64);
     if (l == 0) sums.hd[w] = hd;
-    if (place == ROUND - 1 || hh + 1 == heads) {
+    if (place == BATCH - 1 || hh + 1 == heads) {
       __syncthreads();
       if (w <= place) finish(hh - place + w);
       if (hh + 1 + w < heads) gates(hh + 1 + w);

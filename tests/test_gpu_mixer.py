@@ -89,7 +89,7 @@ def test_scan_and_gradients(B, T, H, G, dk, dv, lens, state):
 
 @pytest.mark.parametrize("B,T,H,G,dk,dv", [(256, 2, 12, 1, 64, 64), (130, 3, 22, 2, 128, 64), (86, 65, 9, 3, 64, 64)])
 def test_scan_many_heads_of_a_key(B, T, H, G, dk, dv):
-    # chunks enough that one workgroup passes through all heads of a group, in rounds of eight
+    # chunks enough that one workgroup passes through all heads of a group, eight at a time
     x, dO, dhT, ls = scan_inputs(B, T, H, G, dk, dv, state=T < 60)
     val, bound = reference(x, ls, dO, dhT)
     d = cuda(x)
