@@ -154,9 +154,12 @@ __device__ __forceinline__ float softplus(float x) {
   return (x < 0.f ? 0.f : x) + (d == 0.f ? y : __logf(u) * (y * __builtin_amdgcn_rcpf(d)));
 }
 
-// the raw step size of one (token, head): dt + dt_bias
-__device__ __forceinline__ float raw_step(const SsmParams &p, size_t row, int h) {
-  return p.dt[row * p.H + h] + (p.bias ? p.bias[h] : 0.f);
+// The step of lane l's token of a chunk of L > 0 tokens, before bias and
+// softplus; lanes from L on repeat the last token.  Loaded ahead of its use, with
+// nothing computed from it there: that would wait for it, and for all loads
+// before it.
+__device__ __forceinline__ float load_step(const SsmParams &p, size_t row0, int L, int h) {
+  return p.dt[(row0 + min(lane_id(), L - 1)) * p.H + h];
 }
 
 // inclusive prefix sum over the 64 lanes of a wave, in double
@@ -227,7 +230,7 @@ __device__ __forceinline__ double lane_val_d(double v, int lane) {
 struct GateTab {
   alignas(256) float s[CH];
   float bh[CH], bl[CH], gam[CH], w[CH], ws[CH];
-  float last, pad[3];
+  float last, A, skip, pad;  // A and skip: the gradient kernel's
 };
 // One wave fills the table from the raw step sizes of its lanes' tokens (lanes
 // from L on are padding: no decay, no input, gamma 0).  Returns the chunk's log2 decay.

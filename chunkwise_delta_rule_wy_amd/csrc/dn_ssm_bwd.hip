@@ -127,10 +127,23 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
       for (int i = 0; i < 2; ++i)
         x[kb][i] = ldg<f32x4>(states + at, state_off + chunk_state_unit<DK>(0, 2 * kb, 0, i));
   };
-  // the raw steps are loaded a batch of heads ahead
-  float raw = 0.f;
-  auto load_raw = [&](int hh) { raw = l < L ? raw_step(p, row0 + l, h_first + min(hh, heads - 1)) : 0.f; };
-  auto gates = [&](int hh) { fill_gates(s.tabs[hh % BATCH], raw, p.A[h_first + hh], L); };
+  // the steps and a head's parameters are loaded a batch of heads ahead
+  float dt = 0.f, bias = 0.f, A = 0.f, skip_next = 0.f;
+  auto load_gates = [&](int hh) {
+    const int h = h_first + min(hh, heads - 1);
+    dt = load_step(p, row0, L, h);
+    A = p.A[h];
+    if (p.bias) bias = p.bias[h];
+    if (p.skip) skip_next = p.skip[h];
+  };
+  auto gates = [&](int hh) {
+    GateTab &T = s.tabs[hh % BATCH];
+    fill_gates(T, dt + bias, A, L);
+    if (l == 0) {
+      T.A = A;
+      T.skip = skip_next;
+    }
+  };
   // a head's sums over the waves and its scalar gradients
   auto finish = [&](int hh) {
     const int h = h_first + hh;
@@ -154,18 +167,18 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     const double incl = wave_incl_scan_d(z);
     const float dlog =
         (float)((double)pairs + (l < 32 ? below : 0.) + (lane_val_d(incl, 63) - incl + z) + before + (double)T.last * hd);
-    const float ddt = (ds + p.A[h] * dlog) * -expm1f(-st);  // sigmoid(x) = 1 - exp(-softplus(x))
+    const float ddt = (ds + T.A * dlog) * -expm1f(-st);  // sigmoid(x) = 1 - exp(-softplus(x))
     if (l < L) p.ddt[(row0 + l) * p.H + h] = sign * ddt;
-    const float dA = wave_sum(st * dlog), db_sum = wave_sum(l < L ? ddt : 0.f);
+    const float dA_sum = wave_sum(st * dlog), db_sum = wave_sum(l < L ? ddt : 0.f);
     if (l == 0) {
       float *out = p.par_part + ((size_t)chunk * p.H + h) * 3;
-      out[0] = sign * dA;
+      out[0] = sign * dA_sum;
       out[1] = sign * db_sum;
       out[2] = sign * ((x.diag[0] + x.diag[1]) + (x.diag[2] + x.diag[3]));
     }
   };
 
-  load_raw(w);
+  load_gates(w);
   if (w < heads) gates(w);
   fetch_rows(h_first, 0);
   fetch_state(p.states, h_first, 0, hr);
@@ -193,11 +206,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     const int place = hh % BATCH;
     const GateTab &T = s.tabs[place];
     typename LD::Sums &sums = s.sums[place];
-    if (place == 0) load_raw(hh + BATCH + w);
+    if (place == 0) load_gates(hh + BATCH + w);
     f32x4 M[2];
     M[0] = M[1] = zero4();
     double hd = 0.;
-    const float skip = p.skip ? p.skip[h] : 0.f;
     for (int tile = 0; tile < p.ntiles; ++tile) {
       // what the next step needs (the last step loads its own again: a load that
       // may not take place would hold two sets of registers)
@@ -298,7 +310,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
       {
         f32x4 a[2], b[2];
         a[0] = a[1] = b[0] = b[1] = zero4();
-        const float wsj = T.ws[j];
+        const float wsj = T.ws[j], skip = T.skip;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           if (2 * kb + 1 < cb) continue;  // zeros

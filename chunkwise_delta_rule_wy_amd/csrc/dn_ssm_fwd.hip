@@ -105,22 +105,24 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
     for (int i = 0; i < SUBS; ++i)
       sy[i].load_clamped(Y + c * (CH * yp) + (size_t)wk.head[i] * p.DV + wk.col[i], 2 * (uint32_t)yp, L, tid);
   };
-  // wave i < TABS fills gate table i; the raw steps are loaded a chunk before
-  // they are needed
+  // wave i < TABS fills gate table i; the steps are loaded a chunk before they
+  // are needed
   const int gh = TABS == 2 && w == 1 ? wk.head[SUBS - 1] : wk.head[0];
-  const float A = p.A[gh];
+  const float A = p.A[gh], bias = p.bias ? p.bias[gh] : 0.f;
   double logd = 0.;
-  auto load_raw = [&](int i) {
-    const int c = at(i);
-    return l < min(CH, sg.len - c * CH) ? raw_step(p, sg.row + (size_t)c * CH + l, gh) : 0.f;
+  auto load_dt = [&](int i) {
+    const int c = at(min(i, nch - 1));
+    return load_step(p, sg.row + (size_t)c * CH, min(CH, sg.len - c * CH), gh);
   };
-  auto gates = [&](int i, float raw) { logd += fill_gates(lds.tabs[i & 1][w], raw, A, min(CH, sg.len - at(i) * CH)); };
+  auto gates = [&](int i, float dt) {
+    logd += fill_gates(lds.tabs[i & 1][w], dt + bias, A, min(CH, sg.len - at(i) * CH));
+  };
   if (nch > 0) fetch(at(0));
   float sign = 1.f;  // of the accumulators
-  float raw = 0.f;
+  float dt = 0.f;
   if (w < TABS && nch > 0) {
-    gates(0, load_raw(0));
-    if (nch > 1) raw = load_raw(1);
+    gates(0, load_dt(0));
+    dt = load_dt(1);
   }
   const uint32_t ax = lds_addr(lds.x), ay = lds_addr(lds.y);
   const typename XT::Col cx = XT::col_base(ax, l);
@@ -166,8 +168,8 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
       S[t] = acc;
     }
     if (w < TABS && i + 1 < nch) {
-      gates(i + 1, raw);
-      if (i + 2 < nch) raw = load_raw(i + 2);
+      gates(i + 1, dt);
+      dt = load_dt(i + 2);
     }
   }
   if (!STORE && w < TABS && l == 0 && wk.col[0] == 0) p.seg_decay[(size_t)wk.seg * p.H + gh] = logd;
@@ -316,18 +318,19 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
     for (int s = 0; s < SUBS; ++s) sv[s].load_clamped(p.v + vo[s] + c * (CH * vp), 2 * (uint32_t)vp, L, tid);
   };
   // wave i < TABS, which has the least of P to compute, fills gate table i; the
-  // raw steps are loaded a chunk before they are needed
+  // steps are loaded a chunk before they are needed
   const int gh = TABS == 2 && w == 1 ? wk.head[SUBS - 1] : wk.head[0];
-  const float A = p.A[gh];
-  auto load_raw = [&](int c) {
-    return l < min(CH, sg.len - c * CH) ? raw_step(p, sg.row + (size_t)c * CH + l, gh) : 0.f;
+  const float A = p.A[gh], bias = p.bias ? p.bias[gh] : 0.f;
+  auto load_dt = [&](int i) {
+    const int c = min(i, nch - 1);
+    return load_step(p, sg.row + (size_t)c * CH, min(CH, sg.len - c * CH), gh);
   };
-  auto gates = [&](int c, float raw) { fill_gates(lds.tabs[c & 1][w], raw, A, min(CH, sg.len - c * CH)); };
+  auto gates = [&](int c, float dt) { fill_gates(lds.tabs[c & 1][w], dt + bias, A, min(CH, sg.len - c * CH)); };
   if (nch > 0) fetch(0);
-  float raw = 0.f;
+  float dt = 0.f;
   if (w < TABS && nch > 0) {
-    gates(0, load_raw(0));
-    if (nch > 1) raw = load_raw(1);
+    gates(0, load_dt(0));
+    dt = load_dt(1);
   }
   const uint32_t aq = lds_addr(lds.q), ak = lds_addr(lds.k), av = lds_addr(lds.v), ap = lds_addr(lds.p);
   // the block right of an even diagonal block stays zero
@@ -375,8 +378,8 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
       }
     }
     if (w < TABS && c + 1 < nch) {
-      gates(c + 1, raw);
-      if (c + 2 < nch) raw = load_raw(c + 2);
+      gates(c + 1, dt);
+      dt = load_dt(c + 2);
     }
     __syncthreads();
 
