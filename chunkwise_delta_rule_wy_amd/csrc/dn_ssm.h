@@ -125,8 +125,9 @@ __device__ __forceinline__ bool segment(const SsmParams &p, int seg, Segment &s)
   s.len = s.last ? len - start : p.segc * CH;
   return true;
 }
-__device__ __forceinline__ int chunk_id(const SsmParams &p, const Segment &s, int c) {
-  return (p.cu ? p.chunk_base[s.n] : s.n * p.NC) + s.chunk + c;
+// its first chunk's number among all
+__device__ __forceinline__ int first_chunk(const SsmParams &p, const Segment &s) {
+  return (p.cu ? p.chunk_base[s.n] : s.n * p.NC) + s.chunk;
 }
 
 // A chunk's states lie in the workspace as the sweeps hold them: units of four

@@ -201,193 +201,199 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   for (int t = 0; t < NTT; ++t) dq[t] = dk[t] = zero4();
   const uint32_t aq = lds_addr(s.q), ak = lds_addr(s.k), ao = lds_addr(s.dO), ad = lds_addr(s.dh);
 
-  for (int hh = 0; hh < heads; ++hh) {
-    const int h = h_first + hh;
-    const int place = hh % BATCH;
+  f32x4 M[2];
+  double hd = 0.;
+  // over the heads and their tiles, in one loop: with one in the other, what a
+  // step loads for the next would be copied, and waited for, in between
+  for (int hh = 0, tile = 0;;) {
+    const int h = h_first + hh, place = hh % BATCH;
     const GateTab &T = s.tabs[place];
     typename LD::Sums &sums = s.sums[place];
-    if (place == 0) load_gates(hh + BATCH + w);
-    f32x4 M[2];
-    M[0] = M[1] = zero4();
-    double hd = 0.;
-    for (int tile = 0; tile < p.ntiles; ++tile) {
-      // what the next step needs (the last step loads its own again: a load that
-      // may not take place would hold two sets of registers)
-      const bool next_tile = tile + 1 < p.ntiles, more = next_tile || hh + 1 < heads;
-      const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
-      const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
-      __syncthreads();
-      // dO is zero behind the sequence; v's rows there meet gates of zero
-      static_assert(decltype(so)::NU == 1, "one unit a thread");
-      so.u[0] = (int)threadIdx.x / decltype(so)::UPR < L ? so.u[0] ^ flip : (u32x4)0u;
+    // what the next step needs (the last step loads its own again: a load that
+    // may not take place would hold two sets of registers)
+    const bool next_tile = tile + 1 < p.ntiles, more = next_tile || hh + 1 < heads;
+    const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
+    if (tile == 0) {
+      M[0] = M[1] = zero4();
+      hd = 0.;
+    }
+    const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
+    __syncthreads();
+    // dO is zero behind the sequence; v's rows there meet gates of zero
+    static_assert(decltype(so)::NU == 1, "one unit a thread");
+    so.u[0] = (int)threadIdx.x / decltype(so)::UPR < L ? so.u[0] ^ flip : (u32x4)0u;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) dr[x >> 1][x & 1] *= sign;
-      sv.template store<VS>(s.v);
-      so.template store<VS>(s.dO);
-      if (own_rows) {
-        float dot = 0.f;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          *reinterpret_cast<bf16x8 *>(s.dh + (n0 + m) * VS + 32 * kb + 8 * g) = bfrag<bf16>(dr[kb][0], dr[kb][1]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot += hr[kb][i >> 2][i & 3] * dr[kb][i >> 2][i & 3];
-        }
-        hd += (double)dot;
-      }
-      if (tile == 0) {
-        const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
-          if (rb < cb) continue;
-          const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
-          f32x4 P;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = computed(G[x][i] * (gm[i] * sj));
-            P[i] = r0 + i >= j ? v : 0.f;
-          }
-          *reinterpret_cast<bf16x4 *>(s.p + j * VS + r0) = cvt_bf16x4(P);
-        }
-      }
-      __syncthreads();
-      fetch_rows(nh, nt);
-      // h dO^T, then dh V^T: the wave's 16 Dk rows.  A state's registers are
-      // free after that for the next one, which arrives during the rest.
-      auto rows = [&](const f32x4 (&st)[2][2], const bf16 *ly, const bf16 *lx, const float *coef, f32x4 (&acc)[NTT],
-                      float *dots) {
-        f32x4 a[NTT];
-#pragma unroll
-        for (int t = 0; t < NTT; ++t) a[t] = zero4();
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          bf16x8 y[NTT];
-#pragma unroll
-          for (int t = 0; t < NTT; ++t) y[t] = frag_row(ly, VS, 16 * (tt0 + t) + m, 32 * kb + 8 * g);
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = st[kb][i >> 2][i & 3];
-          const Split sp = split3(x);
-#pragma unroll
-          for (int k = 2; k >= 0; --k)
-#pragma unroll
-            for (int t = 0; t < NTT; ++t) a[t] = mma32(a[t], sp.p[k], y[t]);
-        }
-        float dot[NTT];
-#pragma unroll
-        for (int t = 0; t < NTT; ++t) {
-          const int r = 16 * (tt0 + t) + m;
-          const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(lx + r * QS + n0 + 4 * g);
-          const float c = coef[r];
-          dot[t] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dot[t] += (float)xv[i] * a[t][i];
-            acc[t][i] += c * a[t][i];
-          }
-        }
-        const float sum = rows_sums(dot);
-        if (g < NTT) {
-          float *d = dots + 16 * (tt0 + g) + m;
-          *d = tile == 0 ? sum : *d + sum;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      rows(hr, s.dO, s.q, T.gam, dq, sums.qd[n0 / 16]);
-      fetch_state(p.states, nh, nt, hr);
-      rows(dr, s.v, s.k, T.ws, dk, sums.kd[n0 / 16]);
-      fetch_state(p.dstates, nh, nt, dr);
-      // M, the wave's row blocks
+    for (int x = 0; x < 4; ++x) dr[x >> 1][x & 1] *= sign;
+    sv.template store<VS>(s.v);
+    so.template store<VS>(s.dO);
+    if (own_rows) {
+      float dot = 0.f;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const bf16x8 vf = frag_row(s.v, VS, j, 32 * kb + 8 * g);
+        *reinterpret_cast<bf16x8 *>(s.dh + (n0 + m) * VS + 32 * kb + 8 * g) = bfrag<bf16>(dr[kb][0], dr[kb][1]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          M[x] = mma32(M[x], frag_row(s.dO, VS, 16 * (2 * half + x) + m, 32 * kb + 8 * g), vf);
+        for (int i = 0; i < 8; ++i) dot += hr[kb][i >> 2][i & 3] * dr[kb][i >> 2][i & 3];
+      }
+      hd += (double)dot;
+    }
+    if (tile == 0) {
+      const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
+        if (rb < cb) continue;
+        const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
+        f32x4 P;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = computed(G[x][i] * (gm[i] * sj));
+          P[i] = r0 + i >= j ? v : 0.f;
+        }
+        *reinterpret_cast<bf16x4 *>(s.p + j * VS + r0) = cvt_bf16x4(P);
+      }
+    }
+    __syncthreads();
+    if (tile == 0 && place == 0) load_gates(hh + BATCH + w);
+    fetch_rows(nh, nt);
+    // h dO^T, then dh V^T: the wave's 16 Dk rows.  A state's registers are
+    // free after that for the next one, which arrives during the rest.
+    auto rows = [&](const f32x4 (&st)[2][2], const bf16 *ly, const bf16 *lx, const float *coef, f32x4 (&acc)[NTT],
+                    float *dots) {
+      f32x4 a[NTT];
+#pragma unroll
+      for (int t = 0; t < NTT; ++t) a[t] = zero4();
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        bf16x8 y[NTT];
+#pragma unroll
+        for (int t = 0; t < NTT; ++t) y[t] = frag_row(ly, VS, 16 * (tt0 + t) + m, 32 * kb + 8 * g);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = st[kb][i >> 2][i & 3];
+        const Split sp = split3(x);
+#pragma unroll
+        for (int k = 2; k >= 0; --k)
+#pragma unroll
+          for (int t = 0; t < NTT; ++t) a[t] = mma32(a[t], sp.p[k], y[t]);
+      }
+      float dot[NTT];
+#pragma unroll
+      for (int t = 0; t < NTT; ++t) {
+        const int r = 16 * (tt0 + t) + m;
+        const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(lx + r * QS + n0 + 4 * g);
+        const float c = coef[r];
+        dot[t] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dot[t] += (float)xv[i] * a[t][i];
+          acc[t][i] += c * a[t][i];
+        }
+      }
+      const float sum = rows_sums(dot);
+      if (g < NTT) {
+        float *d = dots + 16 * (tt0 + g) + m;
+        *d = tile == 0 ? sum : *d + sum;
       }
       __builtin_amdgcn_sched_barrier(0);
-      // dv, token j, the wave's two column tiles
-      {
-        f32x4 a[2], b[2];
-        a[0] = a[1] = b[0] = b[1] = zero4();
-        const float wsj = T.ws[j], skip = T.skip;
+    };
+    rows(hr, s.dO, s.q, T.gam, dq, sums.qd[n0 / 16]);
+    fetch_state(p.states, nh, nt, hr);
+    rows(dr, s.v, s.k, T.ws, dk, sums.kd[n0 / 16]);
+    fetch_state(p.dstates, nh, nt, dr);
+    // M, the wave's row blocks
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          if (2 * kb + 1 < cb) continue;  // zeros
-          const bf16x8 pf = frag_row(s.p, VS, j, 32 * kb + 8 * g);
+    for (int kb = 0; kb < 2; ++kb) {
+      const bf16x8 vf = frag_row(s.v, VS, j, 32 * kb + 8 * g);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) a[x] = mma32(a[x], frag_tr(ao, 2 * VS, 32 * kb, 16 * (2 * half + x), l), pf);
-        }
-        mfma_settle();
+      for (int x = 0; x < 2; ++x)
+        M[x] = mma32(M[x], frag_row(s.dO, VS, 16 * (2 * half + x) + m, 32 * kb + 8 * g), vf);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // dv, token j, the wave's two column tiles
+    {
+      f32x4 a[2], b[2];
+      a[0] = a[1] = b[0] = b[1] = zero4();
+      const float wsj = T.ws[j], skip = T.skip;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const bf16x8 kf = frag_row(s.k, QS, j, 32 * kb + 8 * g);
+      for (int kb = 0; kb < 2; ++kb) {
+        if (2 * kb + 1 < cb) continue;  // zeros
+        const bf16x8 pf = frag_row(s.p, VS, j, 32 * kb + 8 * g);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) b[x] = mma32(b[x], frag_tr(ad, 2 * VS, 32 * kb, 16 * (2 * half + x), l), kf);
-        }
+        for (int x = 0; x < 2; ++x) a[x] = mma32(a[x], frag_tr(ao, 2 * VS, 32 * kb, 16 * (2 * half + x), l), pf);
+      }
+      mfma_settle();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int c = 16 * (2 * half + x) + 4 * g;
-          const bf16x4 ov = *reinterpret_cast<const bf16x4 *>(s.dO + j * VS + c);
-          f32x4 o;
+      for (int kb = 0; kb < KB; ++kb) {
+        const bf16x8 kf = frag_row(s.k, QS, j, 32 * kb + 8 * g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = sign * (a[x][i] + wsj * b[x][i] + skip * (float)ov[i]);
-          if (j < L)
+        for (int x = 0; x < 2; ++x) b[x] = mma32(b[x], frag_tr(ad, 2 * VS, 32 * kb, 16 * (2 * half + x), l), kf);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int c = 16 * (2 * half + x) + 4 * g;
+        const bf16x4 ov = *reinterpret_cast<const bf16x4 *>(s.dO + j * VS + c);
+        f32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = sign * (a[x][i] + wsj * b[x][i] + skip * (float)ov[i]);
+        if (j < L)
           stg<bf16x4>(p.dv + (row0 * p.H + h) * p.DV + tile * SSM_TILE, 2 * (j * (p.H * p.DV) + c), cvt_bf16x4(o));
+      }
+    }
+    if (!next_tile) {
+      // the head's sums over the 64 x 64 matrices; `below` sums a column's rows
+      // after the tile
+      const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
+      float below = 0.f, diag = 0.f, diag_e = 0.f;
+#pragma unroll
+      for (int x = 1; x >= 0; --x) {
+        const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
+        if (rb < cb) continue;
+        const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
+        f32x4 e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = computed(M[x][i] * gm[i]);
+          dG[x][i] += (r0 + i >= j ? v : 0.f) * sj;
+          const float u = computed(v * G[x][i]);
+          e[i] = r0 + i > j ? u : 0.f;
+          diag = r0 + i == j ? M[x][i] : diag;
+          diag_e = r0 + i == j ? u : diag_e;
         }
+        // over the rows from this one on
+        e[2] += e[3];
+        e[1] += e[2];
+        e[0] += e[1];
+        float after;
+        const float sum = row_suffix(e[0], g, after);
+        after += below;
+        below += sum;
+        f32x4 d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = r0 + i > j ? (e[i] + after) * sj : 0.f;
+        const float sums_m = row_sums16(d, m);
+        if (m < 4) sums.pairs[cb][r0 + m] = sums_m;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (g == 0) sums.col_e[half][j] = below;
+      if (half == cb / 2) {
+        diag_e = cross_row_sum(diag_e);
+        if (g == 0) sums.diag_e[j] = diag_e;
+        diag = wave_sum(diag);
+        if (l == 0) sums.diag[cb] = diag;
+      }
+      hd = row_sum16_d(hd);
+      hd += __shfl_xor(hd, 16, 64);
+      hd += __shfl_xor(hd, 32, 64);
+      if (l == 0) sums.hd[w] = hd;
+      if (place == BATCH - 1 || hh + 1 == heads) {
+        __syncthreads();
+        if (w <= place) finish(hh - place + w);
+        if (hh + 1 + w < heads) gates(hh + 1 + w);
       }
     }
-    // the head's sums over the 64 x 64 matrices; `below` sums a column's rows
-    // after the tile
-    const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
-    const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
-    float below = 0.f, diag = 0.f, diag_e = 0.f;
-#pragma unroll
-    for (int x = 1; x >= 0; --x) {
-      const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
-      if (rb < cb) continue;
-      const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
-      f32x4 e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = computed(M[x][i] * gm[i]);
-        dG[x][i] += (r0 + i >= j ? v : 0.f) * sj;
-        const float u = computed(v * G[x][i]);
-        e[i] = r0 + i > j ? u : 0.f;
-        diag = r0 + i == j ? M[x][i] : diag;
-        diag_e = r0 + i == j ? u : diag_e;
-      }
-      // over the rows from this one on
-      e[2] += e[3];
-      e[1] += e[2];
-      e[0] += e[1];
-      float after;
-      const float sum = row_suffix(e[0], g, after);
-      after += below;
-      below += sum;
-      f32x4 d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = r0 + i > j ? (e[i] + after) * sj : 0.f;
-      const float sums_m = row_sums16(d, m);
-      if (m < 4) sums.pairs[cb][r0 + m] = sums_m;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (g == 0) sums.col_e[half][j] = below;
-    if (half == cb / 2) {
-      diag_e = cross_row_sum(diag_e);
-      if (g == 0) sums.diag_e[j] = diag_e;
-      diag = wave_sum(diag);
-      if (l == 0) sums.diag[cb] = diag;
-    }
-    hd = row_sum16_d(hd);
-    hd += __shfl_xor(hd, 16, 64);
-    hd += __shfl_xor(hd, 32, 64);
-    if (l == 0) sums.hd[w] = hd;
-    if (place == BATCH - 1 || hh + 1 == heads) {
-      __syncthreads();
-      if (w <= place) finish(hh - place + w);
-      if (hh + 1 + w < heads) gates(hh + 1 + w);
-    }
+    if (!more) break;
+    hh += next_tile ? 0 : 1;
+    tile = nt;
   }
 
   // dG^T into LDS (rows j, row blocks above the diagonal zero), then its

@@ -118,6 +118,7 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
     logd += fill_gates(lds.tabs[i & 1][w], dt + bias, A, min(CH, sg.len - at(i) * CH));
   };
   if (nch > 0) fetch(at(0));
+  const int chunk0 = STORE ? first_chunk(p, sg) : 0;
   float sign = 1.f;  // of the accumulators
   float dt = 0.f;
   if (w < TABS && nch > 0) {
@@ -138,7 +139,7 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
     fetch(at(min(i + 1, nch - 1)));  // without a branch, which would hold two sets of registers
     const typename XT::Col bx = {fresh(cx.a), fresh(cx.b)};
     if (STORE) {
-      float *dst = (REV ? p.dstates : p.states) + ((size_t)chunk_id(p, sg, c) * p.H + head) * per_state + col * DK;
+      float *dst = (REV ? p.dstates : p.states) + ((size_t)(chunk0 + c) * p.H + head) * per_state + col * DK;
 #pragma unroll
       for (int t = 0; t < NT; ++t) stg<f32x4>(dst, chunk_state_unit<DK>(t, 0, m, g), sign * S[t]);
     }
