@@ -111,7 +111,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     st.template store<QS>(s.k);
   }
   Stage<CH, SSM_TILE, GRAD_THREADS> sv, so;
-  f32x4 hr[2][2], dr[2][2];  // the wave's rows of h and dh: [32-column block][half of 8 columns]
+  f32x4 hr[2][2], dr[2][2], dr_next[2][2];  // the wave's rows of h and dh: [32-column block][half of 8 columns]
   const uint32_t state_off = chunk_state_unit<DK>(n0 / 16, g >> 1, m, 2 * (g & 1));
   auto fetch_rows = [&](int h, int tile) {
     const size_t off = (row0 * p.H + h) * p.DV + tile * SSM_TILE;
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   if (w < heads) gates(w);
   fetch_rows(h_first, 0);
   fetch_state(p.states, h_first, 0, hr);
-  fetch_state(p.dstates, h_first, 0, dr);
+  fetch_state(p.dstates, h_first, 0, dr_next);
   __syncthreads();
 
   // G: tiles of rows r (four per lane), column j
@@ -201,29 +201,18 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   for (int t = 0; t < NTT; ++t) dq[t] = dk[t] = zero4();
   const uint32_t aq = lds_addr(s.q), ak = lds_addr(s.k), ao = lds_addr(s.dO), ad = lds_addr(s.dh);
 
-  f32x4 M[2];
+  f32x4 M[2], gm[2];  // M and Gamma of the head, the wave's blocks
   double hd = 0.;
-  // over the heads and their tiles, in one loop: with one in the other, what a
-  // step loads for the next would be copied, and waited for, in between
-  for (int hh = 0, tile = 0;;) {
-    const int h = h_first + hh, place = hh % BATCH;
-    const GateTab &T = s.tabs[place];
-    typename LD::Sums &sums = s.sums[place];
-    // what the next step needs (the last step loads its own again: a load that
-    // may not take place would hold two sets of registers)
-    const bool next_tile = tile + 1 < p.ntiles, more = next_tile || hh + 1 < heads;
-    const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
-    if (tile == 0) {
-      M[0] = M[1] = zero4();
-      hd = 0.;
-    }
-    const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
-    __syncthreads();
+  // A step's rows, dh and, for a head's first tile, P go to LDS (at the end of the
+  // step that loads them, which takes 30 registers less than at the start of
+  // the next).
+  auto stage = [&](int hh, int tile, int l) {
+    const int g = l >> 4, m = l & 15, j = 16 * cb + m;
     // dO is zero behind the sequence; v's rows there meet gates of zero
     static_assert(decltype(so)::NU == 1, "one unit a thread");
     so.u[0] = (int)threadIdx.x / decltype(so)::UPR < L ? so.u[0] ^ flip : (u32x4)0u;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) dr[x >> 1][x & 1] *= sign;
+    for (int x = 0; x < 4; ++x) dr[x >> 1][x & 1] = sign * dr_next[x >> 1][x & 1];
     sv.template store<VS>(s.v);
     so.template store<VS>(s.dO);
     if (own_rows) {
@@ -234,29 +223,46 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) dot += hr[kb][i >> 2][i & 3] * dr[kb][i >> 2][i & 3];
       }
-      hd += (double)dot;
+      hd = tile == 0 ? (double)dot : hd + (double)dot;
     }
     if (tile == 0) {
+      const GateTab &T = s.tabs[hh % BATCH];
       const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
         if (rb < cb) continue;
-        const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
+        gm[x] = decay_ratios(T, r0, bhj, blj, 1.f);
         f32x4 P;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float v = computed(G[x][i] * (gm[i] * sj));
+          const float v = computed(G[x][i] * (gm[x][i] * sj));
           P[i] = r0 + i >= j ? v : 0.f;
         }
         *reinterpret_cast<bf16x4 *>(s.p + j * VS + r0) = cvt_bf16x4(P);
       }
     }
     __syncthreads();
+  };
+  gm[0] = gm[1] = zero4();
+  stage(0, 0, l);
+  // over the heads and their tiles, in one loop: with one in the other, what a
+  // step loads for the next would be copied, and waited for, in between
+  for (int hh = 0, tile = 0;;) {
+    const int h = h_first + hh, place = hh % BATCH;
+    const GateTab &T = s.tabs[place];
+    typename LD::Sums &sums = s.sums[place];
+    // what the next step needs (the last step loads its own again: a load that
+    // may not take place would hold two sets of registers)
+    const bool next_tile = tile + 1 < p.ntiles, more = next_tile || hh + 1 < heads;
+    const int nh = next_tile || !more ? h : h + 1, nt = next_tile ? tile + 1 : more ? 0 : tile;
+    if (tile == 0) M[0] = M[1] = zero4();
+    const int l = fresh(lane), g = l >> 4, m = l & 15, j = 16 * cb + m;
     if (tile == 0 && place == 0) load_gates(hh + BATCH + w);
     fetch_rows(nh, nt);
-    // h dO^T, then dh V^T: the wave's 16 Dk rows.  A state's registers are
-    // free after that for the next one, which arrives during the rest.
+    fetch_state(p.dstates, nh, nt, dr_next);
+    // h dO^T, then dh V^T: the wave's 16 Dk rows.  h's registers are free after
+    // that for the next one, which arrives during the rest.
     auto rows = [&](const f32x4 (&st)[2][2], const bf16 *ly, const bf16 *lx, const float *coef, f32x4 (&acc)[NTT],
                     float *dots) {
       f32x4 a[NTT];
@@ -299,7 +305,6 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     rows(hr, s.dO, s.q, T.gam, dq, sums.qd[n0 / 16]);
     fetch_state(p.states, nh, nt, hr);
     rows(dr, s.v, s.k, T.ws, dk, sums.kd[n0 / 16]);
-    fetch_state(p.dstates, nh, nt, dr);
     // M, the wave's row blocks
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -342,17 +347,16 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     if (!next_tile) {
       // the head's sums over the 64 x 64 matrices; `below` sums a column's rows
       // after the tile
-      const float bhj = T.bh[j], blj = T.bl[j], sj = T.s[j];
+      const float sj = T.s[j];
       float below = 0.f, diag = 0.f, diag_e = 0.f;
 #pragma unroll
       for (int x = 1; x >= 0; --x) {
         const int rb = 2 * half + x, r0 = 16 * rb + 4 * g;
         if (rb < cb) continue;
-        const f32x4 gm = decay_ratios(T, r0, bhj, blj, 1.f);
         f32x4 e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float v = computed(M[x][i] * gm[i]);
+          const float v = computed(M[x][i] * gm[x][i]);
           dG[x][i] += (r0 + i >= j ? v : 0.f) * sj;
           const float u = computed(v * G[x][i]);
           e[i] = r0 + i > j ? u : 0.f;
@@ -394,6 +398,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     if (!more) break;
     hh += next_tile ? 0 : 1;
     tile = nt;
+    __syncthreads();
+    stage(hh, tile, fresh(lane));
   }
 
   // dG^T into LDS (rows j, row blocks above the diagonal zero), then its
