@@ -85,7 +85,7 @@ Plan plan_of(const dn_ssm_shape *s, bool packed, bool backward) {
 
 // Sets of a group's heads for the gradient kernel: one workgroup per CU where
 // the heads give as many, since every set costs a start and a share of fp32
-// partial sums (4 x 4096 tokens, 32 heads: 214 us with one set, 252 us with
+// partial sums (4 x 4096 tokens, 32 heads: 198 us with one set, 234 us with
 // four, their sums included).
 void sets_of(const dn_ssm_shape *s, const Plan &pl, int &sets, int &heads) {
   const int64_t R = s->H / s->G, wgs = pl.nchunks * s->G;

@@ -26,12 +26,12 @@
 // and dG only the row blocks 2 half, 2 half + 1, and of dv the columns' half;
 // for dq and dk a wave owns 16 of the Dk rows.
 //
-// 245 registers allow two waves on a SIMD, one workgroup on a CU, so that what
+// 227 registers allow two waves on a SIMD, one workgroup on a CU, so that what
 // the next head needs is loaded as soon as its registers are free and without
-// a branch.  4 x 4096 tokens, 32 heads of 128 x 64 (256 workgroups): 214 us.
-// The states (537 MB) and v, dO, dv (201 MB) pass at 3.4 TB/s; without the loads
-// the rest takes 177 us, without most of the products the loads take 192 us,
-// so that neither hides the other entirely.
+// a branch.  4 x 4096 tokens, 32 heads of 128 x 64 (256 workgroups): 198 us.
+// Bound by the reads of the states (537 MB; with v, dO and dv 738 MB at 3.7 TB/s,
+// where a plain sum over a large array reads 3.9 TB/s): without most of the
+// products it takes 188 us, without the loads 172 us.
 #include "dn_ssm.h"
 
 namespace dn {
