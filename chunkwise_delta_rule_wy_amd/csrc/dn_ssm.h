@@ -61,7 +61,7 @@ struct SsmParams {
   bf16 *dq, *dk, *dv;
   float *dq_part, *dk_part;  // fp32 partial sums over sets of heads, or null
   float *ddt, *dA, *ddt_bias, *dskip, *dh0;  // ddt_bias, dskip, dh0 may be null
-  float *par_part;           // [chunk][H][3]: dA, ddt_bias, dskip
+  double *par_part;          // [chunk][H][3]: dA, ddt_bias, dskip
   int64_t rows;              // B T
   int T, H, G, DV, N;
   int ntiles;                // Dv / 64
@@ -141,18 +141,44 @@ __device__ __forceinline__ uint32_t chunk_state_unit(int t, int c, int m, int u)
   return 16 * (((c * (DK / 16) + t) * 16 + m) * 4 + u);
 }
 
-// e^x with the rounding of x log2(e) put back, which would cost |x| 2^-24
+// e^x for -200 <= x <= 0: 2^n e^r, x = n ln 2 + r with ln 2 in two parts (the
+// first has 16 bits, so that its product with n is exact), e^r by its series
+// up to r^7 / 7! (|r| < 0.35: the rest is below 2^-25 of r).
 __device__ __forceinline__ float exp_of(float x) {
-  const float t = x * wy::LOG2E, r = __builtin_fmaf(x, wy::LOG2E, -t) + x * 1.925963033e-8f;
-  return wy::fexp2(t) * __builtin_fmaf(r, 0.6931471806f, 1.f);
+  const float n = __builtin_rintf(x * wy::LOG2E);
+  float r = __builtin_fmaf(n, -0.693145751953125f, x);
+  r = __builtin_fmaf(n, -1.428606765330187e-06f, r);
+  float p = 1.f / 5040;
+  p = __builtin_fmaf(p, r, 1.f / 720);
+  p = __builtin_fmaf(p, r, 1.f / 120);
+  p = __builtin_fmaf(p, r, 1.f / 24);
+  p = __builtin_fmaf(p, r, 1.f / 6);
+  p = __builtin_fmaf(p, r, 0.5f);
+  return __builtin_ldexpf(1.f + __builtin_fmaf(p * r, r, r), (int)n);
 }
-// log(1 + e^x) = max(x, 0) + log1p(e^-|x|); log1p(y) = y log(u) / (u - 1) with
-// u the rounded 1 + y, whose rounding the quotient takes back.  The largest
+// log(1 + e^x) = max(x, 0) + log1p(y), y = e^-|x|; log1p(y) = 2 atanh z with z =
+// y / (2 + y) <= 1/3, by the series 2 (z + z^3 / 3 + ...  + z^15 / 15).  The
+// quotient is corrected for its own rounding and for that of 2 + y.  A step size
+// is off by 4e-8 on average and without a bias (below 1e-8 of it): one that all
+// tokens share does not cancel in dA as the tokens' terms may.  The largest
 // negative steps, minus infinity among them, give 0; NaN stays NaN.
 __device__ __forceinline__ float softplus(float x) {
   const float n = -fabsf(x);
-  const float y = exp_of(n < -200.f ? -200.f : n), u = 1.f + y, d = u - 1.f;
-  return (x < 0.f ? 0.f : x) + (d == 0.f ? y : __logf(u) * (y * __builtin_amdgcn_rcpf(d)));
+  const float y = exp_of(n < -200.f ? -200.f : n), d = 2.f + y, e = y - (d - 2.f);
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  float z = y * r;
+  z = __builtin_fmaf(__builtin_fmaf(-e, z, __builtin_fmaf(-d, z, y)), r, z);
+  const float q = z * z;
+  float s = 1.f / 15;
+  s = __builtin_fmaf(s, q, 1.f / 13);
+  s = __builtin_fmaf(s, q, 1.f / 11);
+  s = __builtin_fmaf(s, q, 1.f / 9);
+  s = __builtin_fmaf(s, q, 1.f / 7);
+  s = __builtin_fmaf(s, q, 1.f / 5);
+  s = __builtin_fmaf(s, q, 1.f / 3);
+  z += z;
+  return (x < 0.f ? 0.f : x) + __builtin_fmaf(z * q, s, z);
 }
 
 // The step of lane l's token of a chunk of L > 0 tokens, before bias and

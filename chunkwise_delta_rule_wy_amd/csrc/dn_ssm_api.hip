@@ -118,7 +118,7 @@ Layout layout_of(const dn_ssm_shape *s, const Plan &pl, bool packed, bool backwa
   if (backward) {
     L.states = take((size_t)pl.nchunks * st);
     L.dstates = take((size_t)pl.nchunks * st);
-    L.part = take(12 * (size_t)pl.nchunks * s->H);
+    L.part = take(24 * (size_t)pl.nchunks * s->H);
     int sets, heads;
     sets_of(s, pl, sets, heads);
     if (sets > 1) {
@@ -181,7 +181,7 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
   if (backward) {
     p.states = reinterpret_cast<float *>(base + L.states);
     p.dstates = reinterpret_cast<float *>(base + L.dstates);
-    p.par_part = reinterpret_cast<float *>(base + L.part);
+    p.par_part = reinterpret_cast<double *>(base + L.part);
     if (p.sets > 1) {
       p.dq_part = reinterpret_cast<float *>(base + L.dq_part);
       p.dk_part = reinterpret_cast<float *>(base + L.dk_part);

@@ -165,16 +165,17 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
     const double su = (double)st * wu, low = (double)st * x.col_e[1][l], z = (double)(T.gam[l] * qd);
     const double before = wave_incl_scan_d(su) - su, below = wave_incl_scan_d(low) - low;
     const double incl = wave_incl_scan_d(z);
-    const float dlog =
-        (float)((double)pairs + (l < 32 ? below : 0.) + (lane_val_d(incl, 63) - incl + z) + before + (double)T.last * hd);
-    const float ddt = (ds + T.A * dlog) * -expm1f(-st);  // sigmoid(x) = 1 - exp(-softplus(x))
+    const double dlog =
+        (double)pairs + (l < 32 ? below : 0.) + (lane_val_d(incl, 63) - incl + z) + before + (double)T.last * hd;
+    const float ddt = (ds + T.A * (float)dlog) * -expm1f(-st);  // sigmoid(x) = 1 - exp(-softplus(x))
     if (l < L) p.ddt[(row0 + l) * p.H + h] = sign * ddt;
-    const float dA_sum = wave_sum(st * dlog), db_sum = wave_sum(l < L ? ddt : 0.f);
-    if (l == 0) {
-      float *out = p.par_part + ((size_t)chunk * p.H + h) * 3;
+    // the parameters' sums, which all tokens enter, in double from here on
+    const double dA_sum = wave_incl_scan_d((double)st * dlog), db_sum = wave_incl_scan_d(l < L ? (double)ddt : 0.);
+    if (l == 63) {
+      double *out = p.par_part + ((size_t)chunk * p.H + h) * 3;
       out[0] = sign * dA_sum;
       out[1] = sign * db_sum;
-      out[2] = sign * ((x.diag[0] + x.diag[1]) + (x.diag[2] + x.diag[3]));
+      out[2] = sign * (((double)x.diag[0] + x.diag[1]) + ((double)x.diag[2] + x.diag[3]));
     }
   };
 
