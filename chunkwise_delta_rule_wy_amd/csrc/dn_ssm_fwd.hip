@@ -47,11 +47,11 @@ int work_items(const SsmParams &p) {
 // on average (by some 2^-25 of their size), and an error of one sign in the
 // states would add up in dA, where it reached 2e-6 of the result.
 //
-// Measured at 4 x 4096 tokens, 32 heads of 128 x 64: without STORE 38 us
+// Measured at 4 x 4096 tokens, 32 heads of 128 x 64: without STORE 37 us
 // forwards (8 segments a sequence) and 62 us both ways (4 segments), bound by
 // issue (a SIMD issues matrix and vector instructions by turns: 260 vector
-// ones a chunk, half of them split3, beside 48 products); with STORE both ways 140 us, 537 MB of
-// states and 150 MB of inputs at 4.9 TB/s.
+// ones a chunk, half of them split3, beside 48 products); with STORE both ways 136 us, 537 MB of
+// states and 150 MB of inputs at 5.1 TB/s.
 template <int DK, int PAIR>
 struct SweepLds {
   static constexpr int YC = SSM_TILE * Work<PAIR>::SUBS;
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void ssm_join_kernel(SsmParams p, int
 // Bound by issue: a chunk of two heads costs a wave 150 products, 96 of them the
 // state update in three parts, and some 900 vector instructions, and the two
 // kinds share a SIMD's turns (77 % of the cycles; twice the waves of half the
-// work each spill).  4 x 4096 tokens, 32 heads of 128 x 64: 73 us.
+// work each spill).  4 x 4096 tokens, 32 heads of 128 x 64: 71 us.
 template <int DK, int PAIR>
 struct FwdLds {
   static constexpr int VC = SSM_TILE * Work<PAIR>::SUBS;
