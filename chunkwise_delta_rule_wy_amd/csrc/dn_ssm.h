@@ -133,9 +133,9 @@ __device__ __forceinline__ int first_chunk(const SsmParams &p, const Segment &s)
 // A chunk's states lie in the workspace as the sweeps hold them: units of four
 // columns, in the order [block of 16 columns][block of 16 Dk rows][row][unit],
 // so that a wave's store is 1 KiB in one piece (4 x 4096 tokens, 32 heads, 128 x
-// 64: the storing sweeps take 140 us and the gradient kernel, which reads
-// them, 250 us; with rows of Dv columns 178 and 270 us).  The byte offset of a
-// unit.
+// 64: the storing sweeps took 140 us and the gradient kernel, which reads them
+// and has become faster since, 250 us; with rows of Dv columns 178 and 270 us).
+// The byte offset of a unit.
 template <int DK>
 __device__ __forceinline__ uint32_t chunk_state_unit(int t, int c, int m, int u) {
   return 16 * (((c * (DK / 16) + t) * 16 + m) * 4 + u);
