@@ -553,6 +553,21 @@ def test_scan_masked_steps_and_vanishing_decays():
     check(dict(gr, o=o, hT=hT), val, {k: b + 1e-37 for k, b in bound.items()}, list(val))
 
 
+def test_step_sizes():
+    # a first token with k = v = 1 leaves s in the state: within 6 half steps of fp32 (exponential 2,
+    # its quotient and series 1.2 each, the sum with the step 1, rounded up) and without a bias
+    dt = torch.cat([torch.linspace(-80, 30, 4000), torch.linspace(-8, 2, 4192)]).reshape(1024, 8).cuda()
+    state = torch.zeros(1024, 8, 64, 64, device="cuda")
+    one = torch.ones(1024, 8, 64, device="cuda")
+    dn.ssm_step(one[:, :1].contiguous(), one[:, :1].contiguous(), one, dt, -torch.ones(8).cuda(), None, None, state)
+    want = ref.softplus(dt.double())
+    err = (state[:, :, 0, 0].double() - want) / want
+    assert err.abs().max() <= 6 * ref.U32
+    # the mean of n independent roundings is off by some 6 U32 / sqrt(n); four times that
+    assert err.mean().abs() <= 4 * 6 * ref.U32 / 8192 ** 0.5
+    assert torch.equal(state, state[:, :, :1, :1].expand_as(state))
+
+
 def test_scan_of_a_pack_without_tokens():
     x, _, dhT, _ = scan_inputs(1, 0, 6, 2, 64, 128, lens=[0, 0, 0])
     d, cu = cuda(x), cu_of([0, 0, 0])
