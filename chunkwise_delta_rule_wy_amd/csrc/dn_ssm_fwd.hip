@@ -173,7 +173,10 @@ __device__ __forceinline__ void sweep(const SsmParams &p, SweepLds<DK, PAIR> &ld
       dt = load_dt(i + 2);
     }
   }
-  if (!STORE && w < TABS && l == 0 && wk.col[0] == 0) p.seg_decay[(size_t)wk.seg * p.H + gh] = logd;
+  // One writer an entry: the two directions run side by side and add the chunks in
+  // opposite orders, so that the sums may differ in their last bit.  The reverse
+  // sweep writes the last segment's, which the forward one skips.
+  if (!STORE && w < TABS && l == 0 && wk.col[0] == 0 && (!REV || sg.last)) p.seg_decay[(size_t)wk.seg * p.H + gh] = logd;
   float *dst = nullptr;
   if (!STORE) dst = p.seg_state[REV] + ((size_t)wk.seg * p.H + head) * per_state;
   else if (REV && sg.first && p.dh0) dst = p.dh0 + ((size_t)sg.n * p.H + head) * per_state;
