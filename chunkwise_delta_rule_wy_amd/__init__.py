@@ -32,6 +32,7 @@ __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_noalloc", "bwd_workspace_bytes",
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdn.so")
 
 DN_F32, DN_BF16 = 0, 1
+DN_ZERO_TAIL = 0x100
 _DTYPES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
 
 
@@ -695,13 +696,13 @@ def ssm_fwd(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None, o
     float32 (dt_bias, skip None: zero); h0 ``[N,H,Dk,Dv]`` float32 or None;
     cu_seqlens int32 ``[N+1]`` on the device for packed sequences (B == 1),
     from 0 to T; where it ends before T, the rows behind it are not used, and
-    theirs in the results are not set.  Returns ``(o, hT)`` (hT None unless
+    theirs in the results are zero.  Returns ``(o, hT)`` (hT None unless
     output_final_state)."""
     lib = load_library()
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
     _is(h0, "h0", torch.float32, (N, H, Dk, Dv), dev)
-    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
+    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16 | DN_ZERO_TAIL))
     o = torch.empty_like(v)
     hT = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev) if output_final_state else None
     wsb = lib.dn_ssm_fwd_workspace(s)
@@ -714,7 +715,8 @@ def ssm_fwd(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None, o
 def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
     """Backward pass of ``<dO, o> + <dhT, hT>`` of ``ssm_fwd`` (``dn_ssm_bwd``;
     the states are recomputed).  Returns a dict: dq, dk, dv in bfloat16, ddt,
-    dA, ddt_bias, dskip (None without the parameter) and dh0 in float32."""
+    dA, ddt_bias, dskip (None without the parameter) and dh0 in float32; rows
+    behind the last packed sequence are zero."""
     lib = load_library()
     dev, (B, T), H, G, Dk, Dv = _ssm_args(q, k, v, dt, A, dt_bias, skip, (torch.bfloat16,), 4)
     N = _seqs(B, cu_seqlens, dev)
@@ -722,7 +724,7 @@ def ssm_bwd(q, k, v, dt, A, dt_bias, skip, h0, dO, dhT=None, cu_seqlens=None):
     _given(dO=dO)
     _is(dO, "dO", v.dtype, tuple(v.shape), dev)
     _is(dhT, "dhT", torch.float32, (N, H, Dk, Dv), dev)
-    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16))
+    s = ctypes.byref(_SsmShape(B, T, H, G, Dk, Dv, N, DN_BF16 | DN_ZERO_TAIL))
     gr = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), ddt=torch.empty_like(dt),
               dA=torch.empty_like(A), ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias),
               dskip=None if skip is None else torch.empty_like(skip),
@@ -784,7 +786,7 @@ def conv_silu(x, w, bias=None, s0=None, cu_seqlens=None):
     dev, (B, T), H, D, W, N = _conv_silu_args(x, w, bias, s0, cu_seqlens, 4)
     y = torch.empty_like(x)
     sT = x.new_empty((N, max(W - 1, 0), H, D)) if s0 is None else torch.empty_like(s0)
-    _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(s0),
+    _call("dn_conv_silu", dev, B, T, H, D, W, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(w), _adr(bias), _adr(s0),
           _adr(cu_seqlens), _adr(y), _adr(sT))
     return y, sT
 
@@ -801,7 +803,7 @@ def conv_silu_bwd(x, w, bias, s0, dy, dsT=None, cu_seqlens=None):
               ds0=torch.empty((N, max(W - 1, 0), H, D), dtype=x.dtype, device=dev))
     wsb = load_library().dn_conv_silu_bwd_workspace(B, T, H, D, W)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_conv_silu_bwd", dev, B, T, H, D, W, N, _DTYPES[x.dtype], _adr(x), _adr(w), _adr(bias), _adr(s0),
+    _call("dn_conv_silu_bwd", dev, B, T, H, D, W, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(w), _adr(bias), _adr(s0),
           _adr(cu_seqlens), _adr(dy), _adr(dsT), *[_adr(g) for g in gr.values()], _adr(ws), wsb)
     return gr
 
@@ -906,7 +908,8 @@ class SsmScan(torch.autograd.Function):
 
 
 def ssm_scan(q, k, v, dt, A, dt_bias=None, skip=None, h0=None, cu_seqlens=None):
-    """Differentiable selective state space scan; returns (o, hT)."""
+    """Differentiable selective state space scan; returns (o, hT).  Rows behind the
+    last packed sequence give zeros and get zero gradients."""
     return SsmScan.apply(q, k, v, dt, A, dt_bias, skip, h0, cu_seqlens)
 
 
@@ -930,7 +933,8 @@ class ConvSilu(torch.autograd.Function):
 
 
 def conv_silu_fn(x, w, bias=None, s0=None, cu_seqlens=None):
-    """Differentiable ``conv_silu``; returns (y, sT)."""
+    """Differentiable ``conv_silu``; returns (y, sT).  Rows behind the last packed
+    sequence give zeros and get zero gradients."""
     return ConvSilu.apply(x, w, bias, s0, cu_seqlens)
 
 

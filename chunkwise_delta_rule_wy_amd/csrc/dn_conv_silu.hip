@@ -44,6 +44,7 @@ struct ConvSiluParams {
   int64_t TT;
   int T, N, C, W, run;
   int runs, rows;
+  int zero_tail;  // packed: clear the rows of y or dx behind the last sequence
 };
 
 // a row's CS_CH channels as they are in memory
@@ -76,6 +77,15 @@ __device__ __forceinline__ void store8(E *dst, const float (&x)[CS_CH]) {
 #pragma unroll
   for (int e = 0; e < CS_CH; ++e) v[e] = to_e<E>(x[e]);
   *reinterpret_cast<V *>(dst) = v;
+}
+// a thread's channels of those of a result's rows [t, end) that are behind the
+// last sequence; called before a run holds anything in registers (behind its
+// loop the backward pass spills)
+template <typename E>
+__device__ __forceinline__ void clear_tail(const ConvSiluParams &p, void *result, int64_t t, int64_t end, int c0) {
+  if (!p.zero_tail) return;
+  typedef E V __attribute__((ext_vector_type(CS_CH)));
+  for (t = max(t, (int64_t)p.cu[p.N]); t < end; ++t) *reinterpret_cast<V *>(static_cast<E *>(result) + t * p.C + c0) = V{};
 }
 __device__ __forceinline__ void zero8(float (&x)[CS_CH]) {
 #pragma unroll
@@ -174,12 +184,13 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
     if (run < (uint32_t)(p.runs + p.N)) pass_state<E, W>(p, run - p.runs, c0, p.s0, p.sT);
     return;
   }
+  int64_t t = (int64_t)run * p.run;
+  const int64_t t1 = min(t + p.run, p.TT);
+  clear_tail<E>(p, p.y, t, t1, c0);
   const E *x = static_cast<const E *>(p.x);
   E *y = static_cast<E *>(p.y), *sT = static_cast<E *>(p.sT);
   float w[W][CS_CH], bias[CS_CH], h[W > 1 ? W - 1 : 1][CS_CH];
   load_weights<W>(p.w, p.bias, c0, w, bias);
-  int64_t t = (int64_t)run * p.run;
-  const int64_t t1 = min(t + p.run, p.TT);
   while (t < t1) {
     Seq s;
     s.find(p, t);
@@ -237,12 +248,13 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
     return;
   }
   if (act) {
+    int64_t a = ((int64_t)blockIdx.y * RUNS + rl) * p.run;
+    const int64_t t1 = min(a + p.run, p.TT);
+    clear_tail<E>(p, p.dx, a, t1, c0);
     const E *x = static_cast<const E *>(p.x), *dy = static_cast<const E *>(p.dy), *dsT = static_cast<const E *>(p.dsT);
     E *dx = static_cast<E *>(p.dx), *ds0 = static_cast<E *>(p.ds0);
     float w[W][CS_CH], bias[CS_CH], h[W > 1 ? W - 1 : 1][CS_CH], dz[W][CS_CH];
     load_weights<W>(p.w, p.bias, c0, w, bias);
-    int64_t a = ((int64_t)blockIdx.y * RUNS + rl) * p.run;
-    const int64_t t1 = min(a + p.run, p.TT);
     while (a < t1) {
       Seq s;
       s.find(p, a);
@@ -462,6 +474,8 @@ using namespace dn;
 extern "C" dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n_seqs, int32_t dtype,
                                   const void *x, const float *w, const float *bias, const void *s0,
                                   const int32_t *cu_seqlens, void *y, void *sT, hipStream_t stream) {
+  const bool zero_tail = cu_seqlens && (dtype & DN_ZERO_TAIL);
+  dtype &= ~DN_ZERO_TAIL;
   const dn_status st = check(B, T, H, D, W, n_seqs, dtype, w, cu_seqlens);
   if (st != DN_OK) return st;
   if (!aligned16(s0) || !aligned16(sT) || !aligned16(w) || !aligned16(bias)) return DN_EINVAL;
@@ -479,6 +493,7 @@ extern "C" dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, in
   p.N = n_seqs;
   p.C = H * D;
   p.W = W;
+  p.zero_tail = zero_tail;
   // runs of 32 tokens, or of 8 where those would leave the CUs without 8 waves each
   const int64_t units = p.C / CS_CH;
   p.run = (p.TT + 31) / 32 * units >= 256 * 8 * 64 ? 32 : 8;
@@ -504,6 +519,8 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
                                       const int32_t *cu_seqlens, const void *dy, const void *dsT, void *dx, float *dw,
                                       float *dbias, void *ds0, void *workspace, size_t workspace_bytes,
                                       hipStream_t stream) {
+  const bool zero_tail = cu_seqlens && (dtype & DN_ZERO_TAIL);
+  dtype &= ~DN_ZERO_TAIL;
   const dn_status st = check(B, T, H, D, W, n_seqs, dtype, w, cu_seqlens);
   if (st != DN_OK) return st;
   if (!dw || !aligned16(s0) || !aligned16(dsT) || !aligned16(ds0) || !aligned16(w) || !aligned16(bias)) return DN_EINVAL;
@@ -526,6 +543,7 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
   p.N = n_seqs;
   p.C = H * D;
   p.W = W;
+  p.zero_tail = zero_tail;
   bwd_plan(p.TT, p.C, p.run, p.rows);
   const int per = CS_THREADS / unit_lanes(p.C);
   if (p.rows + (n_seqs + per - 1) / per > 65535) return DN_EUNSUPPORTED;

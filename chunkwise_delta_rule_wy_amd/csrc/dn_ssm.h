@@ -71,6 +71,7 @@ struct SsmParams {
   int NC;                    // chunks of a sequence (not packed)
   int nseg, nchunks;         // upper bounds over all sequences
   int sets, set_heads;       // backward: sets of heads of a group, heads of a set
+  int zero_tail;             // packed: clear the results' rows behind the last sequence
 };
 
 hipError_t launch_ssm_sweep(const SsmParams &p, int DK, bool store, bool backward, hipStream_t stream);
@@ -124,6 +125,16 @@ __device__ __forceinline__ bool segment(const SsmParams &p, int seg, Segment &s)
   s.last = len - start <= p.segc * CH;
   s.len = s.last ? len - start : p.segc * CH;
   return true;
+}
+// Clears the rows behind the last packed sequence of a result with rows of
+// `units` elements of T, all workgroups together.
+template <typename T>
+__device__ __forceinline__ void clear_tail(const SsmParams &p, void *result, int64_t units) {
+  T *out = static_cast<T *>(result);
+  const int64_t end = p.rows * units;
+  for (int64_t i = p.cu[p.N] * units + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < end;
+       i += (int64_t)gridDim.x * blockDim.x)
+    out[i] = T{};
 }
 // its first chunk's number among all
 __device__ __forceinline__ int first_chunk(const SsmParams &p, const Segment &s) {

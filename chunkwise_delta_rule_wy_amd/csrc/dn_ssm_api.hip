@@ -20,10 +20,10 @@ dn_status check_dims(int32_t H, int32_t G, int32_t Dk, int32_t Dv, int32_t dtype
 
 dn_status check_shape(const dn_ssm_shape *s, bool packed) {
   if (!s || s->B <= 0 || s->T < 0 || s->n_seqs <= 0) return DN_EINVAL;
-  const dn_status st = check_dims(s->H, s->G, s->Dk, s->Dv, s->dtype);
+  const dn_status st = check_dims(s->H, s->G, s->Dk, s->Dv, s->dtype & ~DN_ZERO_TAIL);
   if (st != DN_OK) return st;
   if (packed ? s->B != 1 : s->n_seqs != s->B) return DN_EINVAL;
-  if (s->dtype != DN_BF16) return DN_EUNSUPPORTED;  // the chunk kernels are bf16
+  if ((s->dtype & ~DN_ZERO_TAIL) != DN_BF16) return DN_EUNSUPPORTED;  // the chunk kernels are bf16
   // the kernels address a chunk's rows with 32-bit byte offsets
   if ((int64_t)128 * s->H * s->Dv > INT32_MAX || (int64_t)128 * s->G * s->Dk > INT32_MAX) return DN_EUNSUPPORTED;
   return DN_OK;
@@ -135,7 +135,7 @@ Layout layout_of(const dn_ssm_shape *s, const Plan &pl, bool packed, bool backwa
 // packed, and the answer covers both plans.
 size_t workspace(const dn_ssm_shape *s, bool backward) {
   if (!s || s->B <= 0 || s->T < 0 || s->n_seqs <= 0) return 0;
-  if (check_dims(s->H, s->G, s->Dk, s->Dv, s->dtype) != DN_OK) return 0;
+  if (check_dims(s->H, s->G, s->Dk, s->Dv, s->dtype & ~DN_ZERO_TAIL) != DN_OK) return 0;
   size_t n = 0;
   if (s->n_seqs == s->B) n = layout_of(s, plan_of(s, false, backward), false, backward).total;
   if (s->B == 1) {
@@ -160,6 +160,7 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
   if (L.total > 0 && (ws_bytes < L.total || !ws || !aligned16(ws))) return DN_ENOWS;
   char *base = static_cast<char *>(ws);
   p.cu = cu;
+  p.zero_tail = packed && (s->dtype & DN_ZERO_TAIL) != 0;
   p.rows = (int64_t)s->B * s->T;
   p.T = s->T;
   p.H = s->H;

@@ -67,6 +67,12 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
   constexpr int KB = DK / 32, QS = LD::QS, VS = LD::VS, NT = LD::NT;
   constexpr int NTT = NT / 2;  // token tiles of a wave's dq and dk
   __shared__ LD s;
+  if (p.zero_tail) {
+    clear_tail<u32x4>(p, p.dq, (int64_t)p.G * DK / 8);
+    clear_tail<u32x4>(p, p.dk, (int64_t)p.G * DK / 8);
+    clear_tail<u32x4>(p, p.dv, (int64_t)p.H * p.DV / 8);
+    clear_tail<float>(p, p.ddt, p.H);
+  }
   const int w = wave_number(), lane = lane_id(), l = lane, g = l >> 4, m = l & 15;
   const int item = xcd_item(blockIdx.x, p.nchunks * p.G * p.sets);
   const int chunk = item / (p.G * p.sets), grp = item % (p.G * p.sets) / p.sets, set = item % p.sets;
@@ -438,7 +444,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void ssm_grad_kernel(SsmParams p) {
 }
 
 // Sums over the sets of heads, four elements per thread (blockIdx.y: dq, dk);
-// rows behind the last packed sequence have none.
+// rows behind the last packed sequence have none and stay as they are.
 constexpr int SUM_THREADS = 256;
 
 __global__ __launch_bounds__(SUM_THREADS) void ssm_set_sum_kernel(SsmParams p, int64_t n4, int64_t n) {

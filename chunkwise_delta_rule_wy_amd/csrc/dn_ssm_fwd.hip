@@ -283,6 +283,7 @@ __global__ __launch_bounds__(NTHR, 2) void ssm_fwd_kernel(SsmParams p) {
   using PT = Swz<CH>;
   constexpr int MT = DK / 16, KB = DK / 32, SUBS = WK::SUBS, TABS = WK::TABS, VC = FwdLds<DK, PAIR>::VC;
   __shared__ FwdLds<DK, PAIR> lds;
+  if (p.zero_tail) clear_tail<u32x4>(p, p.o, (int64_t)p.H * p.DV / 8);
   const WK wk(p, xcd_item(blockIdx.x, gridDim.x));
   Segment sg;
   if (!segment(p, wk.seg, sg)) return;

@@ -424,8 +424,10 @@ dn_status dn_short_conv_l2_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32
  *   A <= 0 is the use; a positive A grows and overflows as the formula does.
  * - Packed sequences by cu_seqlens as dn_chunk_fwd, except that cu[n_seqs] may
  *   be less than T: rows behind the last sequence are not used, and theirs in
- *   o and the gradients are left as they were.  A sequence without tokens
- *   passes h0 through to hT.
+ *   o and the gradients are left as they were, or set to zero where the dtype
+ *   is or'ed with DN_ZERO_TAIL (zero is their gradients' value; the Python
+ *   functions ask for it, as their results are new memory).  A sequence without
+ *   tokens passes h0 through to hT.
  * - States, step sizes and decays are fp32 or wider throughout, and hT, ddt
  *   and the parameter gradients have fp32 accuracy; o and the gradients of
  *   q, k and v are rounded to bf16 once at the end and in at most one product
@@ -443,8 +445,13 @@ dn_status dn_short_conv_l2_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32
 typedef struct {
     int32_t B, T, H, G, Dk, Dv;
     int32_t n_seqs;  /* B, or the number of packed sequences */
-    int32_t dtype;   /* dn_dtype of q, k, v, o and their gradients */
+    int32_t dtype;   /* dn_dtype of q, k, v, o and their gradients (| DN_ZERO_TAIL) */
 } dn_ssm_shape;
+
+/* For the dtype of dn_ssm_fwd, dn_ssm_bwd, dn_conv_silu and dn_conv_silu_bwd:
+ * the results' rows behind the last packed sequence are set to zero.  Without
+ * cu_seqlens it has no effect. */
+#define DN_ZERO_TAIL 0x100
 
 /* Bytes of device workspace (16-byte aligned) of the two passes; they cover
  * packed input where B == 1. */
@@ -488,7 +495,7 @@ dn_status dn_ssm_step(int32_t B, int32_t H, int32_t G, int32_t Dk, int32_t Dv, i
  * and s0 NULL: zero.  sT receives each sequence's last W - 1 inputs, those of
  * s0 included where the sequence is shorter, bit for bit (NULL: not written;
  * it may not alias s0).  Packed sequences by cu_seqlens with
- * B == 1, as dn_short_conv, with cu[n_seqs] <= T as in dn_ssm_fwd.  D a
+ * B == 1, as dn_short_conv, with cu[n_seqs] <= T and DN_ZERO_TAIL as in dn_ssm_fwd.  D a
  * multiple of 8, W in 1..4, H D (W + 1) below 2^31, and fewer than 2^31
  * quadruples of channels times runs of 32 tokens (DN_EUNSUPPORTED otherwise).
  */

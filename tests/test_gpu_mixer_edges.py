@@ -41,3 +41,110 @@ def test_segment_decays_have_one_writer():
     assert len(inner) == 9 and (fwd[inner] < 0).all() and torch.isfinite(fwd[inner]).all()
     assert torch.equal(fwd[inner], bwd[inner])
     assert torch.isnan(fwd[last]).all() and (bwd[last] < 0).all()
+
+
+def padded(t, tail):
+    """Rows of NaN behind the tokens of a [1,T,...] tensor."""
+    return torch.cat([t, torch.full((1, tail, *t.shape[2:]), float("nan"), dtype=t.dtype, device=t.device)], 1)
+
+
+def spoil_free_memory(total=1 << 28):
+    """Leaves NaN in the memory that the next tensors get."""
+    for size in (1 << 12, 1 << 14, 1 << 16, 1 << 18, 1 << 20, 1 << 22):
+        junk = [torch.full((size // 4,), float("nan"), device="cuda") for _ in range(min(64, total // size))]
+        del junk
+
+
+@pytest.mark.parametrize("lens,tail,H,G,dk,dv", [
+    ([70, 0, 33], 97, 4, 1, 64, 64),        # whole chunks behind the last sequence
+    ([2200, 5], 100, 2, 1, 64, 64),         # cut into segments
+    ([64, 63], 1, 3, 3, 64, 128),           # one row
+    ([0, 0], 40, 4, 2, 64, 64),             # no tokens at all
+    ([5], 0, 2, 1, 64, 64),                 # no rows behind
+    ([130], 4000, 1, 1, 128, 64),           # few workgroups, many rows
+])
+def test_rows_behind_the_last_sequence_are_zero(lens, tail, H, G, dk, dv):
+    """Where offsets end before the rows do, the Python functions return zeros there, whatever the
+    rows hold, and everything before them as without the rows."""
+    n = sum(lens)
+    x, dO, dhT, _ = scan_inputs(1, n, H, G, dk, dv, lens)
+    d, cu, dO, dhT = cuda(x), cu_of(lens), dO.cuda(), dhT.cuda()
+    w, b = randn(H, dv, 4, seed=21).cuda(), randn(H, dv, seed=22).cuda()
+    s0 = randn(len(lens), 3, H, dv, seed=23, dtype=BF).cuda()
+
+    def calls(d, dO):
+        par = (d["A"], d["dt_bias"], d["skip"], d["h0"])
+        spoil_free_memory()
+        o, hT = dn.ssm_fwd(d["q"], d["k"], d["v"], d["dt"], *par, cu)
+        spoil_free_memory()
+        g = dn.ssm_bwd(d["q"], d["k"], d["v"], d["dt"], *par, dO, dhT, cu)
+        spoil_free_memory()
+        y, sT = dn.conv_silu(d["v"], w, b, s0, cu)
+        spoil_free_memory()
+        gc = dn.conv_silu_bwd(d["v"], w, b, s0, dO, s0, cu)
+        return dict(g, o=o, hT=hT, y=y, sT=sT, **{"conv_" + k: t for k, t in gc.items()})
+
+    want = calls(d, dO)
+    got = calls({k: padded(t, tail) if k in ("q", "k", "v", "dt") else t for k, t in d.items()}, padded(dO, tail))
+    # the plan of a longer tensor may cut elsewhere: compared bit for bit where it does not
+    val, bound = reference(x, lens, dO.cpu(), dhT.cpu())
+    for name, t in got.items():
+        if t.shape[:2] == (1, n + tail):
+            assert not t[:, n:].any(), name  # NaN counts as any
+            got[name] = t = t[:, :n]
+        if name in val:
+            assert ref.worst(t.reshape(val[name].shape), val[name], bound[name]) <= 1, name
+        elif name not in ("conv_dw", "conv_dbias"):
+            assert torch.equal(t, want[name]), name
+        else:  # the same terms |dz x|, |dz| <= 1.1 |dy|, added in two orders
+            terms = 1.1 * dO.float().abs().sum(1) * max([1.0] + [float(t.abs().max()) for t in (d["v"], s0) if t.numel()])
+            terms = terms[0] if name == "conv_dbias" else terms[0, ..., None]
+            assert ((t - want[name]).abs() <= 2 * (n + 64) * ref.U32 * terms).all(), name
+
+
+@pytest.mark.parametrize("lens,tail", [([40, 0, 110], 75), ([150], 300)])
+def test_mixer_trains_on_padded_packs(lens, tail):
+    """Projection, convolutions, scan and norm through autograd with rows behind the last sequence:
+    the weights' gradients are those of the pack without them, and no gradient holds what the
+    memory held before."""
+    n, H, G, dk, dv, W = sum(lens), 4, 2, 64, 64, 4
+    cu = cu_of(lens)
+    par = dict(scale=1 + randn(H, dv, seed=1, scale=0.1), wv=randn(H, dv, W, seed=2, scale=0.5),
+               wq=randn(G, dk, W, seed=3, scale=0.5), wk=randn(G, dk, W, seed=4, scale=0.5), bv=randn(H, dv, seed=5),
+               A=-1 - randn(H, seed=6).abs(), dt_bias=randn(H, seed=7) - 3, skip=randn(H, seed=8), wn=randn(dv, seed=9))
+    data = dict(xv=randn(1, n + tail, H, dv, seed=10), xq=randn(1, n + tail, G, dk, seed=11, dtype=BF),
+                xk=randn(1, n + tail, G, dk, seed=12, dtype=BF), dt=randn(1, n + tail, H, seed=13),
+                z=randn(1, n + tail, H, dv, seed=14, dtype=BF), weight=randn(1, n + tail, H, dv, seed=15))
+
+    def train(rows):
+        p = {k: t.cuda().requires_grad_() for k, t in par.items()}
+        x = {k: t[:, :rows].contiguous().cuda().requires_grad_(k != "weight") for k, t in data.items()}
+        scaled = x["xv"] * p["scale"]  # stands for the projection, whose weights all rows enter
+        spoil_free_memory()
+        v, _ = dn.conv_silu_fn(scaled.to(BF), p["wv"], p["bv"], None, cu)
+        spoil_free_memory()
+        q, _ = dn.conv_silu_fn(x["xq"], p["wq"], None, None, cu)
+        k, _ = dn.conv_silu_fn(x["xk"], p["wk"], None, None, cu)
+        spoil_free_memory()
+        o, _ = dn.ssm_scan(q, k, v, x["dt"], p["A"], p["dt_bias"], p["skip"], None, cu)
+        y = dn.gated_norm_fn(o, x["z"], p["wn"])
+        kept = dict(scaled=scaled, q=q, k=k, v=v)
+        for t in kept.values():
+            t.retain_grad()
+        spoil_free_memory()
+        (y[:, :n].float() * x["weight"][:, :n]).sum().backward()  # a program's loss takes the tokens alone
+        # sums of the absolute values of the terms of each sum over tokens (|dz| <= 1.1 |dy|)
+        size = {"w" + i: 1.1 * kept[i].grad.float().abs().sum((0, 1))[..., None] * t.float().abs().max()
+                for i, t in (("v", scaled), ("q", x["xq"]), ("k", x["xk"]))}
+        size.update(bv=1.1 * v.grad.float().abs().sum((0, 1)), scale=(scaled.grad * x["xv"]).abs().sum((0, 1)),
+                    wn=(x["weight"][:, :n] * y[:, :n].float() / p["wn"]).abs().sum((0, 1, 2)))
+        return {k: t.grad for k, t in x.items() if k != "weight"}, {k: t.grad for k, t in p.items()}, size
+
+    gx, want, size = train(n)
+    gx2, got, _ = train(n + tail)
+    for name, t in gx2.items():
+        assert not t[:, n:].any() and torch.equal(t[:, :n], gx[name]), name
+    for name, t in got.items():
+        # the same terms, for some parameters added in two orders (the norm's are n H)
+        bound = 2 * (n * H + 64) * ref.U32 * size[name].detach() if name in size else 0
+        assert torch.isfinite(t).all() and ((t - want[name]).abs() <= bound).all(), name

@@ -224,3 +224,19 @@ def test_conv_silu_refuses_unaligned_weights(lib):
         assert lib.dn_conv_silu_step(1, 1, 8, 4, 1, P(FAKE), P(w), P(b), P(FAKE), P(FAKE), None) == EINVAL
         assert lib.dn_conv_silu_bwd(1, 4, 1, 8, 4, 1, 1, P(FAKE), P(w), P(b), None, None, P(FAKE), None, P(FAKE), P(FAKE),
                                     None, None, P(FAKE), 1 << 30, None) == EINVAL
+
+
+def test_the_tail_flag_belongs_to_packed_passes(lib):
+    # accepted with a type, refused without a known one and in calls that know no packs
+    assert ssm_fwd(lib, ssm_shape(dtype=0x101), q=None) == EINVAL
+    assert ssm_fwd(lib, ssm_shape(dtype=0x100)) == EUNSUPPORTED and ssm_fwd(lib, ssm_shape(dtype=0x105)) == EINVAL
+    s, flagged = ssm_shape(), ssm_shape(dtype=0x101)
+    assert lib.dn_ssm_bwd_workspace(ctypes.byref(flagged)) == lib.dn_ssm_bwd_workspace(ctypes.byref(s)) > 0
+    assert ssm_bwd(lib, flagged, ws=None) == ENOWS
+    assert lib.dn_ssm_step(2, 4, 2, 64, 64, 0x101, P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, None, P(FAKE),
+                           P(FAKE), None) == EINVAL
+    assert lib.dn_conv_silu_step(2, 2, 16, 4, 0x101, P(FAKE), P(FAKE), None, P(FAKE), P(FAKE), None) == EINVAL
+    assert lib.dn_conv_silu(2, 8, 2, 16, 4, 2, 0x102, P(FAKE), P(FAKE), None, None, None, P(FAKE), None, None) == EINVAL
+    assert lib.dn_conv_silu_bwd(2, 8, 2, 16, 4, 2, 0x101, P(FAKE), P(FAKE), None, None, None, P(FAKE), None, P(FAKE),
+                                P(FAKE), None, None, None, 0, None) == ENOWS
+    assert lib.dn_gated_norm(8, 64, 1, 0x101, P(FAKE), P(FAKE), P(FAKE), 1e-5, 0, P(FAKE), None) == EINVAL
