@@ -88,7 +88,7 @@ Plan plan_of(const dn_ssm_shape *s, bool packed, bool backward) {
 // partial sums (4 x 4096 tokens, 32 heads: 198 us with one set, 234 us with
 // four, their sums included).
 void sets_of(const dn_ssm_shape *s, const Plan &pl, int &sets, int &heads) {
-  const int64_t R = s->H / s->G, wgs = pl.nchunks * s->G;
+  const int64_t R = s->H / s->G, wgs = (pl.nchunks < 256 ? pl.nchunks : 256) * s->G;  // 256 fill it
   int64_t n = wgs > 0 ? (256 + wgs - 1) / wgs : 1;
   if (n > R) n = R;
   heads = (int)((R + n - 1) / n);
@@ -151,11 +151,13 @@ dn_status setup(const dn_ssm_shape *s, const int32_t *cu, bool backward, void *w
                 hipStream_t stream) {
   const bool packed = cu != nullptr;
   const Plan pl = plan_of(s, packed, backward);
-  const int64_t top = UINT32_MAX / 512;  // a grid has fewer than 2^32 threads, in workgroups of up to 512
+  // a grid has fewer than 2^32 threads, in workgroups of up to 512: segments, the
+  // join's states, and the gradient kernel's chunks
+  const int64_t top = UINT32_MAX / 512;
+  if (pl.nseg * s->H * (s->Dv / 64) > top) return DN_EUNSUPPORTED;
+  if (pl.split && (int64_t)s->n_seqs * s->H * (s->Dk * s->Dv / 1024) > top) return DN_EUNSUPPORTED;
   sets_of(s, pl, p.sets, p.set_heads);
-  if (pl.nseg * s->H * (s->Dv / 64) > top || pl.nchunks * s->H > top || pl.nchunks * s->G * p.sets > top ||
-      (int64_t)s->n_seqs * s->H * (s->Dk * s->Dv / 1024) > top)
-    return DN_EUNSUPPORTED;
+  if (backward && (pl.nchunks > top || pl.nchunks * s->G * p.sets > top)) return DN_EUNSUPPORTED;
   const Layout L = layout_of(s, pl, packed, backward);
   if (L.total > 0 && (ws_bytes < L.total || !ws || !aligned16(ws))) return DN_ENOWS;
   char *base = static_cast<char *>(ws);

@@ -439,8 +439,9 @@ dn_status dn_short_conv_l2_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32
  * - Supported: Dk in {64, 128}; Dv a positive multiple of 64 up to 1024;
  *   DN_BF16 (dn_ssm_step also DN_F32); pointers of q, k, v, o, states and
  *   their gradients 16-byte aligned; 128 H Dv and 128 G Dk below 2^31; fewer
- *   than 2^23 workgroups a launch (one per sequence, head and 64 columns at
- *   the most).  Otherwise DN_EUNSUPPORTED or DN_EINVAL.
+ *   than 2^23 each of: sequences (cut ones: segments) times heads times Dv / 64;
+ *   where sequences are cut, n_seqs H Dk Dv / 1024; in the backward pass,
+ *   chunks of 64 tokens times groups.  Otherwise DN_EUNSUPPORTED or DN_EINVAL.
  */
 typedef struct {
     int32_t B, T, H, G, Dk, Dv;

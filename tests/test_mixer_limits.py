@@ -1,0 +1,56 @@
+"""Which sizes the state space mixer's calls take: launches that do not take
+place refuse nothing.  The checks need no GPU: what is accepted goes on to the
+workspace's check, which fails here."""
+import ctypes
+
+import pytest
+import torch
+
+import chunkwise_delta_rule_wy_amd as dn
+from test_mixer_ref import ENOWS, EUNSUPPORTED, ssm_bwd, ssm_fwd, ssm_shape
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return dn.load_library()
+
+
+def test_scan_limits_are_those_of_the_launches(lib):
+    # 2^23 chunks of two heads: forwards no launch counts chunks, backwards one does (2^24 of them are too many)
+    long = ssm_shape(B=1, n_seqs=1, T=1 << 29, H=2, G=1)
+    assert ssm_fwd(lib, long, ws=None) == ENOWS
+    half = ssm_shape(B=1, n_seqs=1, T=1 << 28, H=4, G=1)
+    assert ssm_bwd(lib, half, ws=None) == ENOWS
+    longer = ssm_shape(B=1, n_seqs=1, T=1 << 30, H=2, G=1)
+    assert ssm_fwd(lib, longer, ws=None) == ENOWS and ssm_bwd(lib, longer, ws=None) == EUNSUPPORTED
+    # 2^20 states of 128 x 128: only sequences that are cut are joined
+    many = ssm_shape(B=1 << 20, n_seqs=1 << 20, T=1, H=1, G=1, Dk=128, Dv=128)
+    assert ssm_bwd(lib, many, ws=None) == ENOWS
+
+
+def test_scan_sizes_do_not_wrap(lib):
+    top = (1 << 31) - 1
+    for kw in (dict(H=1 << 17, G=1 << 17), dict(H=1, G=1), dict(H=1 << 18, G=1)):
+        s = ssm_shape(B=top, n_seqs=top, T=top, **kw)
+        assert ssm_bwd(lib, s) == EUNSUPPORTED and ssm_fwd(lib, s) == EUNSUPPORTED
+    p = ssm_shape(B=1, n_seqs=top, T=top, H=1 << 17, G=1 << 17)
+    assert lib.dn_ssm_fwd(ctypes.byref(p), *[0x10000] * 5, None, None, None, 0x10000, 0x10000, None, 0x10000, 1 << 60,
+                          None) == EUNSUPPORTED
+
+
+@pytest.mark.gpu
+def test_scan_of_very_many_sequences():
+    # one token each, more states than a join would have workgroups for: o = (s q.k + skip) v
+    N, dk, dv = 524289, 128, 128
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, v = (torch.randn(N, 1, 1, d, generator=g, device="cuda").to(torch.bfloat16) for d in (dk, dk, dv))
+    dt, A, skip = torch.randn(N, 1, 1, generator=g, device="cuda"), -torch.ones(1).cuda(), torch.ones(1).cuda()
+    o, hT = dn.ssm_fwd(q, k, v, dt, A, None, skip, output_final_state=False)
+    assert hT is None
+    s = torch.logaddexp(dt.double(), torch.zeros_like(dt, dtype=torch.float64))[..., None]
+    terms = (q.double() * k.double())
+    want = (s * terms.sum(-1, keepdim=True) + 1) * v.double()
+    # P is rounded to bf16 once (half a step of the sum, its fp32 sum over dk before it), and o once
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 * (s * terms.sum(-1, keepdim=True)).abs() * (1 + 2.0 ** -6)
+                                      + 2.0 ** -24 * (dk + 16) * (s * terms.abs().sum(-1, keepdim=True) + 1)) * v.double().abs()
+    assert ((o.double() - want).abs() <= bound).all()
