@@ -243,8 +243,9 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
   for (int j = 0; j < W; ++j) zero8(dw[j]);
   zero8(db);
   if ((int)blockIdx.y >= p.rows) {  // sequences without tokens
-    const int n = ((int)blockIdx.y - p.rows) * RUNS + rl;
-    if (act && n < p.N) pass_state<E, W>(p, n, c0, p.dsT, p.ds0);
+    const int64_t step = (int64_t)(gridDim.y - p.rows) * RUNS;
+    if (act)
+      for (int64_t n = ((int)blockIdx.y - p.rows) * RUNS + rl; n < p.N; n += step) pass_state<E, W>(p, (int)n, c0, p.dsT, p.ds0);
     return;
   }
   if (act) {
@@ -433,9 +434,10 @@ void launch_fwd_e(const ConvSiluParams &p, unsigned grid, hipStream_t st) {
 template <typename E, int W>
 void launch_bwd_w(const ConvSiluParams &p, hipStream_t st) {
   const int ul = unit_lanes(p.C), units = p.C / CS_CH, per = CS_THREADS / ul;
-  // behind the rows, one workgroup row for every `per` sequences that may be empty
-  const int extra = p.ds0 ? (p.N + per - 1) / per : 0;
-  const dim3 grid((units + ul - 1) / ul, p.rows + extra);
+  // behind the rows, one workgroup row for every `per` sequences that may be empty,
+  // or as many as a grid has (65535 with the rows), which then go on to further ones
+  const int64_t groups = p.ds0 ? ((int64_t)p.N + per - 1) / per : 0, most = 65535 - p.rows;
+  const dim3 grid((units + ul - 1) / ul, p.rows + (int)(groups < most ? groups : most));
   if (grid.y == 0) return;
   if (ul == 64) hipLaunchKernelGGL((conv_silu_bwd_kernel<E, W, 64>), grid, dim3(CS_THREADS), 0, st, p);
   else hipLaunchKernelGGL((conv_silu_bwd_kernel<E, W, 16>), grid, dim3(CS_THREADS), 0, st, p);
@@ -545,8 +547,6 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
   p.W = W;
   p.zero_tail = zero_tail;
   bwd_plan(p.TT, p.C, p.run, p.rows);
-  const int per = CS_THREADS / unit_lanes(p.C);
-  if (p.rows + (n_seqs + per - 1) / per > 65535) return DN_EUNSUPPORTED;
   if (p.rows > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < dn_conv_silu_bwd_workspace(B, T, H, D, W)))
     return DN_ENOWS;
   if (dtype == DN_BF16) launch_bwd_e<bf16>(p, stream);

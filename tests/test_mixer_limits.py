@@ -54,3 +54,40 @@ def test_scan_of_very_many_sequences():
     bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 * (s * terms.sum(-1, keepdim=True)).abs() * (1 + 2.0 ** -6)
                                       + 2.0 ** -24 * (dk + 16) * (s * terms.abs().sum(-1, keepdim=True) + 1)) * v.double().abs()
     assert ((o.double() - want).abs() <= bound).all()
+
+
+def conv_bwd(lib, n_seqs, ds0, W=4, H=1, D=256, T=8, wsb=0):
+    F = 0x10000
+    return lib.dn_conv_silu_bwd(1, T, H, D, W, n_seqs, 1, F, F, None, None, F, F, None, F, F, None, ds0, F, wsb, None)
+
+
+def test_convolution_takes_any_number_of_sequences(lib):
+    # the backward pass as well as the forward one, with or without gradients of the states
+    for n in (300000, 1 << 30):
+        for ds0 in (None, 0x10000):
+            assert conv_bwd(lib, n, ds0) == ENOWS
+            assert conv_bwd(lib, n, ds0, W=1) == ENOWS
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,D,N", [(2, 128, 270001), (1, 8, 1048600)])
+def test_convolution_of_very_many_sequences(H, D, N):
+    # nearly all without tokens, which pass their state's gradient on; a few with some
+    lens = torch.zeros(N, dtype=torch.int64)
+    at = [0, 5, N // 2, N - 2, N - 1]
+    lens[at] = torch.tensor([3, 1, 40, 2, 9])
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).to(torch.int32).cuda()
+    T, W = int(lens.sum()), 2
+    g = torch.Generator("cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    x, dy, s0, dsT = r(1, T, H, D), r(1, T, H, D), r(N, W - 1, H, D), r(N, W - 1, H, D)
+    w, b = r(H, D, W).float(), r(H, D).float()
+    y, sT = dn.conv_silu(x, w, b, s0, cu)
+    gr = dn.conv_silu_bwd(x, w, b, s0, dy, dsT, cu)
+    empty = (lens == 0).cuda()
+    assert torch.equal(sT[empty], s0[empty]) and torch.equal(gr["ds0"][empty], dsT[empty])
+    few = torch.cat([torch.zeros(1, dtype=torch.int64), lens[at].cumsum(0)]).to(torch.int32).cuda()
+    y0, sT0 = dn.conv_silu(x, w, b, s0[at], few)
+    g0 = dn.conv_silu_bwd(x, w, b, s0[at], dy, dsT[at], few)
+    assert torch.equal(y, y0) and torch.equal(sT[at], sT0) and torch.equal(gr["ds0"][at], g0["ds0"])
+    assert all(torch.equal(gr[n], g0[n]) for n in ("dx", "dw", "dbias"))
