@@ -343,7 +343,7 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
   __syncthreads();
   const int base = blockIdx.x * PER, n = p.C * (W + 1);
   for (int i = threadIdx.x; i < PER; i += CS_THREADS) {
-    if (base + i >= n) break;
+    if (i >= n - base) break;
     float sum = 0.f;
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) sum += part[r][i];
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
 
 // dw and dbias from the rows of partial sums
 __global__ __launch_bounds__(CS_THREADS) void conv_silu_sum_kernel(ConvSiluParams p) {
-  const int64_t n = (int64_t)p.C * (p.W + 1), col0 = (int64_t)blockIdx.x * SUM_COLS, i = col0 + threadIdx.x;
+  const int64_t n = (int64_t)p.C * (p.W + 1), col0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * SUM_COLS, i = col0 + threadIdx.x;
   const float a = column_sum(p.part, p.rows, n, col0);
   if (threadIdx.x >= SUM_COLS || i >= n) return;
   const int64_t c = i / (p.W + 1);
@@ -552,7 +552,10 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
   if (dtype == DN_BF16) launch_bwd_e<bf16>(p, stream);
   else launch_bwd_e<float>(p, stream);
   if (hipGetLastError() != hipSuccess) return DN_EHIP;
-  hipLaunchKernelGGL(conv_silu_sum_kernel, dim3(((int64_t)p.C * (W + 1) + SUM_COLS - 1) / SUM_COLS), dim3(CS_THREADS), 0, stream, p);
+  // a grid has fewer than 2^32 threads in one direction: rows of 2^20 workgroups
+  const int64_t sums = ((int64_t)p.C * (W + 1) + SUM_COLS - 1) / SUM_COLS, line = sums < 1 << 20 ? sums : 1 << 20;
+  hipLaunchKernelGGL(conv_silu_sum_kernel, dim3((unsigned)line, (unsigned)((sums + line - 1) / line)), dim3(CS_THREADS), 0,
+                     stream, p);
   return hipGetLastError() == hipSuccess ? DN_OK : DN_EHIP;
 }
 

@@ -91,3 +91,21 @@ def test_convolution_of_very_many_sequences(H, D, N):
     g0 = dn.conv_silu_bwd(x, w, b, s0[at], dy, dsT[at], few)
     assert torch.equal(y, y0) and torch.equal(sT[at], sT0) and torch.equal(gr["ds0"][at], g0["ds0"])
     assert all(torch.equal(gr[n], g0[n]) for n in ("dx", "dw", "dbias"))
+
+
+@pytest.mark.gpu
+def test_convolution_of_very_many_channels():
+    # 2^28 sums of weights' gradients and more; the last channels against the same by themselves
+    H, D, W, T, last = 128, (1 << 20) + 8, 1, 3, 16
+    g = torch.Generator("cuda").manual_seed(6)
+    x, dy = (torch.randn(1, T, H, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w, b = (torch.randn(H, D, *s, generator=g, device="cuda") for s in ((W,), ()))
+    assert H * D * (W + 1) >= 1 << 28
+    gr = dn.conv_silu_bwd(x, w, b, None, dy)
+    cut = lambda t: t[..., -1:, -last:].contiguous()  # noqa: E731
+    g0 = dn.conv_silu_bwd(cut(x), w[-1:, -last:].contiguous(), cut(b), None, cut(dy))
+    assert torch.equal(cut(gr["dx"]), g0["dx"])
+    assert torch.equal(gr["dw"][-1:, -last:], g0["dw"]) and torch.equal(cut(gr["dbias"]), g0["dbias"])
+    first = dn.conv_silu_bwd(x[:, :, :1, :64].contiguous(), w[:1, :64].contiguous(), b[:1, :64].contiguous(), None,
+                             dy[:, :, :1, :64].contiguous())
+    assert torch.equal(gr["dw"][:1, :64], first["dw"])
