@@ -552,7 +552,8 @@ extern "C" dn_status dn_conv_silu_bwd(int32_t B, int32_t T, int32_t H, int32_t D
   if (dtype == DN_BF16) launch_bwd_e<bf16>(p, stream);
   else launch_bwd_e<float>(p, stream);
   if (hipGetLastError() != hipSuccess) return DN_EHIP;
-  // a grid has fewer than 2^32 threads in one direction: rows of 2^20 workgroups
+  // A grid has fewer than 2^32 threads in one direction (one of 2^32 + 32768 ran
+  // 32768, without an error): lines of 2^20 workgroups.
   const int64_t sums = ((int64_t)p.C * (W + 1) + SUM_COLS - 1) / SUM_COLS, line = sums < 1 << 20 ? sums : 1 << 20;
   hipLaunchKernelGGL(conv_silu_sum_kernel, dim3((unsigned)line, (unsigned)((sums + line - 1) / line)), dim3(CS_THREADS), 0,
                      stream, p);
