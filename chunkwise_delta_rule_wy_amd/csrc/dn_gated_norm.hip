@@ -203,7 +203,7 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_bwd_kernel(GatedNormPar
 
 // dw from the workgroups' partial sums
 __global__ __launch_bounds__(GN_THREADS) void gated_norm_sum_kernel(GatedNormParams p) {
-  const int wr = blockIdx.y, col0 = blockIdx.x * SUM_COLS, c = col0 + threadIdx.x;
+  const int wr = blockIdx.x, col0 = blockIdx.y * SUM_COLS, c = col0 + threadIdx.x;
   const float a = column_sum(p.part + (size_t)wr * p.blocks * p.D, p.blocks, p.D, col0);
   if (threadIdx.x < SUM_COLS && c < p.D) p.dw[(size_t)wr * p.D + c] = a;
 }
@@ -297,7 +297,8 @@ extern "C" dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32
   if (rows > 0 && (!x || !z || !dy || !dx || !dz)) return DN_EINVAL;
   for (const void *q : {x, z, dy, static_cast<const void *>(dx), static_cast<const void *>(dz)})
     if (!aligned16(q)) return DN_EINVAL;
-  if (rows > INT32_MAX || R > 65535) return DN_EUNSUPPORTED;
+  // a workgroup for every weight row at the least, and fewer than 2^32 threads
+  if (rows > INT32_MAX || R >= 1 << 24) return DN_EUNSUPPORTED;
   if (!workspace || !aligned16(workspace) || workspace_bytes < dn_gated_norm_bwd_workspace(rows, D, R)) return DN_ENOWS;
   GatedNormParams p = {};
   p.x = x;
@@ -316,6 +317,6 @@ extern "C" dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32
   if (dtype == DN_BF16) launch_e<bf16>(p, gate_first != 0, true, stream);
   else launch_e<float>(p, gate_first != 0, true, stream);
   if (hipGetLastError() != hipSuccess) return DN_EHIP;
-  hipLaunchKernelGGL(gated_norm_sum_kernel, dim3((D + SUM_COLS - 1) / SUM_COLS, R), dim3(GN_THREADS), 0, stream, p);
+  hipLaunchKernelGGL(gated_norm_sum_kernel, dim3(R, (D + SUM_COLS - 1) / SUM_COLS), dim3(GN_THREADS), 0, stream, p);
   return hipGetLastError() == hipSuccess ? DN_OK : DN_EHIP;
 }

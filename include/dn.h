@@ -546,7 +546,7 @@ size_t dn_gated_norm_bwd_workspace(int64_t rows, int32_t D, int32_t R);
 
 /*
  * Backward of dn_gated_norm from dy [rows, D] (dtype): dx, dz in the dtype, dw
- * [R,D] fp32.  No atomics: results repeat bit for bit.
+ * [R,D] fp32; R below 2^24 (DN_EUNSUPPORTED otherwise).  No atomics: results repeat bit for bit.
  */
 dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32_t dtype, const void *x, const void *z,
                             const float *w, float eps, int32_t gate_first, const void *dy,

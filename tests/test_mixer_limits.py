@@ -109,3 +109,31 @@ def test_convolution_of_very_many_channels():
     first = dn.conv_silu_bwd(x[:, :, :1, :64].contiguous(), w[:1, :64].contiguous(), b[:1, :64].contiguous(), None,
                              dy[:, :, :1, :64].contiguous())
     assert torch.equal(gr["dw"][:1, :64], first["dw"])
+
+
+def norm_bwd(lib, R, rows=None, ws=None):
+    F = 0x10000
+    return lib.dn_gated_norm_bwd(rows or R, 8, R, 1, F, F, F, 1e-5, 0, F, F, F, F, ws, 0, None)
+
+
+def test_norm_takes_any_number_of_heads(lib):
+    assert norm_bwd(lib, 65536) == ENOWS and norm_bwd(lib, (1 << 24) - 1) == ENOWS
+    assert norm_bwd(lib, 1 << 24) == EUNSUPPORTED  # 2^32 threads
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [False, True])
+def test_norm_of_very_many_heads(first):
+    # three heads alone get the same gradients as among 70001
+    R, D, n = 70001, 24, 3
+    g = torch.Generator("cuda").manual_seed(7)
+    x, z, dy = (torch.randn(n, R, D, generator=g, device="cuda") for _ in range(3))
+    w = torch.randn(R, D, generator=g, device="cuda")
+    got = dn.gated_norm_bwd(x, z, w, dy, gate_first=first)
+    for at in ([0, 1, 2], [65534, 65535, 65536], [R - 3, R - 2, R - 1]):
+        cut = lambda t: t[:, at].contiguous()  # noqa: E731
+        want = dn.gated_norm_bwd(cut(x), cut(z), w[at], cut(dy), gate_first=first)
+        assert torch.equal(cut(got[0]), want[0]) and torch.equal(cut(got[1]), want[1])
+        # three terms, added in some order
+        size = (dy.abs() * dn.gated_norm(x, z, w, gate_first=first).abs() / w.abs()).sum(0)[at]
+        assert ((got[2][at] - want[2]).abs() <= 8 * 2.0 ** -24 * size).all()
