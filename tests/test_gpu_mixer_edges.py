@@ -148,3 +148,38 @@ def test_mixer_trains_on_padded_packs(lens, tail):
         # the same terms, for some parameters added in two orders (the norm's are n H)
         bound = 2 * (n * H + 64) * ref.U32 * size[name].detach() if name in size else 0
         assert torch.isfinite(t).all() and ((t - want[name]).abs() <= bound).all(), name
+
+
+@pytest.mark.parametrize("T,H,G,dk,dv,rate,bias", [(1100, 4, 2, 128, 64, 1.0, -3.0), (2300, 2, 1, 64, 64, 0.02, -2.0),
+                                                   (2048, 8, 1, 128, 128, 0.3, -3.0)])
+def test_states_and_parameter_gradients_have_fp32_accuracy(T, H, G, dk, dv, rate, bias):
+    """hT, dh0 and the gradients in fp32 against 64 bits over many chunks, uncut and cut, strong and
+    weak decays, in the Euclidean norm, which tells three bf16 parts of an fp32 operand from two
+    where a bound on the largest error cannot.
+
+    A state is a sum of products with independent relative errors, in half steps of fp32 (U32): the
+    step size about 2 (6 at most), the exponents' rounding |x| ln 2 / 2 with |x| below 5 where a weight
+    counts, 1.7, the exponential and a product 1.2, and its own sums, six a chunk over the 16 chunks that
+    it remembers at the most, each 0.6 on average, 6: the root of their squares is below 7, and 8 is
+    asked.  Measured: 1.2 to 2.6; with two parts 15 to 42.
+
+    The parameters' gradients add the tokens' errors up; the independent ones average out, and 6 is
+    asked of the sum (whose terms do not cancel for these inputs).  Measured: 0.5 to 2.3; with two
+    parts 11 to 82 for dA and ddt_bias, and without the accumulators' change of sign dA 3.2, 12.6, 12.7."""
+    g = torch.Generator("cuda").manual_seed(11)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    silu = torch.nn.functional.silu
+    q, k, v = (silu(n(1, T, *s)).to(BF) for s in ((G, dk), (G, dk), (H, dv)))
+    dt, A = n(1, T, H), -rate * (1 + torch.rand(H, generator=g, device="cuda"))
+    par = (n(H) * 0.3 + bias, n(H), n(1, H, dk, dv))  # dt_bias, skip, h0
+    dO, dhT = n(1, T, H, dv).to(BF), n(1, H, dk, dv)
+    leaves = [t.double().requires_grad_() for t in (q, k, v, dt, A, *par)]
+    s = ref.softplus(leaves[3][0] + leaves[5])
+    o, hT = ref.scan(leaves[0][0], leaves[1][0], leaves[2][0], s, s * leaves[4], leaves[6], leaves[7], [T])
+    grads = torch.autograd.grad([o, hT], leaves[3:], [dO[0].double(), dhT.double()])
+    want = dict(zip(("ddt", "dA", "ddt_bias", "dskip", "dh0"), grads), hT=hT.detach())
+    _, got_h = dn.ssm_fwd(q, k, v, dt, A, *par)
+    got = dict(dn.ssm_bwd(q, k, v, dt, A, *par, dO, dhT), hT=got_h)
+    for name, limit in dict(hT=8, dh0=8, ddt=8, dA=6, ddt_bias=6, dskip=6).items():
+        err = float((got[name].double() - want[name]).norm() / want[name].norm()) / ref.U32
+        assert err <= limit, (name, err)
