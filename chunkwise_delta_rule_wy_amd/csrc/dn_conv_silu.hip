@@ -19,10 +19,11 @@
 // at 4 x 4096 tokens of 4096 channels, W = 4, bf16: 53 us forwards (5.1 TB/s,
 // the rate of a large copy; with eight channels and eight rows 55 us) and 90 us
 // backwards (4.5 TB/s; batches of one row 93 us, of four, which leave three waves
-// on a SIMD, 97 us, of four without the early loads 93 us).  The weights'
-// gradients are summed in registers over a run, in LDS over a workgroup's runs
-// and by a second kernel over the workgroups, in a fixed order, so that they
-// repeat bit for bit.
+// on a SIMD, 97 us, of four without the early loads 93 us).  In fp32 both passes
+// together, whole calls, take 267 us: 1.34 GB at 5.0 TB/s.  The weights' gradients
+// are summed in registers over a run, in LDS over a workgroup's runs and by a
+// second kernel over the workgroups, in a fixed order, so that they repeat bit for
+// bit.
 #include "dn.h"
 #include "dn_rows.h"
 
@@ -65,13 +66,13 @@ struct Raw {
 };
 
 template <typename E>
-__device__ __forceinline__ void load8(const E *src, float (&x)[CS_CH]) {
+__device__ __forceinline__ void load_ch(const E *src, float (&x)[CS_CH]) {
   Raw<E> r;
   r.load(src, true);
   r.get(x);
 }
 template <typename E>
-__device__ __forceinline__ void store8(E *dst, const float (&x)[CS_CH]) {
+__device__ __forceinline__ void store_ch(E *dst, const float (&x)[CS_CH]) {
   typedef E V __attribute__((ext_vector_type(CS_CH)));
   V v;
 #pragma unroll
@@ -87,7 +88,7 @@ __device__ __forceinline__ void clear_tail(const ConvSiluParams &p, void *result
   typedef E V __attribute__((ext_vector_type(CS_CH)));
   for (t = max(t, (int64_t)p.cu[p.N]); t < end; ++t) *reinterpret_cast<V *>(static_cast<E *>(result) + t * p.C + c0) = V{};
 }
-__device__ __forceinline__ void zero8(float (&x)[CS_CH]) {
+__device__ __forceinline__ void zero_ch(float (&x)[CS_CH]) {
 #pragma unroll
   for (int e = 0; e < CS_CH; ++e) x[e] = 0.f;
 }
@@ -125,7 +126,7 @@ __device__ __forceinline__ void load_weights(const float *wt, const float *bias,
 #pragma unroll
     for (int j = 0; j < W; ++j) w[j][e] = f[e * W + j];
   if (bias) load_f32<CS_CH>(bias + c0, b);
-  else zero8(b);
+  else zero_ch(b);
 }
 
 // the W - 1 inputs before token t of sequence s
@@ -136,9 +137,9 @@ __device__ __forceinline__ void load_history(const ConvSiluParams &p, const Seq 
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     const int64_t i = t - (W - 1) + k;
-    if (i >= s.st) load8<E>(x + i * p.C + c0, h[k]);
-    else if (s0) load8<E>(s0 + ((int64_t)s.n * (W - 1) + (i - s.st) + (W - 1)) * p.C + c0, h[k]);
-    else zero8(h[k]);
+    if (i >= s.st) load_ch<E>(x + i * p.C + c0, h[k]);
+    else if (s0) load_ch<E>(s0 + ((int64_t)s.n * (W - 1) + (i - s.st) + (W - 1)) * p.C + c0, h[k]);
+    else zero_ch(h[k]);
   }
 }
 template <int N>
@@ -169,9 +170,9 @@ __device__ __forceinline__ void pass_state(const ConvSiluParams &p, int n, int c
   for (int k = 0; k < W - 1; ++k) {
     const size_t at = ((size_t)n * (W - 1) + k) * p.C + c0;
     float x[CS_CH];
-    if (in) load8<E>(static_cast<const E *>(in) + at, x);
-    else zero8(x);
-    store8<E>(static_cast<E *>(out) + at, x);
+    if (in) load_ch<E>(static_cast<const E *>(in) + at, x);
+    else zero_ch(x);
+    store_ch<E>(static_cast<E *>(out) + at, x);
   }
 }
 
@@ -211,14 +212,14 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_kernel(ConvSiluParams p)
           const float z = conv_at<W>(w, bias, h, xv, e);
           o[e] = z * sigmoidf(z);
         }
-        store8<E>(y + (t + i) * p.C + c0, o);
+        store_ch<E>(y + (t + i) * p.C + c0, o);
         if constexpr (W > 1) shift<W - 1>(h, xv);
       }
     }
     t = end;
     if (sT && end == s.nx) {
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) store8<E>(sT + ((int64_t)s.n * (W - 1) + k) * p.C + c0, h[k]);
+      for (int k = 0; k < W - 1; ++k) store_ch<E>(sT + ((int64_t)s.n * (W - 1) + k) * p.C + c0, h[k]);
     }
   }
 }
@@ -240,8 +241,8 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
   const bool act = unit < units;
   float dw[W][CS_CH], db[CS_CH];
 #pragma unroll
-  for (int j = 0; j < W; ++j) zero8(dw[j]);
-  zero8(db);
+  for (int j = 0; j < W; ++j) zero_ch(dw[j]);
+  zero_ch(db);
   if ((int)blockIdx.y >= p.rows) {  // sequences without tokens
     const int64_t step = (int64_t)(gridDim.y - p.rows) * RUNS;
     if (act)
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
       const int64_t b = min(t1, s.nx), first = a == s.st ? a - (W - 1) : a;  // places [first, b)
       load_history<E, W>(p, s, a, c0, h);
 #pragma unroll
-      for (int k = 0; k < W; ++k) zero8(dz[k]);
+      for (int k = 0; k < W; ++k) zero_ch(dz[k]);
       const int64_t lim = min(b + (W - 1), s.nx);  // rows behind it are not used
       Raw<E> xn[CS_BWD_BATCH], yn[CS_BWD_BATCH];
       auto fetch = [&](int64_t u0) {
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
               g[e] *= sg * (1.f + z * (1.f - sg));
             }
           } else {
-            zero8(g);
+            zero_ch(g);
           }
           if (u < b) {
 #pragma unroll
@@ -322,12 +323,12 @@ __global__ __launch_bounds__(CS_THREADS, UL == 64 ? 4 : 3) void conv_silu_bwd_ke
           }
           if (dsT && q >= s.nx - (W - 1)) {
             float d[CS_CH];
-            load8<E>(dsT + ((int64_t)s.n * (W - 1) + (q - s.nx) + (W - 1)) * p.C + c0, d);
+            load_ch<E>(dsT + ((int64_t)s.n * (W - 1) + (q - s.nx) + (W - 1)) * p.C + c0, d);
 #pragma unroll
             for (int e = 0; e < CS_CH; ++e) o[e] += d[e];
           }
-          if (q >= s.st) store8<E>(dx + q * p.C + c0, o);
-          else if (ds0) store8<E>(ds0 + ((int64_t)s.n * (W - 1) + (q - s.st) + (W - 1)) * p.C + c0, o);
+          if (q >= s.st) store_ch<E>(dx + q * p.C + c0, o);
+          else if (ds0) store_ch<E>(ds0 + ((int64_t)s.n * (W - 1) + (q - s.st) + (W - 1)) * p.C + c0, o);
         }
       }
       a = b;
@@ -372,20 +373,20 @@ __global__ __launch_bounds__(CS_THREADS) void conv_silu_step_kernel(const E *x, 
   const int c0 = (idx % units) * CS_CH;
   float h[W > 1 ? W - 1 : 1][CS_CH], xv[CS_CH], w[W][CS_CH], bias[CS_CH], o[CS_CH];
   E *st = state + ((size_t)n * (W - 1)) * C + c0;
-  load8<E>(x + (size_t)n * C + c0, xv);
+  load_ch<E>(x + (size_t)n * C + c0, xv);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) load8<E>(st + (size_t)k * C, h[k]);
+  for (int k = 0; k < W - 1; ++k) load_ch<E>(st + (size_t)k * C, h[k]);
   load_weights<W>(wt, bs, c0, w, bias);
 #pragma unroll
   for (int e = 0; e < CS_CH; ++e) {
     const float z = conv_at<W>(w, bias, h, xv, e);
     o[e] = z * sigmoidf(z);
   }
-  store8<E>(y + (size_t)n * C + c0, o);
+  store_ch<E>(y + (size_t)n * C + c0, o);
   if constexpr (W > 1) {
 #pragma unroll
-    for (int k = 0; k + 1 < W - 1; ++k) store8<E>(st + (size_t)k * C, h[k + 1]);
-    store8<E>(st + (size_t)(W - 2) * C, xv);
+    for (int k = 0; k + 1 < W - 1; ++k) store_ch<E>(st + (size_t)k * C, h[k + 1]);
+    store_ch<E>(st + (size_t)(W - 2) * C, xv);
   }
 }
 

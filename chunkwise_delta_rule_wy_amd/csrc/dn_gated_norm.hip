@@ -242,7 +242,12 @@ void launch_lk(const GatedNormParams &p, bool first, bool bwd, hipStream_t st) {
 
 // Lanes per row and 16-byte units per lane, by the row's units: the fewest
 // lanes that hold a row with one unit each, so that a wave takes several
-// narrow rows; more units per lane only beyond a workgroup's 256.
+// narrow rows, but eight at the least, which leaves lanes idle in rows of one
+// to four units (2^21 rows of 8, 16, 32 bf16 values, both passes: 218, 246, 314 us;
+// with one, two and four lanes 51, 94, 203 us).  From 65 to 128 units a wave takes
+// two a lane, so that its sums need no LDS (2^15 rows of 1024 bf16 values: 133 us,
+// with 256 lanes 142 us; of 512 fp32 values 88 and 100 us); beyond a workgroup's 256
+// units a lane has several.
 template <typename E>
 void launch_e(const GatedNormParams &p, bool first, bool bwd, hipStream_t st) {
   const int u = p.D / Vec16<E>::N;

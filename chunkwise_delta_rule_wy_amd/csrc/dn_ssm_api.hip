@@ -30,7 +30,14 @@ dn_status check_shape(const dn_ssm_shape *s, bool packed) {
 }
 
 // Two column tiles share a workgroup where Dv has them, else two heads that
-// share their keys (SsmPair).
+// share their keys (SsmPair): keys and queries then pass through LDS once for
+// both.  That gains where workgroups fill the device (whole calls, single tiles
+// in brackets: 4 x 4096 tokens, 32 heads of 128 x 64, both passes, 519 us [543];
+// 16384 tokens, 16 heads of 128 x 128, 118 [127]; 65536 packed ones, 32 heads, 802
+// [903]; 2048 tokens, 512 heads, 266 [312]) and loses where few of them walk an
+// uncut chain of chunks (2048 tokens, 4 to 128 heads of 128 x 128, 133 to 142 us
+// [104 to 108]; 128 x 64, both passes, 4 to 64 heads, 260 to 297 [200 to 236]; 1357
+// ragged ones 61 [58]): the rule does not tell these apart.
 int pair_of(const dn_ssm_shape *s) {
   if (s->Dv % 128 == 0) return dn::SSM_TILES;
   return (s->H / s->G) % 2 == 0 ? dn::SSM_HEADS : dn::SSM_SINGLE;

@@ -26,12 +26,14 @@
 // and dG only the row blocks 2 half, 2 half + 1, and of dv the columns' half;
 // for dq and dk a wave owns 16 of the Dk rows.
 //
-// 227 registers allow two waves on a SIMD, one workgroup on a CU, so that what
+// 233 registers allow two waves on a SIMD, one workgroup on a CU, so that what
 // the next head needs is loaded as soon as its registers are free and without
 // a branch.  4 x 4096 tokens, 32 heads of 128 x 64 (256 workgroups): 198 us.
-// Bound by the reads of the states (537 MB; with v, dO and dv 738 MB at 3.7 TB/s,
-// where a plain sum over a large array reads 3.9 TB/s): without most of the
-// products it takes 188 us, without the loads 172 us.
+// Neither side bounds it alone: the states, v, dO and dv are 738 MB, 3.7 TB/s
+// where a large copy reaches 5.2; without most of the products it takes 188 us,
+// without the loads 172 us.  The CU's one workgroup runs loads, LDS and products
+// largely one after another, and bank conflicts of the rows, which are padded by
+// 16 bytes and not swizzled, take 36 % of its LDS cycles.
 #include "dn_ssm.h"
 
 namespace dn {

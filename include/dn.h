@@ -498,7 +498,8 @@ dn_status dn_ssm_step(int32_t B, int32_t H, int32_t G, int32_t Dk, int32_t Dv, i
  * it may not alias s0).  Packed sequences by cu_seqlens with
  * B == 1, as dn_short_conv, with cu[n_seqs] <= T and DN_ZERO_TAIL as in dn_ssm_fwd.  D a
  * multiple of 8, W in 1..4, H D (W + 1) below 2^31, and fewer than 2^31
- * quadruples of channels times runs of 32 tokens (DN_EUNSUPPORTED otherwise).
+ * quadruples of channels times runs of 32 tokens, the sequences added to the
+ * runs where sT is written (DN_EUNSUPPORTED otherwise).
  */
 dn_status dn_conv_silu(int32_t B, int32_t T, int32_t H, int32_t D, int32_t W, int32_t n_seqs,
                        int32_t dtype, const void *x, const float *w, const float *bias, const void *s0,
