@@ -183,3 +183,72 @@ def test_states_and_parameter_gradients_have_fp32_accuracy(T, H, G, dk, dv, rate
     for name, limit in dict(hT=8, dh0=8, ddt=8, dA=6, ddt_bias=6, dskip=6).items():
         err = float((got[name].double() - want[name]).norm() / want[name].norm()) / ref.U32
         assert err <= limit, (name, err)
+
+
+@pytest.mark.parametrize("N,top,H,G,dk,dv,tail", [(150, 60, 2, 1, 64, 64, 0), (300, 20, 3, 3, 64, 128, 65), (40, 130, 4, 1, 128, 64, 7)])
+def test_packs_of_many_short_sequences(N, top, H, G, dk, dv, tail):
+    """Tens to hundreds of sequences, shorter than a segment and mostly than a chunk, empty ones among
+    them, in packs long enough to be cut."""
+    gen = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, top, (N,), generator=gen).tolist()
+    n = sum(lens)
+    assert n > 32 * 64
+    x, dO, dhT, _ = scan_inputs(1, n, H, G, dk, dv, lens)
+    val, bound = reference(x, lens, dO, dhT)
+    d = {k: padded(t, tail) if k in ("q", "k", "v", "dt") else t for k, t in cuda(x).items()}
+    cu = cu_of(lens)
+    o, hT = dn.ssm_fwd(**d, cu_seqlens=cu)
+    gr = dn.ssm_bwd(d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"], padded(dO, tail).cuda(),
+                    dhT.cuda(), cu)
+    got = dict(gr, o=o, hT=hT)
+    for name in val:
+        t = got[name]
+        if t.shape[:2] == (1, n + tail):
+            assert not t[:, n:].any(), name
+            t = t[:, :n]
+        assert ref.worst(t.reshape(val[name].shape), val[name], bound[name]) <= 1, name
+
+
+def test_scan_with_growing_states():
+    # A > 0 is allowed: the states grow as the formula says
+    x, dO, dhT, ls = scan_inputs(1, 300, 2, 1, 64, 64, A=0.05)
+    val, bound = reference(x, ls, dO, dhT)
+    d = cuda(x)
+    o, hT = dn.ssm_fwd(**d)
+    gr = dn.ssm_bwd(d["q"], d["k"], d["v"], d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"], dO.cuda(), dhT.cuda())
+    for name, t in dict(gr, o=o, hT=hT).items():
+        assert ref.worst(t.reshape(val[name].shape), val[name], bound[name]) <= 1, name
+
+
+def test_captured_passes_follow_the_offsets():
+    """Offsets changed between the replays of a captured pass, also to fewer tokens: every replay as
+    the eager calls, with zeros behind the sequences where earlier replays left values."""
+    T, N, H, G, dk, dv = 2500, 4, 2, 1, 64, 64
+    x, dO, dhT, _ = scan_inputs(1, T, H, G, dk, dv, [T - 3, 1, 1, 1])
+    d, dO, dhT = cuda(x), dO.cuda(), dhT.cuda()
+    w, b = randn(H, dv, 4, seed=1).cuda(), randn(H, dv, seed=2).cuda()
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+
+    def train():
+        v, sT = dn.conv_silu(d["v"], w, b, None, cu)
+        args = (d["q"], d["k"], v, d["dt"], d["A"], d["dt_bias"], d["skip"], d["h0"])
+        o, hT = dn.ssm_fwd(*args, cu)
+        g = dn.ssm_bwd(*args, dO, dhT, cu)
+        gc = dn.conv_silu_bwd(d["v"], w, b, None, g["dv"], None, cu)
+        return [v, sT, o, hT, *g.values(), *gc.values()]
+
+    packs = [[2200, 0, 37, 200], [0, 0, 0, 0], [600, 600, 1, 1299], [5, 64, 0, 900], [T, 0, 0, 0]]
+    cu.copy_(cu_of(packs[0]))
+    train()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = train()
+    for lens in packs:
+        cu.copy_(cu_of(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = train()
+        assert all(torch.equal(a, c) for a, c in zip(out, want)), lens
+        for t in out:
+            if t.shape[:2] == (1, T):
+                assert torch.isfinite(t.float()).all() and not t[:, sum(lens):].any()
