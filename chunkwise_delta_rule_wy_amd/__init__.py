@@ -27,6 +27,8 @@ __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_noalloc", "bwd_workspace_bytes",
            "short_conv", "short_conv_bwd", "DeltaRule", "delta_rule", "ShortConv", "short_conv_fn",
            "ssm_fwd", "ssm_bwd", "ssm_step", "ssm_scan", "SsmScan", "conv_silu", "conv_silu_bwd", "conv_silu_step",
            "conv_silu_fn", "ConvSilu", "gated_norm", "gated_norm_bwd", "gated_norm_fn", "GatedNorm",
+           "glr_fwd", "glr_bwd", "glr_step", "glr_states", "glr_scan", "GlrScan",
+           "add_norm", "add_norm_bwd", "add_norm_fn", "AddNorm", "norm8", "linear8",
            "load_library", "LIB_PATH", "DnError"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdn.so")
@@ -127,6 +129,21 @@ def load_library():
     lib.dn_gated_norm_bwd_workspace.restype = Z
     lib.dn_gated_norm_bwd.argtypes = ([ctypes.c_int64, I, I, I] + [P] * 3 + [ctypes.c_float, I] + [P] * 4
                                       + [P, Z, P])
+    F, D = ctypes.c_float, ctypes.c_double
+    lib.dn_glr_states.argtypes = lib.dn_glr_fwd_workspace.argtypes = [I] * 4
+    lib.dn_glr_bwd_workspace.argtypes = [I] * 5
+    lib.dn_add_norm_bwd_workspace.argtypes = [ctypes.c_int64, I]
+    for name in ("glr_states", "glr_fwd_workspace", "glr_bwd_workspace", "add_norm_bwd_workspace"):
+        getattr(lib, "dn_" + name).restype = Z
+    lib.dn_glr_fwd.argtypes = [I] * 6 + [P] * 6 + [F] + [P] * 5 + [P, Z, P]
+    lib.dn_glr_bwd.argtypes = [I] * 6 + [P] * 6 + [F] + [P] * 12 + [P, Z, P]
+    lib.dn_glr_step.argtypes = [I] * 4 + [P] * 6 + [F] + [P, P] + [P]
+    lib.dn_add_norm.argtypes = [ctypes.c_int64, I, I, I] + [P] * 3 + [F, D] + [P] * 3 + [P]
+    lib.dn_add_norm_bwd.argtypes = [ctypes.c_int64, I, I, I] + [P] * 2 + [F, D] + [P] * 6 + [P, Z, P]
+    lib.dn_norm8.argtypes = [ctypes.c_int64, I, I, I] + [P] * 3 + [F] + [P] * 3 + [P]
+    lib.dn_linear8.argtypes = [I] * 3 + [P] * 6 + [I] + [P] + [P]
+    for name in ("glr_fwd", "glr_bwd", "glr_step", "add_norm", "add_norm_bwd", "norm8", "linear8"):
+        getattr(lib, "dn_" + name).restype = ctypes.c_int
     for name in ("ssm_fwd", "ssm_bwd", "ssm_step", "conv_silu", "conv_silu_bwd", "conv_silu_step", "gated_norm",
                  "gated_norm_bwd"):
         getattr(lib, "dn_" + name).restype = ctypes.c_int
@@ -957,3 +974,266 @@ class GatedNorm(torch.autograd.Function):
 def gated_norm_fn(x, z, w, eps: float = 1e-5, gate_first: bool = False):
     """Differentiable ``gated_norm``."""
     return GatedNorm.apply(x, z, w, eps, gate_first)
+
+
+# --------------------------------------------- the gated linear recurrence
+
+
+def _glr_args(x, r, i, lam, br, bi, state, cu_seqlens, dims):
+    """(device, leading sizes, H, D, sequences), checked; state may be None."""
+    dev = _gpu(x, "x", (dims,), tuple(_DTYPES))
+    lead, (H, D) = tuple(x.shape[:-2]), x.shape[-2:]
+    _given(r=r, i=i, lam=lam)
+    N = _seqs(lead[0], cu_seqlens, dev)
+    for t, name in ((x, "x"), (r, "r"), (i, "i")):
+        _is(t, name, x.dtype, tuple(x.shape), dev)
+    for t, name in ((lam, "lam"), (br, "br"), (bi, "bi")):
+        _is(t, name, torch.float32, (H, D), dev)
+    _is(state, "state", torch.float32, (N, H, D), dev)
+    return dev, lead, H, D, N
+
+
+def glr_states(x):
+    """New memory for the states that ``glr_fwd`` keeps for ``glr_bwd`` (x
+    ``[B,T,H,D]``): float32 ``[rows,H,D]``, about one row for 64 tokens."""
+    dev = _gpu(x, "x", (4,), tuple(_DTYPES))
+    B, T, H, D = x.shape
+    return torch.empty((load_library().dn_glr_states(B, T, H, D), H, D), dtype=torch.float32, device=dev)
+
+
+def _glr_states(states, B, T, H, D, dev):
+    if states is not None:
+        _is(states, "states", torch.float32, (load_library().dn_glr_states(B, T, H, D), H, D), dev)
+
+
+def glr_fwd(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: float = 8.0, states=None):
+    """Forward pass of the gated linear recurrence (``dn_glr_fwd``), every channel
+    by itself:
+
+        s_t = sigmoid(r_t + br),  a_t = exp(-power softplus(lam) s_t),
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + bi) x_t,  y_t = h_t.
+
+    x, r, i ``[B,T,H,D]`` float32 or bfloat16 (D a multiple of 8); lam, br, bi
+    ``[H,D]`` float32 (br, bi None: zero); h0 ``[N,H,D]`` float32 or None;
+    cu_seqlens as in ``ssm_fwd``; states from ``glr_states``, filled for
+    ``glr_bwd``.  Returns ``(y, hT)``, y in x's dtype, hT ``[N,H,D]`` float32."""
+    dev, (B, T), H, D, N = _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
+    _glr_states(states, B, T, H, D, dev)
+    y = torch.empty_like(x)
+    hT = torch.empty((N, H, D), dtype=torch.float32, device=dev)
+    wsb = load_library().dn_glr_fwd_workspace(B, T, H, D)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_glr_fwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(r), _adr(i), _adr(lam), _adr(br),
+          _adr(bi), float(power), _adr(h0), _adr(cu_seqlens), _adr(y), _adr(hT), _adr(states), _adr(ws), wsb)
+    return y, hT
+
+
+def glr_bwd(x, r, i, lam, br, bi, h0, dy, dhT=None, cu_seqlens=None, power: float = 8.0, states=None):
+    """Backward pass of ``<dy, y> + <dhT, hT>`` of ``glr_fwd`` (``dn_glr_bwd``), dy
+    in x's dtype, dhT float32 (None: 0); states: those that the forward call
+    filled (None: computed again).  Returns a dict: dx, dr, di in x's dtype,
+    dlam, dbr, dbi (None without the bias) and dh0 in float32; rows behind the
+    last packed sequence are zero."""
+    dev, (B, T), H, D, N = _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
+    _given(dy=dy)
+    _is(dy, "dy", x.dtype, tuple(x.shape), dev)
+    _is(dhT, "dhT", torch.float32, (N, H, D), dev)
+    _glr_states(states, B, T, H, D, dev)
+    gr = dict(dx=torch.empty_like(x), dr=torch.empty_like(r), di=torch.empty_like(i), dlam=torch.empty_like(lam),
+              dbr=None if br is None else torch.empty_like(br), dbi=None if bi is None else torch.empty_like(bi),
+              dh0=torch.empty((N, H, D), dtype=torch.float32, device=dev))
+    wsb = load_library().dn_glr_bwd_workspace(B, T, H, D, states is not None)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_glr_bwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(r), _adr(i), _adr(lam), _adr(br),
+          _adr(bi), float(power), _adr(h0), _adr(cu_seqlens), _adr(states), _adr(dy), _adr(dhT),
+          *[_adr(g) for g in gr.values()], _adr(ws), wsb)
+    return gr
+
+
+def glr_step(x, r, i, lam, br, bi, state, power: float = 8.0):
+    """One token of every sequence (``dn_glr_step``): x, r, i ``[B,H,D]``, state
+    ``[B,H,D]`` float32 updated in place.  Returns y ``[B,H,D]``."""
+    try:
+        E, dev, xs, f32 = x.dtype, x.get_device(), x.shape, torch.float32
+        fits = (len(xs) == 3 and E in _DTYPES and dev >= 0 and xs.numel() <= _MAX_SIZE and x.is_contiguous()
+                and _fits(r, E, xs, dev) and _fits(i, E, xs, dev) and _fits(lam, f32, xs[1:], dev)
+                and (br is None or _fits(br, f32, xs[1:], dev)) and (bi is None or _fits(bi, f32, xs[1:], dev))
+                and _fits(state, f32, xs, dev))
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _given(state=state)
+        _glr_args(x, r, i, lam, br, bi, state, None, 3)
+    y = torch.empty_like(x)
+    _call("dn_glr_step", dev, xs[0], xs[1], xs[2], _DTYPES[E], x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(),
+          _adr(br), _adr(bi), power, state.data_ptr(), y.data_ptr())
+    return y
+
+
+class GlrScan(torch.autograd.Function):
+    """Autograd wrapper: forward by ``glr_fwd``, backward by ``glr_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, r, i, lam, br, bi, h0, cu_seqlens, power, save_states):
+        states = glr_states(x) if save_states else None
+        y, hT = glr_fwd(x, r, i, lam, br, bi, h0, cu_seqlens, power, states)
+        ctx.save_for_backward(x, r, i, lam, br, bi, h0, cu_seqlens, states)
+        ctx.power = power
+        ctx.set_materialize_grads(False)
+        return y, hT
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dhT):
+        x, r, i, lam, br, bi, h0, cu, states = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else _grad(dy)
+        gr = glr_bwd(x, r, i, lam, br, bi, h0, dy, None if dhT is None else _grad(dhT), cu, ctx.power, states)
+        return (gr["dx"], gr["dr"], gr["di"], gr["dlam"], gr["dbr"], gr["dbi"], None if h0 is None else gr["dh0"], None, None,
+                None)
+
+
+def glr_scan(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: float = 8.0, save_states: bool = True):
+    """Differentiable gated linear recurrence; returns (y, hT).  ``save_states``
+    keeps states from the forward pass for the backward pass (1/16 of x's bytes
+    and less) instead of computing them again.  Rows behind the last packed
+    sequence give zeros and get zero gradients."""
+    return GlrScan.apply(x, r, i, lam, br, bi, h0, cu_seqlens, power, save_states)
+
+
+# ------------------------------- the residual stream around a token mixer
+
+
+def _add_norm_args(x, residual, w):
+    """(device, rows, D, residual's dtype), checked; residual may be None."""
+    dev = _gpu(x, "x", tuple(range(1, 9)), tuple(_DTYPES))
+    D = x.shape[-1]
+    _is(x, "x", x.dtype, tuple(x.shape), dev)
+    R = x.dtype
+    if residual is not None:
+        R = residual.dtype if isinstance(residual, torch.Tensor) and residual.dtype is torch.float32 else x.dtype
+        _is(residual, "residual", R, tuple(x.shape), dev)
+    _is(w, "w", torch.float32, (D,), dev)
+    return dev, x.numel() // D if D else 0, D, R
+
+
+def _dropped(p, seed, dev):
+    """Whether dropout drops anything, its arguments checked."""
+    if not 0 <= p < 1:
+        raise ValueError("p must be at least 0 and below 1")
+    if p == 0:
+        return False
+    _given(seed=seed)
+    _is(seed, "seed", torch.int64, (2,), dev)
+    return round(p * 65536) > 0
+
+
+def add_norm(x, residual, w, eps: float = 1e-5, p: float = 0.0, seed=None):
+    """The residual's addition with dropout and root-mean-square norm over the last
+    dimension (``dn_add_norm``): ``h = residual + dropout(x)``, ``y = h /
+    sqrt(mean(h^2) + eps) * w``.  x ``[..., D]`` float32 or bfloat16; residual of
+    its shape in its dtype or float32, or None (zero); w float32 ``[D]``.  p is the
+    share that is dropped, to the nearest 2^-16; seed, with p > 0, an int64
+    tensor ``[2]`` on the device, a key and the number of a stream: the mask
+    depends on it and a value's place alone and is not stored.  Returns ``(y, h)``:
+    y in x's dtype, h in the residual's (x itself where nothing is added or
+    dropped)."""
+    dev, rows, D, R = _add_norm_args(x, residual, w)
+    _given(w=w)
+    drop = _dropped(p, seed, dev)
+    y = torch.empty_like(x)
+    h = torch.empty_like(x, dtype=R) if residual is not None or drop else None
+    _call("dn_add_norm", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], _adr(x), _adr(residual), _adr(w), eps, p,
+          _adr(seed) if drop else None, _adr(y), _adr(h))
+    return y, x if h is None else h
+
+
+def add_norm_bwd(h, w, dy, dh=None, eps: float = 1e-5, p: float = 0.0, seed=None):
+    """Backward of ``add_norm`` (``dn_add_norm_bwd``) from its h, dy in x's dtype and
+    dh in h's (the gradient of h itself; None: 0), with the forward call's p and
+    seed: ``(dx, dres, dw)``, dx in x's dtype (dres itself where nothing is dropped
+    and the types agree), dres in h's, dw float32."""
+    _given(h=h)
+    dev, rows, D, R = _add_norm_args(dy, h, w)
+    _given(w=w)
+    drop = _dropped(p, seed, dev)
+    _is(dh, "dh", R, tuple(h.shape), dev)
+    dres, dw = torch.empty_like(h), torch.empty_like(w)
+    dx = torch.empty_like(dy) if drop or R is not dy.dtype else None
+    wsb = load_library().dn_add_norm_bwd_workspace(rows, D)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _call("dn_add_norm_bwd", dev, rows, D, _DTYPES[dy.dtype], _DTYPES[R], _adr(h), _adr(w), eps, p,
+          _adr(seed) if drop else None, _adr(dy), _adr(dh), _adr(dx), _adr(dres), _adr(dw), _adr(ws), wsb)
+    return dres if dx is None else dx, dres, dw
+
+
+class AddNorm(torch.autograd.Function):
+    """Autograd wrapper: forward by ``add_norm``, backward by ``add_norm_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w, eps, p, seed):
+        y, h = add_norm(x, residual, w, eps, p, seed)
+        ctx.save_for_backward(h, w, seed)
+        ctx.eps, ctx.p, ctx.dtype, ctx.added = eps, p, x.dtype, residual is not None
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh):
+        h, w, seed = ctx.saved_tensors
+        dy = torch.zeros_like(h, dtype=ctx.dtype) if dy is None else _grad(dy)
+        dx, dres, dw = add_norm_bwd(h, w, dy, None if dh is None else _grad(dh), ctx.eps, ctx.p, seed)
+        return dx, dres if ctx.added else None, dw, None, None, None
+
+
+def add_norm_fn(x, residual, w, eps: float = 1e-5, p: float = 0.0, seed=None):
+    """Differentiable ``add_norm``; returns (y, h).  The seed's values must stay
+    until the backward pass."""
+    return AddNorm.apply(x, residual, w, eps, p, seed)
+
+
+def norm8(x, residual=None, w=None, eps: float = 1e-5):
+    """``add_norm`` for serving with its rows in 8 bits (``dn_norm8``): ``(y8, scale,
+    h)``, y8 float8_e4m3fn of x's shape, scale float32 of its leading sizes, ``y =
+    scale y8`` with ``scale = max |y| / 448``.  Without w the sum itself is
+    rounded: ``norm8(weight)[:2]`` gives ``linear8`` its weights.  h as
+    ``add_norm`` returns it."""
+    dev, rows, D, R = _add_norm_args(x, residual, w)
+    y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    h = torch.empty_like(x, dtype=R) if residual is not None else None
+    _call("dn_norm8", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], _adr(x), _adr(residual), _adr(w), eps, _adr(y), _adr(scale),
+          _adr(h))
+    return y, scale, x if h is None else h
+
+
+_ACTS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def linear8(x, xs, w, ws, bias=None, residual=None, act: str = "none"):
+    """Product of 8-bit rows with 8-bit weights (``dn_linear8``): ``act(xs ws (x w^T)
+    + bias) + residual``.  x ``[..., K]`` and w ``[N, K]`` float8_e4m3fn with scales
+    xs ``[...]`` and ws ``[N]`` (float32), as ``norm8`` returns them; K a multiple of
+    16; bias ``[N]`` float32 or None; residual ``[..., N]`` bfloat16 or None; act
+    "none", "silu" or "gelu" (with the normal distribution's integral).  Returns y
+    ``[..., N]`` bfloat16."""
+    if act not in _ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(_ACTS))
+    E = torch.float8_e4m3fn
+    dev = _gpu(x, "x", tuple(range(1, 9)), (E,))
+    _gpu(w, "w", (2,), (E,))
+    _given(xs=xs, ws=ws)
+    lead, K, N = tuple(x.shape[:-1]), x.shape[-1], w.shape[0]
+    _is(x, "x", E, tuple(x.shape), dev)
+    _is(w, "w", E, (N, K), dev)
+    _is(xs, "xs", torch.float32, lead, dev)
+    _is(ws, "ws", torch.float32, (N,), dev)
+    _is(bias, "bias", torch.float32, (N,), dev)
+    _is(residual, "residual", torch.bfloat16, lead + (N,), dev)
+    y = torch.empty(lead + (N,), dtype=torch.bfloat16, device=dev)
+    M = xs.numel()
+    if M > _MAX_SIZE:
+        raise ValueError("x has 2^31 rows or more")
+    _call("dn_linear8", dev, M, N, K, x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), _adr(bias), _adr(residual),
+          _ACTS[act], y.data_ptr())
+    return y

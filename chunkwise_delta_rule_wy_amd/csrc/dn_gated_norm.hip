@@ -24,7 +24,7 @@
 namespace dn {
 namespace {
 
-constexpr int GN_THREADS = 256;
+constexpr int GN_THREADS = ROW_THREADS;
 // Workgroups: four per CU backwards (as many rows of partial sums), and up to
 // eight forwards, all that a CU holds, which then go on to further rows
 // (262144 rows of 256 values, bf16: 80 us, with four per CU 114 us, with
@@ -42,64 +42,6 @@ struct GatedNormParams {
   int blocks;    // backward: workgroups per weight row
   float eps;
 };
-
-template <typename E, int LPR, int K>
-struct Row {
-  static constexpr int V = Vec16<E>::N, N = K * V;
-  __device__ static __forceinline__ int col(int k, int lane) { return (k * LPR + lane) * V; }
-  __device__ static __forceinline__ void load(const E *src, int lane, int D, float (&x)[N]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = col(k, lane);
-      if (c < D) {
-        const typename Vec16<E>::type v = *reinterpret_cast<const typename Vec16<E>::type *>(src + c);
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[k * V + e] = to_f<E>(v[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[k * V + e] = 0.f;
-      }
-    }
-  }
-  __device__ static __forceinline__ void load_w(const float *src, int lane, int D, float (&x)[N]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = col(k, lane);
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[k * V + e] = c < D ? src[c + e] : 0.f;
-    }
-  }
-  __device__ static __forceinline__ void store(E *dst, int lane, int D, const float (&x)[N]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = col(k, lane);
-      if (c >= D) continue;
-      typename Vec16<E>::type v;
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = to_e<E>(x[k * V + e]);
-      *reinterpret_cast<typename Vec16<E>::type *>(dst + c) = v;
-    }
-  }
-};
-
-// sum over a row's lanes; a row as wide as the workgroup goes through LDS
-// (two buffers taken in turn, one barrier a sum)
-template <int LPR>
-__device__ __forceinline__ float lanes_sum(float x, float (*buf)[GN_THREADS / 64], int &turn) {
-  if constexpr (LPR <= 64) {
-    return group_sum<LPR>(x);
-  } else {
-    x = group_sum<64>(x);
-    float *b = buf[turn];
-    turn ^= 1;
-    if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = x;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < LPR / 64; ++i) s += b[i];
-    return s;
-  }
-}
 
 __device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 

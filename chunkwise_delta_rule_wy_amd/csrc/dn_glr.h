@@ -1,0 +1,275 @@
+// Shared parts of the gated linear recurrence's kernels (gfx950).
+//
+// Every channel is a recurrence of its own.  With s = sigmoid(r + br),
+// log a = -power softplus(lam) s, m = sqrt(1 - a^2) and u = sigmoid(i + bi) x:
+//
+//   h_t = a_t h_{t-1} + m_t u_t,   y = h
+//
+// and going back, with c the gradient that reaches h_t from later tokens (dhT at
+// a sequence's last one):
+//
+//   g_t = dy_t + c,   c <- a_t g_t
+//   W = log a dL/dlog a = g log a (a h_{t-1} - u a^2 / m)
+//   dr = (1 - s) W,   di = g m u (1 - sigmoid(i + bi)),   dx = g m sigmoid(i + bi)
+//   dbr = sum dr,     dbi = sum di,     dlam = sigmoid(lam) / softplus(lam) sum W
+//
+// Where a = 1 (a recurrence gate of minus infinity) m and W are 0 and the token
+// leaves the state as it is.
+//
+// Both directions are composed of maps c -> A c + B, which are associative.  A
+// workgroup takes 64 channels, two a lane, and walks through a segment of rows
+// tile by tile.  In a tile a thread has a run of consecutive rows and composes
+// their maps; one exchange through LDS then gives every run the state it starts
+// from.  Each tensor is read once where the sequences times the channels fill
+// the device; else sequences are cut into segments, whose maps are composed in
+// a pass before.  Packed sequences are cut wherever they lie: the state in front
+// of a sequence's first row is h0, and whatever reaches that row from the rows
+// before is dropped, not multiplied by zero, so that nothing crosses sequences.
+#pragma once
+
+#include "dn_internal.h"
+#include "dn_rows.h"
+
+namespace dn {
+
+constexpr int GLR_CH = 64;      // channels of a workgroup
+constexpr int GLR_LANES = 32;   // lanes of a row, two channels each
+constexpr int GLR_THREADS = 512;
+constexpr int GLR_WAVES = GLR_THREADS / 64;
+constexpr int GLR_RUNS = GLR_THREADS / GLR_LANES;  // runs of rows side by side
+constexpr int GLR_TILE = 128;   // rows of a segment's unit
+constexpr int GLR_STATE = 64;   // rows between two states kept for the backward pass
+
+struct GlrParams {
+  const void *x, *r, *i, *dy;
+  const float *lam, *br, *bi;  // br, bi may be null
+  const float *h0, *dhT;       // may be null
+  const int32_t *cu;           // packed sequences, or null: N sequences of T rows
+  void *y, *dx, *dr, *di;      // y may be null
+  float *hT, *dh0;             // may be null
+  float *states;               // state entering each block of GLR_STATE rows (may be null forwards)
+  float *sum_f, *sum_r;        // maps of the segments, [segment][A, B][C]
+  float *part;                 // [segment][dlam, dbr, dbi][C]
+  float *dlam, *dbr, *dbi;     // dbr, dbi may be null
+  int64_t rows;
+  int T, N, C, groups;         // groups: of GLR_CH channels
+  int flat;                    // segments run over all rows; else they lie in one sequence, NS to each
+  int NS, segt, nseg;          // segt: tiles of a segment
+  int cut;                     // segments continue one another
+  int zero_tail;
+  float power;
+};
+
+hipError_t launch_glr_sum(const GlrParams &p, int dtype, bool backward, hipStream_t stream);
+hipError_t launch_glr_fwd(const GlrParams &p, int dtype, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrParams &p, int dtype, hipStream_t stream);
+
+struct GlrStepParams {
+  const void *x, *r, *i;
+  const float *lam, *br, *bi;
+  float *state;
+  void *y;
+  int64_t n;  // B C
+  int C;
+  float power;
+};
+hipError_t launch_glr_step(const GlrStepParams &p, int dtype, hipStream_t stream);
+
+// ------------------------------------------------------------------ device
+
+constexpr float GLR_LOG2E = 1.44269504088896340736f, GLR_LN2 = 0.69314718055994530942f;
+
+template <typename E> struct Pair;  // two neighbouring channels
+template <> struct Pair<bf16> { typedef bf16x2v type; };
+template <> struct Pair<float> { typedef f32x2 type; };
+
+template <typename E>
+__device__ __forceinline__ f32x2 to_f2(typename Pair<E>::type v) {
+  return (f32x2){to_f<E>(v[0]), to_f<E>(v[1])};
+}
+template <typename E>
+__device__ __forceinline__ typename Pair<E>::type to_e2(f32x2 v) {
+  if constexpr (std::is_same<E, bf16>::value) return __builtin_bit_cast(bf16x2v, pk_bf16(v[0], v[1]));
+  else return v;
+}
+
+__device__ __forceinline__ float glr_softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// What a channel's gates need: log2 of the decay at an open gate, and the biases
+// in units of -log2 e.
+struct GlrChannel {
+  float k2, br, bi;
+};
+__device__ __forceinline__ GlrChannel glr_channel(const float *lam, const float *br, const float *bi, float power, int c) {
+  return {-power * GLR_LOG2E * glr_softplus(lam[c]), br ? -GLR_LOG2E * br[c] : 0.f, bi ? -GLR_LOG2E * bi[c] : 0.f};
+}
+
+// sigmoid(z + bias), bias in units of -log2 e
+__device__ __forceinline__ float glr_sigmoid(float z, float bias) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(__builtin_fmaf(z, -GLR_LOG2E, bias)));
+}
+
+// 1 - a^2 for a = 2^l2, l2 <= 0: with v = -2 log a, 1 - e^-v by its series below
+// 0.4, where the difference would lose digits (the rest is below 2^-24 of it).
+__device__ __forceinline__ float glr_rest(float a, float l2) {
+  const float v = (-2.f * GLR_LN2) * l2;
+  float q = 1.f / 5040;
+  q = __builtin_fmaf(q, -v, 1.f / 720);
+  q = __builtin_fmaf(q, -v, 1.f / 120);
+  q = __builtin_fmaf(q, -v, 1.f / 24);
+  q = __builtin_fmaf(q, -v, 1.f / 6);
+  q = __builtin_fmaf(q, -v, 0.5f);
+  return v < 0.4f ? v * __builtin_fmaf(q, -v, 1.f) : __builtin_fmaf(-a, a, 1.f);
+}
+
+// A c + B, where A = 0 drops c, whatever it is.
+__device__ __forceinline__ f32x2 glr_map(f32x2 A, f32x2 c, f32x2 B) {
+  return (f32x2){A[0] == 0.f ? B[0] : __builtin_fmaf(A[0], c[0], B[0]), A[1] == 0.f ? B[1] : __builtin_fmaf(A[1], c[1], B[1])};
+}
+__device__ __forceinline__ f32x2 glr_fma(f32x2 a, f32x2 b, f32x2 c) {
+  return (f32x2){__builtin_fmaf(a[0], b[0], c[0]), __builtin_fmaf(a[1], b[1], c[1])};
+}
+
+// The sequence of a row: number n, rows [beg, end).  Behind the last packed
+// sequence n = N and there is no end.
+struct GlrSeq {
+  int n;
+  int64_t beg, end;
+  __device__ __forceinline__ void find(const GlrParams &p, int64_t row) {
+    if (p.cu) {
+      int lo = 0, hi = p.N + 1;  // the first offset behind the row
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] > row) hi = mid;
+        else lo = mid + 1;
+      }
+      n = lo < 1 ? 0 : lo - 1;
+      beg = p.cu[n];
+      end = n < p.N ? p.cu[n + 1] : INT64_MAX;
+    } else {
+      n = (int)(row / p.T);
+      beg = (int64_t)n * p.T;
+      end = beg + p.T;
+    }
+  }
+  // on to the sequence of a later row
+  __device__ __forceinline__ void walk(const GlrParams &p, int64_t row) {
+    while (row >= end) {
+      ++n;
+      beg = end;
+      end = n >= p.N ? INT64_MAX : p.cu ? p.cu[n + 1] : beg + p.T;
+    }
+  }
+  // back to the sequence of an earlier row
+  __device__ __forceinline__ void back(const GlrParams &p, int64_t row) {
+    while (row < beg && n > 0) {
+      --n;
+      end = beg;
+      beg = p.cu ? p.cu[n] : end - p.T;
+    }
+  }
+};
+
+// A segment's rows [row0, row1), the number of its first block of states and
+// the range of segments that its first and last rows' sequences reach.
+struct GlrSegment {
+  int64_t row0, row1, state0;
+  int first, last;
+};
+__device__ __forceinline__ GlrSegment glr_segment(const GlrParams &p, int seg) {
+  GlrSegment s;
+  const int64_t span = (int64_t)p.segt * GLR_TILE;
+  if (p.flat) {
+    s.row0 = seg * span;
+    s.row1 = min(s.row0 + span, p.rows);
+    s.state0 = s.row0 / GLR_STATE;
+    s.first = s.last = seg;
+    if (p.cut && s.row1 > s.row0) {
+      GlrSeq q;
+      q.find(p, s.row0);
+      if (q.n < p.N) s.first = (int)max((int64_t)0, q.beg / span);
+      q.find(p, s.row1 - 1);
+      if (q.n < p.N) s.last = (int)min((int64_t)p.nseg - 1, (q.end - 1) / span);
+    }
+  } else {
+    const int n = seg / p.NS, k = seg - n * p.NS;
+    s.row0 = (int64_t)n * p.T + k * span;
+    s.row1 = min(s.row0 + span, (int64_t)(n + 1) * p.T);
+    s.state0 = (int64_t)n * ((p.T + GLR_STATE - 1) / GLR_STATE) + k * (span / GLR_STATE);
+    s.first = n * p.NS;
+    s.last = s.first + p.NS - 1;
+  }
+  return s;
+}
+
+// The rows of a run that need care: bit j of `starts` (`ends`) where row j is its
+// sequence's first (last), of `dead` where it lies behind the last sequence or
+// behind the segment's end (`live` rows are left of the latter).
+struct GlrFlags {
+  uint32_t starts, ends, dead;
+  int live;
+};
+template <int ROWS>
+__device__ __forceinline__ bool glr_flags(const GlrParams &p, GlrSeq &q, int64_t row, int64_t row1, GlrFlags &f) {
+  f.starts = f.ends = f.dead = 0;
+  f.live = ROWS;
+  q.walk(p, row);
+  if (row > q.beg && row + ROWS < q.end && row + ROWS <= row1 && q.n < p.N) return false;
+  const int64_t left = row1 - row;
+  f.live = left < 0 ? 0 : left < ROWS ? (int)left : ROWS;
+  GlrSeq w = q;
+  for (int j = 0; j < f.live; ++j) {
+    w.walk(p, row + j);
+    if (w.n >= p.N) f.dead |= 1u << j;
+    else {
+      if (row + j == w.beg) f.starts |= 1u << j;
+      if (row + j == w.end - 1) f.ends |= 1u << j;
+    }
+  }
+  return true;
+}
+
+// The ROWS rows of a run, two channels a lane; rows behind the segment's end
+// repeat its last one.
+template <typename E, int ROWS>
+__device__ __forceinline__ void glr_load(const void *src, int64_t row, int64_t row1, int C, int c,
+                                         typename Pair<E>::type (&v)[ROWS]) {
+  const int64_t left = row1 - 1 - row;
+  const int most = left < ROWS - 1 ? (int)left : ROWS - 1;
+  const E *at = static_cast<const E *>(src) + row * C + c;
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j)
+    v[j] = *reinterpret_cast<const typename Pair<E>::type *>(at + (int64_t)min(j, most) * C);
+}
+
+__device__ __forceinline__ f32x2 other_half(f32x2 v) {
+  return (f32x2){__shfl_xor(v[0], 32, 64), __shfl_xor(v[1], 32, 64)};
+}
+
+// Composes the maps of the segments [from, to), in order or (BACK) from the last
+// to the first, and applies them to zero: the waves take contiguous parts.
+template <bool BACK>
+__device__ __forceinline__ f32x2 glr_join(const GlrParams &p, const float *sums, int from, int to, int c, f32x4 *lds) {
+  const int lane = threadIdx.x % GLR_LANES, wave = wave_id();
+  const int per = (to - from + GLR_WAVES - 1) / GLR_WAVES;
+  const int lo = min(from + wave * per, to), hi = min(lo + per, to);
+  f32x2 A = {1.f, 1.f}, B = {0.f, 0.f};
+  for (int k = 0; k < hi - lo; ++k) {
+    const float *m = sums + (size_t)(BACK ? hi - 1 - k : lo + k) * 2 * p.C + c;
+    const f32x2 a = *reinterpret_cast<const f32x2 *>(m), b = *reinterpret_cast<const f32x2 *>(m + p.C);
+    A = (f32x2){a[0] * A[0], a[1] * A[1]};
+    B = glr_map(a, B, b);
+  }
+  if ((threadIdx.x & 32) == 0) lds[wave * GLR_LANES + lane] = (f32x4){A[0], A[1], B[0], B[1]};
+  __syncthreads();
+  f32x2 r = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < GLR_WAVES; ++k) {
+    const f32x4 m = lds[(BACK ? GLR_WAVES - 1 - k : k) * GLR_LANES + lane];
+    r = glr_map((f32x2){m[0], m[1]}, r, (f32x2){m[2], m[3]});
+  }
+  __syncthreads();
+  return r;
+}
+
+}  // namespace dn

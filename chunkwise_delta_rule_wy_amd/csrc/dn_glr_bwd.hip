@@ -1,0 +1,231 @@
+// Gated linear recurrence, backward pass (dn_glr.h has the mathematics).  A
+// workgroup walks through its segment from the last tile to the first.  In a tile
+// the states come forwards from the one kept in front of it, and the gradients
+// go backwards from the tile behind; both exchanges between the runs share one
+// barrier.  The parameters' gradients are summed in registers over the segment,
+// in LDS over the runs and by a second kernel over the segments, in a fixed order.
+#include "dn_glr.h"
+
+namespace dn {
+namespace {
+
+template <typename E, int ROWS>
+__global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
+  typedef typename Pair<E>::type P2;
+  constexpr int TILE = GLR_RUNS * ROWS;
+  static_assert(TILE % GLR_STATE == 0 && GLR_TILE % TILE == 0, "a tile starts with a kept state");
+  __shared__ f32x4 fwd_maps[2][GLR_WAVES][GLR_LANES], bwd_maps[2][GLR_WAVES][GLR_LANES];
+  __shared__ float sums[3][GLR_RUNS][GLR_CH];
+  const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
+  const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = wave_id();
+  const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
+  const bool mine = ch < p.C, upper = threadIdx.x & 32;
+  const GlrSegment s = glr_segment(p, seg);
+  const GlrChannel k0 = glr_channel(p.lam, p.br, p.bi, p.power, c), k1 = glr_channel(p.lam, p.br, p.bi, p.power, c + 1);
+  // sequences without tokens pass dhT on
+  if (p.dh0 && (p.cu || p.T == 0))
+    for (int64_t n = (int64_t)seg * GLR_RUNS + run; n < p.N; n += (int64_t)p.nseg * GLR_RUNS)
+      if (mine && (!p.cu || p.cu[n] == p.cu[n + 1]))
+        *reinterpret_cast<f32x2 *>(p.dh0 + n * p.C + ch) =
+            p.dhT ? *reinterpret_cast<const f32x2 *>(p.dhT + n * p.C + ch) : (f32x2){0.f, 0.f};
+  f32x2 carry = {0.f, 0.f};  // the gradient that reaches the tile from behind
+  if (p.cut) carry = glr_join<true>(p, p.sum_r, seg + 1, s.last + 1, c, &fwd_maps[0][0][0]);
+  f32x2 dlam = {0.f, 0.f}, dbr = {0.f, 0.f}, dbi = {0.f, 0.f};
+  const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
+  P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
+  const auto load = [&](int64_t row) {
+    glr_load<E>(p.x, row, s.row1, p.C, c, x);
+    glr_load<E>(p.r, row, s.row1, p.C, c, r);
+    glr_load<E>(p.i, row, s.row1, p.C, c, i);
+    glr_load<E>(p.dy, row, s.row1, p.C, c, dy);
+  };
+  GlrSeq q = {};
+  if (tiles > 0) {
+    q.find(p, s.row1 - 1);
+    load(s.row0 + (tiles - 1) * TILE + run * ROWS);
+  }
+  int turn = 0;
+  for (int64_t t = tiles - 1; t >= 0; --t, turn ^= 1) {
+    const int64_t row = s.row0 + t * TILE + run * ROWS;
+    f32x2 state = *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
+    q.back(p, row);
+    GlrFlags f;
+    const bool slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
+    // a, 1 - sigmoid(r), m, sigmoid(i), x and dy stay until the gradients
+    f32x2 a[ROWS], sr[ROWS], m[ROWS], si[ROWS], xv[ROWS], dv[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const f32x2 rj = to_f2<E>(r[j]), ij = to_f2<E>(i[j]);
+      xv[j] = to_f2<E>(x[j]);
+      dv[j] = to_f2<E>(dy[j]);
+      sr[j] = (f32x2){glr_sigmoid(rj[0], k0.br), glr_sigmoid(rj[1], k1.br)};
+      si[j] = (f32x2){glr_sigmoid(ij[0], k0.bi), glr_sigmoid(ij[1], k1.bi)};
+      const float l0 = k0.k2 * sr[j][0], l1 = k1.k2 * sr[j][1];
+      a[j] = (f32x2){__builtin_amdgcn_exp2f(l0), __builtin_amdgcn_exp2f(l1)};
+      m[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)), __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1))};
+    }
+    if (t > 0) load(row - TILE);
+    const auto input = [&](int j) {
+      return (f32x2){m[j][0] * si[j][0] * xv[j][0], m[j][1] * si[j][1] * xv[j][1]};
+    };
+    f32x2 A = {1.f, 1.f}, B = {0.f, 0.f}, Ar = {1.f, 1.f}, G = {0.f, 0.f};
+    const auto at = [&](const float *st, int j) {  // row j's sequence of a state
+      GlrSeq w = q;
+      w.walk(p, row + j);
+      return st ? *reinterpret_cast<const f32x2 *>(st + (size_t)w.n * p.C + c) : (f32x2){0.f, 0.f};
+    };
+    if (slow) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        f32x2 aj = a[j], b = input(j);
+        if (j >= f.live) {
+          aj = (f32x2){1.f, 1.f};
+          b = (f32x2){0.f, 0.f};
+        } else if (f.dead >> j & 1) {
+          aj = b = (f32x2){0.f, 0.f};
+        } else if (f.starts >> j & 1) {
+          b = glr_fma(aj, at(p.h0, j), b);
+          aj = (f32x2){0.f, 0.f};
+        }
+        B = glr_map(aj, B, b);
+        A = (f32x2){A[0] * aj[0], A[1] * aj[1]};
+      }
+#pragma unroll
+      for (int j = ROWS - 1; j >= 0; --j) {
+        f32x2 aj = a[j], b = {a[j][0] * dv[j][0], a[j][1] * dv[j][1]};
+        if (j >= f.live) {
+          aj = (f32x2){1.f, 1.f};
+          b = (f32x2){0.f, 0.f};
+        } else if (f.dead >> j & 1) {
+          aj = b = (f32x2){0.f, 0.f};
+        } else if (f.ends >> j & 1) {
+          b = glr_fma(aj, at(p.dhT, j), b);
+          aj = (f32x2){0.f, 0.f};
+        }
+        G = glr_map(aj, G, b);
+        Ar = (f32x2){Ar[0] * aj[0], Ar[1] * aj[1]};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        B = glr_fma(a[j], B, input(j));
+        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
+      }
+#pragma unroll
+      for (int j = ROWS - 1; j >= 0; --j) G = (f32x2){a[j][0] * (dv[j][0] + G[0]), a[j][1] * (dv[j][1] + G[1])};
+      Ar = A;
+    }
+    const f32x2 oA = other_half(A), oB = other_half(B), oAr = other_half(Ar), oG = other_half(G);
+    if (!upper) {
+      const f32x2 tB = glr_map(oA, B, oB);
+      fwd_maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
+    } else {
+      const f32x2 tG = glr_map(oAr, G, oG);
+      bwd_maps[turn][wave][lane] = (f32x4){Ar[0] * oAr[0], Ar[1] * oAr[1], tG[0], tG[1]};
+    }
+    __syncthreads();
+    for (int k = 0; k < wave; ++k) {
+      const f32x4 v = fwd_maps[turn][k][lane];
+      state = glr_map((f32x2){v[0], v[1]}, state, (f32x2){v[2], v[3]});
+    }
+    if (upper) state = glr_map(oA, state, oB);
+    f32x2 g = {0.f, 0.f};
+#pragma unroll
+    for (int k = GLR_WAVES - 1; k >= 0; --k) {
+      if (k == wave) g = carry;
+      const f32x4 v = bwd_maps[turn][k][lane];
+      carry = glr_map((f32x2){v[0], v[1]}, carry, (f32x2){v[2], v[3]});
+    }
+    if (!upper) g = glr_map(oAr, g, oG);
+    // the state in front of every row
+    f32x2 h[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      if (slow && j < f.live && f.starts >> j & 1) state = at(p.h0, j);
+      h[j] = state;
+      state = glr_fma(a[j], state, input(j));
+    }
+#pragma unroll
+    for (int j = ROWS - 1; j >= 0; --j) {
+      const bool dead = slow && (j >= f.live || f.dead >> j & 1);
+      if (slow && !dead && f.ends >> j & 1) g = at(p.dhT, j);
+      f32x2 dx, dr, di, W;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ge = dv[j][e] + g[e], u = si[j][e] * xv[j][e], l = (e ? k1.k2 : k0.k2) * GLR_LN2 * sr[j][e];
+        // l / m is 0 where m is (also where 1 - a^2 fell below the fp32 range)
+        const float over = m[j][e] > 0.f ? l * __builtin_amdgcn_rcpf(m[j][e]) : 0.f;
+        W[e] = ge * (l * a[j][e] * h[j][e] - u * a[j][e] * a[j][e] * over);
+        dr[e] = (1.f - sr[j][e]) * W[e];
+        dx[e] = ge * m[j][e] * si[j][e];
+        di[e] = ge * m[j][e] * u * (1.f - si[j][e]);
+        if (!(slow && j >= f.live)) g[e] = dead ? 0.f : a[j][e] * ge;
+      }
+      if (slow) {
+        if (dead) dx = dr = di = (f32x2){0.f, 0.f};
+        else {
+          dlam += W;
+          dbr += dr;
+          dbi += di;
+          if (p.dh0 && mine && f.starts >> j & 1) {
+            GlrSeq w = q;
+            w.walk(p, row + j);
+            *reinterpret_cast<f32x2 *>(p.dh0 + (size_t)w.n * p.C + ch) = g;
+          }
+        }
+        if (!mine || j >= f.live || (dead && !p.zero_tail)) continue;
+      } else {
+        dlam += W;
+        dbr += dr;
+        dbi += di;
+        if (!mine) continue;
+      }
+      const int64_t o = (row + j) * p.C + ch;
+      *reinterpret_cast<P2 *>(static_cast<E *>(p.dx) + o) = to_e2<E>(dx);
+      *reinterpret_cast<P2 *>(static_cast<E *>(p.dr) + o) = to_e2<E>(dr);
+      *reinterpret_cast<P2 *>(static_cast<E *>(p.di) + o) = to_e2<E>(di);
+    }
+  }
+  *reinterpret_cast<f32x2 *>(&sums[0][run][2 * lane]) = dlam;
+  *reinterpret_cast<f32x2 *>(&sums[1][run][2 * lane]) = dbr;
+  *reinterpret_cast<f32x2 *>(&sums[2][run][2 * lane]) = dbi;
+  __syncthreads();
+  const int which = threadIdx.x / GLR_CH, col = threadIdx.x % GLR_CH;
+  if (which >= 3 || grp * GLR_CH + col >= p.C) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < GLR_RUNS; ++k) sum += sums[which][k][col];
+  p.part[((size_t)seg * 3 + which) * p.C + grp * GLR_CH + col] = sum;
+}
+
+// The parameters' gradients from the segments' sums.
+__global__ __launch_bounds__(ROW_THREADS) void glr_param_kernel(GlrParams p) {
+  const int64_t col0 = (int64_t)blockIdx.x * SUM_COLS, n = 3 * (int64_t)p.C, col = col0 + threadIdx.x;
+  const float a = column_sum(p.part, p.nseg, n, col0);
+  if (threadIdx.x >= SUM_COLS || col >= n) return;
+  const int which = (int)(col / p.C), c = (int)(col - (int64_t)which * p.C);
+  if (which == 0) {
+    // sigmoid(lam) / softplus(lam) is 1 to fp32's last digit where e^lam is below 2^-24
+    const float lam = p.lam[c];
+    p.dlam[c] = lam < -20.f ? a : a / ((1.f + expf(-lam)) * glr_softplus(lam));
+  } else if (which == 1) {
+    if (p.dbr) p.dbr[c] = a;
+  } else if (p.dbi) {
+    p.dbi[c] = a;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_glr_bwd(const GlrParams &p, int dtype, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
+  if (dtype == 1) hipLaunchKernelGGL((glr_bwd_kernel<bf16, 4>), grid, thr, 0, st, p);
+  else hipLaunchKernelGGL((glr_bwd_kernel<float, 4>), grid, thr, 0, st, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(glr_param_kernel, dim3((unsigned)((3 * (int64_t)p.C + SUM_COLS - 1) / SUM_COLS)), dim3(ROW_THREADS), 0,
+                     st, p);
+  return hipGetLastError();
+}
+
+}  // namespace dn

@@ -1,0 +1,248 @@
+// Gated linear recurrence, forward pass, segment maps of both directions, and
+// the single-token step (dn_glr.h has the mathematics).
+#include "dn_glr.h"
+
+namespace dn {
+namespace {
+
+constexpr int ROWS = GLR_TILE / GLR_RUNS;  // rows of a run
+
+// The maps of whole segments: a thread walks through one sixteenth of its
+// segment's rows, and the runs' maps meet in LDS at the end.
+template <typename E, bool BACK>
+__global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
+  typedef typename Pair<E>::type P2;
+  __shared__ f32x4 maps[GLR_RUNS][GLR_LANES];
+  const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
+  const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES;
+  const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
+  const GlrSegment s = glr_segment(p, seg);
+  const GlrChannel k0 = glr_channel(p.lam, p.br, p.bi, p.power, c), k1 = glr_channel(p.lam, p.br, p.bi, p.power, c + 1);
+  const int per = p.segt * (GLR_TILE / GLR_RUNS);  // rows of a run, a multiple of ROWS
+  const int64_t beg = s.row0 + (int64_t)run * per, end = min(beg + per, s.row1);
+  f32x2 A = {1.f, 1.f}, B = {0.f, 0.f};
+  GlrSeq q;
+  if (beg < end) q.find(p, beg);
+  // in row order: going back the maps are composed on the other side, c -> A (a c + b) + B
+  for (int64_t row = beg; row < end; row += ROWS) {
+    P2 r[ROWS], x[ROWS], i[ROWS];
+    glr_load<E>(p.r, row, end, p.C, c, r);
+    glr_load<E>(BACK ? p.dy : p.x, row, end, p.C, c, x);
+    if (!BACK) glr_load<E>(p.i, row, end, p.C, c, i);
+    GlrFlags f;
+    const bool slow = glr_flags<ROWS>(p, q, row, end, f);
+    GlrSeq w = q;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const f32x2 rj = to_f2<E>(r[j]), xj = to_f2<E>(x[j]);
+      const float s0 = glr_sigmoid(rj[0], k0.br), s1 = glr_sigmoid(rj[1], k1.br);
+      f32x2 a = {__builtin_amdgcn_exp2f(k0.k2 * s0), __builtin_amdgcn_exp2f(k1.k2 * s1)}, b;
+      if (BACK) {
+        b = (f32x2){a[0] * xj[0], a[1] * xj[1]};
+      } else {
+        const f32x2 ij = to_f2<E>(i[j]);
+        b = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[0], k0.k2 * s0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
+                    __builtin_amdgcn_sqrtf(glr_rest(a[1], k1.k2 * s1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
+      }
+      if (slow) {
+        if (j >= f.live) {
+          a = (f32x2){1.f, 1.f};
+          b = (f32x2){0.f, 0.f};
+        } else if (f.dead >> j & 1) {
+          a = b = (f32x2){0.f, 0.f};
+        } else if ((BACK ? f.ends : f.starts) >> j & 1) {
+          // the state in front of the row, or the gradient behind it, is h0 or dhT
+          w.walk(p, row + j);
+          const float *st = BACK ? p.dhT : p.h0;
+          if (st) b = glr_fma(a, *reinterpret_cast<const f32x2 *>(st + (size_t)w.n * p.C + c), b);
+          a = (f32x2){0.f, 0.f};
+        }
+      }
+      if (BACK) {
+        B = glr_map(A, b, B);
+        A = (f32x2){A[0] * a[0], A[1] * a[1]};
+      } else {
+        B = glr_map(a, B, b);
+        A = (f32x2){a[0] * A[0], a[1] * A[1]};
+      }
+    }
+  }
+  maps[run][lane] = (f32x4){A[0], A[1], B[0], B[1]};
+  __syncthreads();
+  if (threadIdx.x >= GLR_LANES || ch >= p.C) return;
+  A = (f32x2){1.f, 1.f};
+  B = (f32x2){0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < GLR_RUNS; ++k) {
+    const f32x4 m = maps[BACK ? GLR_RUNS - 1 - k : k][lane];
+    A = (f32x2){A[0] * m[0], A[1] * m[1]};
+    B = glr_map((f32x2){m[0], m[1]}, B, (f32x2){m[2], m[3]});
+  }
+  float *out = (BACK ? p.sum_r : p.sum_f) + (size_t)seg * 2 * p.C + ch;
+  *reinterpret_cast<f32x2 *>(out) = A;
+  *reinterpret_cast<f32x2 *>(out + p.C) = B;
+}
+
+template <typename E>
+__global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
+  typedef typename Pair<E>::type P2;
+  __shared__ f32x4 maps[2][GLR_WAVES][GLR_LANES];
+  const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
+  const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = wave_id();
+  const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
+  const bool mine = ch < p.C;
+  const GlrSegment s = glr_segment(p, seg);
+  const GlrChannel k0 = glr_channel(p.lam, p.br, p.bi, p.power, c), k1 = glr_channel(p.lam, p.br, p.bi, p.power, c + 1);
+  // sequences without tokens pass h0 on
+  if (p.hT && (p.cu || p.T == 0))
+    for (int64_t n = (int64_t)seg * GLR_RUNS + run; n < p.N; n += (int64_t)p.nseg * GLR_RUNS)
+      if (mine && (!p.cu || p.cu[n] == p.cu[n + 1]))
+        *reinterpret_cast<f32x2 *>(p.hT + n * p.C + ch) =
+            p.h0 ? *reinterpret_cast<const f32x2 *>(p.h0 + n * p.C + ch) : (f32x2){0.f, 0.f};
+  f32x2 carry = {0.f, 0.f};  // the state in front of the tile
+  if (p.cut) carry = glr_join<false>(p, p.sum_f, s.first, seg, c, &maps[0][0][0]);
+  if (s.row0 >= s.row1) return;
+  GlrSeq q;
+  q.find(p, s.row0);
+  P2 x[ROWS], r[ROWS], i[ROWS];
+  const auto load = [&](int64_t row) {
+    glr_load<E>(p.x, row, s.row1, p.C, c, x);
+    glr_load<E>(p.r, row, s.row1, p.C, c, r);
+    glr_load<E>(p.i, row, s.row1, p.C, c, i);
+  };
+  load(s.row0 + run * ROWS);
+  int turn = 0;
+  int64_t block = s.state0;
+  for (int64_t tile = s.row0; tile < s.row1; tile += GLR_TILE, turn ^= 1, block += GLR_TILE / GLR_STATE) {
+    const int64_t row = tile + run * ROWS;
+    GlrFlags f;
+    const bool slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
+    f32x2 a[ROWS], b[ROWS], A = {1.f, 1.f}, B = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const f32x2 xj = to_f2<E>(x[j]), rj = to_f2<E>(r[j]), ij = to_f2<E>(i[j]);
+      const float l0 = k0.k2 * glr_sigmoid(rj[0], k0.br), l1 = k1.k2 * glr_sigmoid(rj[1], k1.br);
+      a[j] = (f32x2){__builtin_amdgcn_exp2f(l0), __builtin_amdgcn_exp2f(l1)};
+      b[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
+                     __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
+    }
+    if (tile + GLR_TILE < s.row1) load(row + GLR_TILE);
+    if (slow) {
+      GlrSeq w = q;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        if (j >= f.live) {
+          a[j] = (f32x2){1.f, 1.f};
+          b[j] = (f32x2){0.f, 0.f};
+        } else if (f.dead >> j & 1) {
+          a[j] = b[j] = (f32x2){0.f, 0.f};
+        } else if (f.starts >> j & 1) {
+          w.walk(p, row + j);
+          if (p.h0) b[j] = glr_fma(a[j], *reinterpret_cast<const f32x2 *>(p.h0 + (size_t)w.n * p.C + c), b[j]);
+          a[j] = (f32x2){0.f, 0.f};
+        }
+        B = glr_map(a[j], B, b[j]);
+        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        B = glr_fma(a[j], B, b[j]);
+        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
+      }
+    }
+    // a wave's two runs, then the waves
+    const f32x2 oA = other_half(A), oB = other_half(B);
+    const bool upper = threadIdx.x & 32;
+    if (!upper) {
+      const f32x2 tB = glr_map(oA, B, oB);
+      maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
+    }
+    __syncthreads();
+    f32x2 h = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < GLR_WAVES; ++k) {
+      if (k == wave) h = carry;
+      if (p.states && k % (GLR_WAVES * GLR_STATE / GLR_TILE) == 0 && k == wave && !upper && mine &&
+          tile + k * (GLR_TILE / GLR_WAVES) < s.row1)
+        *reinterpret_cast<f32x2 *>(p.states + (block + k / (GLR_WAVES * GLR_STATE / GLR_TILE)) * p.C + ch) = carry;
+      const f32x4 m = maps[turn][k][lane];
+      carry = glr_map((f32x2){m[0], m[1]}, carry, (f32x2){m[2], m[3]});
+    }
+    if (upper) h = glr_map(oA, h, oB);
+    E *y = static_cast<E *>(p.y) + row * p.C + ch;
+    if (slow) {
+      GlrSeq w = q;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        h = glr_map(a[j], h, b[j]);
+        if (j < f.live && mine) {
+          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<P2 *>(y + (int64_t)j * p.C) = to_e2<E>(h);
+          if (p.hT && f.ends >> j & 1) {
+            w.walk(p, row + j);
+            *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + ch) = h;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        h = glr_fma(a[j], h, b[j]);
+        if (p.y && mine) *reinterpret_cast<P2 *>(y + (int64_t)j * p.C) = to_e2<E>(h);
+      }
+    }
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
+  constexpr int V = 4;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (at >= p.n) return;
+  typedef typename four<E>::type E4;
+  const E4 x = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.x) + at);
+  const E4 r = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.r) + at);
+  const E4 i = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.i) + at);
+  f32x4 h = *reinterpret_cast<const f32x4 *>(p.state + at);
+  const int c = (int)(at % p.C);
+  E4 y;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const GlrChannel k = glr_channel(p.lam, p.br, p.bi, p.power, c + e);
+    const float l2 = k.k2 * glr_sigmoid(to_f<E>(r[e]), k.br), a = __builtin_amdgcn_exp2f(l2);
+    h[e] = __builtin_fmaf(a, h[e], __builtin_amdgcn_sqrtf(glr_rest(a, l2)) * glr_sigmoid(to_f<E>(i[e]), k.bi) * to_f<E>(x[e]));
+    y[e] = to_e<E>(h[e]);
+  }
+  *reinterpret_cast<f32x4 *>(p.state + at) = h;
+  *reinterpret_cast<E4 *>(static_cast<E *>(p.y) + at) = y;
+}
+
+}  // namespace
+
+hipError_t launch_glr_sum(const GlrParams &p, int dtype, bool backward, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
+  if (dtype == 1) {
+    if (backward) hipLaunchKernelGGL((glr_sum_kernel<bf16, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_sum_kernel<bf16, false>), grid, thr, 0, st, p);
+  } else {
+    if (backward) hipLaunchKernelGGL((glr_sum_kernel<float, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_sum_kernel<float, false>), grid, thr, 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_glr_fwd(const GlrParams &p, int dtype, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
+  if (dtype == 1) hipLaunchKernelGGL(glr_fwd_kernel<bf16>, grid, thr, 0, st, p);
+  else hipLaunchKernelGGL(glr_fwd_kernel<float>, grid, thr, 0, st, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_glr_step(const GlrStepParams &p, int dtype, hipStream_t st) {
+  const dim3 grid((unsigned)((p.n / 4 + 255) / 256)), thr(256);
+  if (dtype == 1) hipLaunchKernelGGL(glr_step_kernel<bf16>, grid, thr, 0, st, p);
+  else hipLaunchKernelGGL(glr_step_kernel<float>, grid, thr, 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace dn

@@ -1,0 +1,305 @@
+// Product of 8-bit rows with 8-bit weights, with its epilogue, for gfx950:
+//
+//   y[m, n] = act(xs[m] ws[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+//
+// x and w are 8-bit floats (4 exponent and 3 mantissa bits), act is none, silu
+// or gelu, y is rounded to bf16 once.
+//
+// The products are the matrix instructions of 128 indices (16 x 16) and of 64
+// (32 x 32); their rate is 4.4 to 4.5 PFLOP/s.  A lane gives them 32 bytes of one
+// row; which of a block's indices these are is free, as long as x and w agree.
+// w is the left operand, so that a lane's results are consecutive columns n of
+// one row m.
+//
+// Many rows: tiles of x and w pass through LDS, a block of 128 indices at a time,
+// loaded directly (no registers) one block ahead.  A row of a tile is 128 bytes,
+// the span of the LDS banks; its 16-byte units are stored at unit ^ (row & 7), so
+// that eight lanes reading one unit of eight rows meet all banks.
+//
+// Few rows: the weights are the traffic, and no tile of them is used twice, so
+// that they go from memory to registers; a workgroup takes 16 columns and its
+// waves share the indices.
+#include "dn.h"
+#include "dn_internal.h"
+#include "dn_wy.h"
+
+namespace dn {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int BK = 128;  // indices (bytes of a row) of a tile
+
+enum Act { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
+
+struct Linear8Params {
+  const uint8_t *x, *w;
+  const float *xs, *ws, *bias;  // bias may be null
+  const bf16 *residual;         // may be null
+  bf16 *y;
+  int M, N, K;
+  int act;
+  int tm, tn;  // tiles over M and N
+};
+
+// what a lane reads instead of a row's indices behind K
+__device__ const u128 g_zero16 = {{0, 0, 0, 0}};
+
+__device__ __forceinline__ float apply(float z, int act) {
+  if (act == ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
+  if (act == ACT_GELU) return 0.5f * z * (1.f + erff(0.70710678118654752440f * z));
+  return z;
+}
+
+// Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD
+// gets a contiguous range of tiles, which run through bands of BAND rows of tiles, so
+// that the tiles which are side by side in time share rows of x and of w in one L2.
+constexpr int BAND = 4;
+__device__ __forceinline__ void tile_of(const Linear8Params &p, int &tm, int &tn) {
+  const int total = p.tm * p.tn, q = total >> 3, r = total & 7, xcd = blockIdx.x & 7;
+  const int t = xcd * q + min(xcd, r) + (blockIdx.x >> 3);
+  const int band = t / (BAND * p.tn), in = t - band * BAND * p.tn, high = min(BAND, p.tm - band * BAND);
+  tm = band * BAND + in % high;
+  tn = in / high;
+}
+
+// A 32-byte operand: the units `unit` (even) and unit + 1 of a row of a tile.
+__device__ __forceinline__ i32x8 operand(uint32_t tile, int row, int unit) {
+  const uint32_t at = tile + row * BK;
+  const i32x4 lo = wy::ld<i32x4>(at + ((unit ^ (row & 7)) << 4)), hi = wy::ld<i32x4>(at + (((unit + 1) ^ (row & 7)) << 4));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kernel(Linear8Params p) {
+  constexpr int WAVES = (TM / WM) * (TN / WN), STAGE = (TM + TN) * BK, NM = WM / 32, NN = WN / 32;
+  constexpr int PITCH = WN + 4;  // epilogue: fp32 rows, 16 bytes off the banks' span
+  constexpr int LDS = 2 * STAGE > WAVES * 32 * PITCH * 4 ? 2 * STAGE : WAVES * 32 * PITCH * 4;
+  __shared__ __attribute__((aligned(128))) char lds[LDS];
+  const uint32_t base = (uint32_t)(size_t)(__attribute__((address_space(3))) char *)lds;
+  const int lane = lane_id(), wave = wave_id();
+  int tm, tn;
+  tile_of(p, tm, tn);
+  const int m0 = tm * TM, n0 = tn * TN;
+
+  // A wave's share of a tile's rows, eight at a time: rows of w first, then of x.
+  constexpr int PIECES = (TM + TN) / 8 / WAVES;
+  static_assert(PIECES * 8 * WAVES == TM + TN && TN % 8 == 0, "the waves share the rows evenly");
+  const uint8_t *src[PIECES];
+  const int unit = (lane & 7) ^ (lane >> 3);  // the unit that lands at lane % 8 of its row
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) {
+    const int r = (j * WAVES + wave) * 8 + (lane >> 3);
+    src[j] = r < TN ? p.w + (size_t)min(n0 + r, p.N - 1) * p.K : p.x + (size_t)min(m0 + r - TN, p.M - 1) * p.K;
+    src[j] += unit * 16;
+  }
+  const auto load = [&](int k, int stage) {
+    const bool some = k + BK <= p.K || k + unit * 16 < p.K;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
+      wy::dma16(some ? (const void *)(src[j] + k) : (const void *)&g_zero16, base + stage * STAGE + (j * WAVES + wave) * 1024);
+  };
+
+  const int wm = (wave % (TM / WM)) * WM, wn = (wave / (TM / WM)) * WN;
+  const int row = lane & 31, half = lane >> 5;
+  f32x16 acc[NN][NM];
+#pragma unroll
+  for (int a = 0; a < NN; ++a)
+#pragma unroll
+    for (int b = 0; b < NM; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  load(0, 0);
+  int stage = 0;
+  for (int k = 0; k < p.K; k += BK, stage ^= 1) {
+    wy::wait_vm<0>();
+    __syncthreads();
+    if (k + BK < p.K) load(k + BK, stage ^ 1);
+    const uint32_t tw = base + stage * STAGE + wn * BK, tx = base + stage * STAGE + (TN + wm) * BK;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      i32x8 fw[NN], fx[NM];
+#pragma unroll
+      for (int a = 0; a < NN; ++a) fw[a] = operand(tw, 32 * a + row, 4 * ks + 2 * half);
+#pragma unroll
+      for (int b = 0; b < NM; ++b) fx[b] = operand(tx, 32 * b + row, 4 * ks + 2 * half);
+#pragma unroll
+      for (int a = 0; a < NN; ++a)
+#pragma unroll
+        for (int b = 0; b < NM; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[a], fx[b], acc[a][b], 0, 0, 0, 0, 0, 0);
+    }
+  }
+
+  // Epilogue: 32 rows m at a time through the wave's own part of LDS, from where
+  // whole rows are stored.
+  mfma_settle();
+  __syncthreads();
+  float *part = reinterpret_cast<float *>(lds) + wave * 32 * PITCH;
+  const int nw = n0 + wn;
+#pragma unroll
+  for (int b = 0; b < NM; ++b) {
+    const int mb = m0 + wm + 32 * b;
+    const float xs = p.xs[min(mb + row, p.M - 1)];
+#pragma unroll
+    for (int a = 0; a < NN; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 32 * a + 8 * i + 4 * half;
+        f32x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = min(nw + n + e, p.N - 1);
+          z[e] = apply(acc[a][b][4 * i + e] * xs * p.ws[c] + (p.bias ? p.bias[c] : 0.f), p.act);
+        }
+        *reinterpret_cast<f32x4 *>(part + row * PITCH + n) = z;
+      }
+    wave_lds_fence();
+    if ((p.N & 7) == 0) {
+      constexpr int LPR = WN / 8;
+      const int n = (lane % LPR) * 8;
+#pragma unroll
+      for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+        if (mb + r < p.M && nw + n < p.N) {
+          const f32x4 lo = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n);
+          const f32x4 hi = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n + 4);
+          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          const size_t at = (size_t)(mb + r) * p.N + nw + n;
+          if (p.residual) {
+            const bf16x8 res = *reinterpret_cast<const bf16x8 *>(p.residual + at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += to_f<bf16>(res[e]);
+          }
+          *reinterpret_cast<u32x4 *>(p.y + at) =
+              (u32x4){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
+        }
+      }
+    } else {
+      for (int o = lane; o < 32 * WN; o += 64) {
+        const int r = o / WN, n = o % WN;
+        if (mb + r < p.M && nw + n < p.N) {
+          const size_t at = (size_t)(mb + r) * p.N + nw + n;
+          const float v = part[r * PITCH + n];
+          p.y[at] = to_e<bf16>(p.residual ? v + to_f<bf16>(p.residual[at]) : v);
+        }
+      }
+    }
+    wave_lds_fence();
+  }
+}
+
+// Few rows: 16 columns a workgroup, blocks of 128 indices dealt to the waves.
+constexpr int FEW_WAVES = 8, FEW_BATCH = 4;
+
+template <int MT>
+__global__ __launch_bounds__(64 * FEW_WAVES) void linear8_few_kernel(Linear8Params p) {
+  __shared__ float part[FEW_WAVES][16 * MT][20];
+  const int lane = lane_id(), wave = wave_id(), row = lane & 15, off = 32 * (lane >> 4);
+  const int n0 = blockIdx.x * 16;
+  const uint8_t *w = p.w + (size_t)min(n0 + row, p.N - 1) * p.K + off;
+  const uint8_t *x[MT];
+#pragma unroll
+  for (int b = 0; b < MT; ++b) x[b] = p.x + (size_t)min(16 * b + row, p.M - 1) * p.K + off;
+  const auto get = [&](const uint8_t *src, int k) {
+    i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+    if (k + off < p.K) lo = *reinterpret_cast<const i32x4 *>(src + k);
+    if (k + off + 16 < p.K) hi = *reinterpret_cast<const i32x4 *>(src + k + 16);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int b = 0; b < MT; ++b) acc[b] = zero4();
+  for (int k = wave * BK; k < p.K; k += FEW_BATCH * FEW_WAVES * BK) {
+    i32x8 fw[FEW_BATCH], fx[FEW_BATCH][MT];
+#pragma unroll
+    for (int j = 0; j < FEW_BATCH; ++j) {
+      fw[j] = get(w, k + j * FEW_WAVES * BK);
+#pragma unroll
+      for (int b = 0; b < MT; ++b) fx[j][b] = get(x[b], k + j * FEW_WAVES * BK);
+    }
+#pragma unroll
+    for (int j = 0; j < FEW_BATCH; ++j)
+#pragma unroll
+      for (int b = 0; b < MT; ++b)
+        acc[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fx[j][b], acc[b], 0, 0, 0, 0, 0, 0);
+  }
+  mfma_settle();
+#pragma unroll
+  for (int b = 0; b < MT; ++b) *reinterpret_cast<f32x4 *>(&part[wave][16 * b + row][4 * (lane >> 4)]) = acc[b];
+  __syncthreads();
+  for (int o = threadIdx.x; o < 256 * MT; o += 64 * FEW_WAVES) {
+    const int m = o >> 4, n = o & 15;
+    if (m >= p.M || n0 + n >= p.N) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < FEW_WAVES; ++k) s += part[k][m][n];
+    s = apply(s * p.xs[m] * p.ws[n0 + n] + (p.bias ? p.bias[n0 + n] : 0.f), p.act);
+    const size_t at = (size_t)m * p.N + n0 + n;
+    if (p.residual) s += to_f<bf16>(p.residual[at]);
+    p.y[at] = to_e<bf16>(s);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+template <int TM, int TN, int WM, int WN>
+hipError_t launch_tile(Linear8Params &p, hipStream_t st) {
+  p.tm = (p.M + TM - 1) / TM;
+  p.tn = (p.N + TN - 1) / TN;
+  hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN>), dim3((unsigned)(p.tm * p.tn)), dim3(64 * (TM / WM) * (TN / WN)),
+                     0, st, p);
+  return hipGetLastError();
+}
+
+template <int MT>
+hipError_t launch_few(const Linear8Params &p, hipStream_t st) {
+  hipLaunchKernelGGL(linear8_few_kernel<MT>, dim3((unsigned)((p.N + 15) / 16)), dim3(64 * FEW_WAVES), 0, st, p);
+  return hipGetLastError();
+}
+
+int64_t tiles(const Linear8Params &p, int t) { return (int64_t)((p.M + t - 1) / t) * ((p.N + t - 1) / t); }
+
+hipError_t launch(Linear8Params &p, hipStream_t st) {
+  if (p.M <= 16) return launch_few<1>(p, st);
+  if (p.M <= 32) return launch_few<2>(p, st);
+  if (p.M <= 64) return launch_few<4>(p, st);
+  // the largest tiles that give the 256 CUs one each
+  if (tiles(p, 256) >= 256) return launch_tile<256, 256, 128, 128>(p, st);
+  if (tiles(p, 128) >= 256) return launch_tile<128, 128, 64, 64>(p, st);
+  return launch_tile<64, 64, 32, 32>(p, st);
+}
+
+}  // namespace
+}  // namespace dn
+
+using namespace dn;
+
+extern "C" dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, const float *xs, const void *w,
+                                const float *ws, const float *bias, const void *residual, int32_t act, void *y,
+                                hipStream_t stream) {
+  if (M < 0 || N <= 0 || K <= 0 || act < ACT_NONE || act > ACT_GELU) return DN_EINVAL;
+  // the rows' 16-byte units, the tiles' count, and the byte offsets within a row
+  if (K % 16 != 0 || K > INT32_MAX - BK * FEW_WAVES * FEW_BATCH) return DN_EUNSUPPORTED;
+  if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) > UINT32_MAX / 256 || N > INT32_MAX - 256 || M > INT32_MAX - 256)
+    return DN_EUNSUPPORTED;
+  if (M == 0) return DN_OK;
+  if (!x || !xs || !w || !ws || !y) return DN_EINVAL;
+  for (const void *q : {x, w, residual, static_cast<const void *>(y)})
+    if (reinterpret_cast<uintptr_t>(q) & 15u) return DN_EINVAL;
+  Linear8Params p = {};
+  p.x = static_cast<const uint8_t *>(x);
+  p.w = static_cast<const uint8_t *>(w);
+  p.xs = xs;
+  p.ws = ws;
+  p.bias = bias;
+  p.residual = static_cast<const bf16 *>(residual);
+  p.y = static_cast<bf16 *>(y);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  return launch(p, stream) == hipSuccess ? DN_OK : DN_EHIP;
+}

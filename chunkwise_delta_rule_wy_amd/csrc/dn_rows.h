@@ -1,6 +1,7 @@
-// Row-wise streaming helpers for the per-(token, head) kernels: a row of Dk
-// elements is read by Dk / N lanes, 16 bytes each (N = 8 for bf16, 4 for
-// fp32); the lanes of a row sit in one wave, so row sums are lane shuffles.
+// Row-wise streaming helpers.  The per-(token, head) kernels read a row of Dk
+// elements by Dk / N lanes, 16 bytes each (N = 8 for bf16, 4 for fp32); the
+// lanes of a row sit in one wave, so row sums are lane shuffles.  The norms'
+// rows are wider (Row).
 #pragma once
 
 #include "dn_internal.h"
@@ -57,6 +58,82 @@ template <int N>
 __device__ __forceinline__ void store_f32(float *dst, const float (&x)[N]) {
 #pragma unroll
   for (int e = 0; e < N; e += 4) *reinterpret_cast<f32x4 *>(dst + e) = (f32x4){x[e], x[e + 1], x[e + 2], x[e + 3]};
+}
+
+// Wide rows: a row of D values (a multiple of 8) lies in the registers of LPR
+// lanes, K units of 16 bytes of E per lane; values of another type T (fp32
+// beside bf16) come and go by the same units.  LPR is part of a wave, or the
+// whole workgroup of ROW_THREADS.
+template <typename E, int LPR, int K>
+struct Row {
+  static constexpr int V = Vec16<E>::N, N = K * V;
+  __device__ static __forceinline__ int col(int k, int lane) { return (k * LPR + lane) * V; }
+  template <typename T>
+  __device__ static __forceinline__ void load(const T *src, int lane, int D, float (&x)[N]) {
+    constexpr int U = Vec16<T>::N;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = col(k, lane);
+      if (c < D) {
+#pragma unroll
+        for (int u = 0; u < V; u += U) {
+          const typename Vec16<T>::type v = *reinterpret_cast<const typename Vec16<T>::type *>(src + c + u);
+#pragma unroll
+          for (int e = 0; e < U; ++e) x[k * V + u + e] = to_f<T>(v[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[k * V + e] = 0.f;
+      }
+    }
+  }
+  __device__ static __forceinline__ void load_w(const float *src, int lane, int D, float (&x)[N]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = col(k, lane);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[k * V + e] = c < D ? src[c + e] : 0.f;
+    }
+  }
+  template <typename T>
+  __device__ static __forceinline__ void store(T *dst, int lane, int D, const float (&x)[N]) {
+    constexpr int U = Vec16<T>::N;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = col(k, lane);
+      if (c >= D) continue;
+#pragma unroll
+      for (int u = 0; u < V; u += U) {
+        typename Vec16<T>::type v;
+#pragma unroll
+        for (int e = 0; e < U; ++e) v[e] = to_e<T>(x[k * V + u + e]);
+        *reinterpret_cast<typename Vec16<T>::type *>(dst + c + u) = v;
+      }
+    }
+  }
+};
+
+// sum (or, with MAX, maximum) over a row's lanes; a row as wide as the workgroup
+// goes through LDS (two buffers taken in turn, one barrier a sum)
+template <int LPR, bool MAX = false>
+__device__ __forceinline__ float lanes_sum(float x, float (*buf)[ROW_THREADS / 64], int &turn) {
+  if constexpr (MAX) {
+#pragma unroll
+    for (int m = 1; m < (LPR < 64 ? LPR : 64); m <<= 1) x = fmaxf(x, __shfl_xor(x, m, 64));
+  } else {
+    x = group_sum<(LPR < 64 ? LPR : 64)>(x);
+  }
+  if constexpr (LPR > 64) {
+    float *b = buf[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < LPR / 64; ++i) s = MAX ? fmaxf(s, b[i]) : s + b[i];
+    return s;
+  }
+  return x;
 }
 
 // Sums over the rows of a [rows][n] fp32 matrix (n a multiple of 4), for the

@@ -554,6 +554,131 @@ dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32_t dtype, c
                             void *dx, void *dz, float *dw,
                             void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Gated linear recurrence, channel by channel (the diagonal case of the gated
+ * recurrences above, S_t = alpha_t S_{t-1} + ..., with a decay and an input gate
+ * of every channel's own): per sequence and channel of the H D,
+ *
+ *     s_t = sigmoid(r_t + br),   a_t = exp(-power softplus(lam) s_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + bi) x_t,   y_t = h_t
+ *
+ * - x, r, i, y [B,T,H,D] in the dtype (r, i before bias and sigmoid); lam, br,
+ *   bi [H,D] fp32 (br, bi NULL: zero); h0, hT [N,H,D] fp32 (h0 NULL: zero; hT NULL:
+ *   not written); power > 0.  x, r, i, y, states and their gradients 16-byte
+ *   aligned.
+ * - Packed sequences by cu_seqlens with B == 1, cu[n_seqs] <= T and DN_ZERO_TAIL as
+ *   in dn_ssm_fwd.  A sequence without tokens passes h0 through to hT.
+ * - States are fp32 throughout; y and the gradients in the dtype are rounded once.
+ * - A recurrence gate r of minus infinity gives a = 1 exactly: the token leaves
+ *   the state as it is.  A value that is not finite reaches its own channel's
+ *   later tokens of its sequence (in the backward pass also the earlier ones);
+ *   it does not cross sequences or channels.
+ * - `states`, from the forward to the backward pass: the fp32 states that the
+ *   backward pass starts from, dn_glr_states(...) rows of H D (NULL: not written, or
+ *   computed again by the backward pass).  They belong to the call's inputs,
+ *   sizes and cu_seqlens.
+ * - D a multiple of 8, H D up to 2^23, B T below 2^31, segments of the rows times
+ *   blocks of 64 channels below 2^23 (DN_EUNSUPPORTED otherwise).  No atomics:
+ *   results repeat bit for bit.
+ */
+size_t dn_glr_states(int32_t B, int32_t T, int32_t H, int32_t D);
+
+/* Bytes of device workspace (16-byte aligned); they cover packed input where
+ * B == 1.  with_states: the backward pass is given `states`. */
+size_t dn_glr_fwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D);
+size_t dn_glr_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D, int32_t with_states);
+
+dn_status dn_glr_fwd(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int32_t dtype, const void *x,
+                     const void *r, const void *i, const float *lam, const float *br, const float *bi, float power,
+                     const float *h0, const int32_t *cu_seqlens, void *y, float *hT, float *states,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Backward pass of L = <dy, y> + <dhT, hT> (dy [B,T,H,D] in the dtype, dhT NULL: 0):
+ * dx, dr, di in the dtype, dlam, dbr, dbi [H,D] and dh0 [N,H,D] in fp32; dbr, dbi
+ * and dh0 may be NULL (not written).
+ */
+dn_status dn_glr_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int32_t dtype, const void *x,
+                     const void *r, const void *i, const float *lam, const float *br, const float *bi, float power,
+                     const float *h0, const int32_t *cu_seqlens, const float *states, const void *dy, const float *dhT,
+                     void *dx, void *dr, void *di, float *dlam, float *dbr, float *dbi, float *dh0,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of B sequences: x, r, i, y [B,H,D]; state [B,H,D] fp32, read and
+ * overwritten.
+ */
+dn_status dn_glr_step(int32_t B, int32_t H, int32_t D, int32_t dtype, const void *x, const void *r, const void *i,
+                      const float *lam, const float *br, const float *bi, float power, float *state, void *y,
+                      hipStream_t stream);
+
+/*
+ * The residual's addition in front of a layer, with dropout and root-mean-square
+ * norm of `rows` rows of D values:
+ *
+ *     h = residual + d x,   d = 0 with probability p, else 1 / (1 - p)
+ *     y = h / sqrt(mean(h^2) + eps) * w
+ *
+ * - x, y [rows, D] in the dtype; residual, h [rows, D] in res_dtype (the dtype, or
+ *   DN_F32; residual NULL: zero; h NULL: not written); w [D] fp32.  h is rounded
+ *   to res_dtype and y is the norm of the rounded values.  y may alias x, and h the
+ *   residual, where their types agree; no other outputs may alias inputs.
+ * - p is taken to the nearest multiple of 2^-16, below 1.  With p > 0, seed points to
+ *   two 64-bit words in device memory, a key and the number of a stream (a layer's,
+ *   a step's): value j of row i is dropped where 16 bits are below 65536 p, bits
+ *   16 (j % 8) and up of the 128 that Philox4x32 with 7 rounds (Salmon et al.,
+ *   "Parallel random numbers: as easy as 1, 2, 3", 2011) gives for the counter
+ *   (block, stream), block = (i D + j) / 8, both 64 bits with the lower word first.
+ *   The mask depends on nothing else and is not stored.
+ * - D a multiple of 8 up to 8192, rows below 2^31 (DN_EUNSUPPORTED otherwise); x,
+ *   residual, h, y and their gradients 16-byte aligned.
+ */
+dn_status dn_add_norm(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, const void *x, const void *residual,
+                      const float *w, float eps, double p, const uint64_t *seed, void *y, void *h, hipStream_t stream);
+
+/* Bytes of device workspace of dn_add_norm_bwd. */
+size_t dn_add_norm_bwd_workspace(int64_t rows, int32_t D);
+
+/*
+ * Backward of dn_add_norm from its h, dy [rows, D] (dtype) and dh [rows, D]
+ * (res_dtype, the gradient that reaches h itself; NULL: 0): dres, the residual's
+ * gradient (res_dtype; NULL: not written), dx = d dres (dtype; NULL: not written;
+ * with p == 0 and equal types it is dres) and dw [D] fp32.  p and seed as in the forward
+ * pass.  dres may alias dh, and dx dy, where their types agree.  No atomics:
+ * results repeat bit for bit.
+ */
+dn_status dn_add_norm_bwd(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, const void *h, const float *w,
+                          float eps, double p, const uint64_t *seed, const void *dy, const void *dh, void *dx, void *dres,
+                          float *dw, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dn_add_norm for serving, without dropout and with the rows in 8 bits: y8
+ * [rows, D] 8-bit floats (4 exponent and 3 mantissa bits, no infinities, largest
+ * value 448) and scale [rows] fp32, scale = max |y| / 448 (of rows of zeros
+ * 1e-30 / 448), y8 = y / scale rounded to nearest even.  w NULL: y = h, the sum
+ * itself.  A row with a value that is not finite has NaN in its place, or as a
+ * whole where it is normed.  Other arguments and errors as dn_add_norm; y8 16-byte
+ * aligned.
+ */
+dn_status dn_norm8(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, const void *x, const void *residual,
+                   const float *w, float eps, void *y8, float *scale, void *h, hipStream_t stream);
+
+/*
+ * Product of 8-bit rows (dn_norm8's) with 8-bit weights:
+ *
+ *     y[m, n] = act(xs[m] ws[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+ *
+ * x [M,K] and w [N,K] 8-bit floats as dn_norm8 writes them, xs [M], ws [N], bias [N]
+ * fp32 (bias NULL: zero), residual, y [M,N] bf16 (residual NULL: zero; y may alias
+ * it); act 0: none, 1: z sigmoid(z), 2: z Phi(z), Phi the normal distribution's
+ * integral.  The sums are those of the matrix instructions (fp32 accumulators),
+ * all else is fp32 and y is rounded once.  K a multiple of 16, K and N up to 2^31 - 4097
+ * and - 257, fewer than 2^24 pieces of 64 x 64 values of y (DN_EUNSUPPORTED otherwise);
+ * x, w, residual, y 16-byte aligned.
+ */
+dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, const float *xs, const void *w, const float *ws,
+                     const float *bias, const void *residual, int32_t act, void *y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
