@@ -47,11 +47,8 @@ struct Linear8Params {
 // what a lane reads instead of a row's indices behind K
 __device__ const u128 g_zero16 = {{0, 0, 0, 0}};
 
-__device__ __forceinline__ float apply(float z, int act) {
-  if (act == ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
-  if (act == ACT_GELU) return 0.5f * z * (1.f + erff(0.70710678118654752440f * z));
-  return z;
-}
+__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(0.70710678118654752440f * z)); }
 
 // Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD
 // gets a contiguous range of tiles, which run through bands of BAND rows of tiles, so
@@ -134,57 +131,60 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
     }
   }
 
-  // Epilogue: 32 rows m at a time through the wave's own part of LDS, from where
-  // whole rows are stored.
+  // Epilogue: 32 rows m at a time through the wave's own part of LDS, so that a
+  // lane finishes and stores 8 neighbouring columns, and keeps their scales.
   mfma_settle();
   __syncthreads();
   float *part = reinterpret_cast<float *>(lds) + wave * 32 * PITCH;
-  const int nw = n0 + wn;
+  constexpr int LPR = WN / 8;
+  const int nw = n0 + wn, n8 = nw + (lane % LPR) * 8;
+  float ws[8], bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int n = min(n8 + e, p.N - 1);
+    ws[e] = p.ws[n];
+    bias[e] = p.bias ? p.bias[n] : 0.f;
+  }
+  const bool whole = (p.N & 7) == 0;  // rows of y start at 16-byte units
 #pragma unroll
   for (int b = 0; b < NM; ++b) {
     const int mb = m0 + wm + 32 * b;
-    const float xs = p.xs[min(mb + row, p.M - 1)];
 #pragma unroll
     for (int a = 0; a < NN; ++a)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = 32 * a + 8 * i + 4 * half;
-        f32x4 z;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = min(nw + n + e, p.N - 1);
-          z[e] = apply(acc[a][b][4 * i + e] * xs * p.ws[c] + (p.bias ? p.bias[c] : 0.f), p.act);
-        }
-        *reinterpret_cast<f32x4 *>(part + row * PITCH + n) = z;
-      }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4 *>(part + row * PITCH + 32 * a + 8 * i + 4 * half) =
+            (f32x4){acc[a][b][4 * i], acc[a][b][4 * i + 1], acc[a][b][4 * i + 2], acc[a][b][4 * i + 3]};
     wave_lds_fence();
-    if ((p.N & 7) == 0) {
-      constexpr int LPR = WN / 8;
-      const int n = (lane % LPR) * 8;
+#pragma unroll 1
+    for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+      if (mb + r >= p.M || n8 >= p.N) continue;
+      const float xs = p.xs[mb + r];
+      const f32x4 lo = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n8 - nw);
+      const f32x4 hi = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n8 - nw + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-      for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-        if (mb + r < p.M && nw + n < p.N) {
-          const f32x4 lo = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n);
-          const f32x4 hi = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n + 4);
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          const size_t at = (size_t)(mb + r) * p.N + nw + n;
-          if (p.residual) {
-            const bf16x8 res = *reinterpret_cast<const bf16x8 *>(p.residual + at);
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * xs * ws[e] + bias[e];
+      if (p.act == ACT_SILU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += to_f<bf16>(res[e]);
-          }
-          *reinterpret_cast<u32x4 *>(p.y + at) =
-              (u32x4){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
-        }
+        for (int e = 0; e < 8; ++e) v[e] = silu(v[e]);
+      } else if (p.act == ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = gelu(v[e]);
       }
-    } else {
-      for (int o = lane; o < 32 * WN; o += 64) {
-        const int r = o / WN, n = o % WN;
-        if (mb + r < p.M && nw + n < p.N) {
-          const size_t at = (size_t)(mb + r) * p.N + nw + n;
-          const float v = part[r * PITCH + n];
-          p.y[at] = to_e<bf16>(p.residual ? v + to_f<bf16>(p.residual[at]) : v);
+      const size_t at = (size_t)(mb + r) * p.N + n8;
+      if (whole) {
+        if (p.residual) {
+          const bf16x8 res = *reinterpret_cast<const bf16x8 *>(p.residual + at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += to_f<bf16>(res[e]);
         }
+        *reinterpret_cast<u32x4 *>(p.y + at) =
+            (u32x4){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n8 + e < p.N) p.y[at + e] = to_e<bf16>(p.residual ? v[e] + to_f<bf16>(p.residual[at + e]) : v[e]);
       }
     }
     wave_lds_fence();
@@ -236,7 +236,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear8_few_kernel(Linear8Para
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < FEW_WAVES; ++k) s += part[k][m][n];
-    s = apply(s * p.xs[m] * p.ws[n0 + n] + (p.bias ? p.bias[n0 + n] : 0.f), p.act);
+    s = s * p.xs[m] * p.ws[n0 + n] + (p.bias ? p.bias[n0 + n] : 0.f);
+    if (p.act == ACT_SILU) s = silu(s);
+    else if (p.act == ACT_GELU) s = gelu(s);
     const size_t at = (size_t)m * p.N + n0 + n;
     if (p.residual) s += to_f<bf16>(p.residual[at]);
     p.y[at] = to_e<bf16>(s);
