@@ -82,21 +82,21 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   const int m0 = tm * TM, n0 = tn * TN;
 
   // A wave's share of a tile's rows, eight at a time: rows of w first, then of x.
-  constexpr int PIECES = (TM + TN) / 8 / WAVES;
-  static_assert(PIECES * 8 * WAVES == TM + TN && TN % 8 == 0, "the waves share the rows evenly");
-  const uint8_t *src[PIECES];
+  constexpr int PIECES = (TM + TN) / 8 / WAVES, OF_W = TN / 8 / WAVES;
+  static_assert(PIECES * 8 * WAVES == TM + TN && OF_W * 8 * WAVES == TN, "the waves share the rows evenly");
+  uint32_t src[PIECES];  // byte offsets from the tile's first row of w or x: K is below 2^23
   const int unit = (lane & 7) ^ (lane >> 3);  // the unit that lands at lane % 8 of its row
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) {
     const int r = (j * WAVES + wave) * 8 + (lane >> 3);
-    src[j] = r < TN ? p.w + (size_t)min(n0 + r, p.N - 1) * p.K : p.x + (size_t)min(m0 + r - TN, p.M - 1) * p.K;
-    src[j] += unit * 16;
+    src[j] = (uint32_t)(j < OF_W ? min(r, p.N - 1 - n0) : min(r - TN, p.M - 1 - m0)) * (uint32_t)p.K + unit * 16;
   }
-  const auto load = [&](int k, int stage) {
-    const bool some = k + BK <= p.K || k + unit * 16 < p.K;
-#pragma unroll
-    for (int j = 0; j < PIECES; ++j)
-      wy::dma16(some ? (const void *)(src[j] + k) : (const void *)&g_zero16, base + stage * STAGE + (j * WAVES + wave) * 1024);
+  const uint8_t *w0 = p.w + (size_t)n0 * p.K, *x0 = p.x + (size_t)m0 * p.K;
+  const auto load = [&](int j, int k, int stage, bool tail) {
+    const uint8_t *from = (j < OF_W ? w0 : x0) + k;
+    const uint32_t to = base + stage * STAGE + (j * WAVES + wave) * 1024;
+    if (!tail) wy::dma16s(from, src[j], to);
+    else wy::dma16(k + unit * 16 < p.K ? (const void *)(from + src[j]) : (const void *)&g_zero16, to);
   };
 
   const int wm = (wave % (TM / WM)) * WM, wn = (wave / (TM / WM)) * WN;
@@ -109,27 +109,70 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
 
-  load(0, 0);
-  int stage = 0;
-  for (int k = 0; k < p.K; k += BK, stage ^= 1) {
-    wy::wait_vm<0>();
-    __syncthreads();
-    if (k + BK < p.K) load(k + BK, stage ^ 1);
-    const uint32_t tw = base + stage * STAGE + wn * BK, tx = base + stage * STAGE + (TN + wm) * BK;
+  // The loop over K, a block of 128 indices a turn.  One wave has a SIMD to itself
+  // in the large tiles, so that whatever it waits for stops the matrix unit: the
+  // operands of the block's second half are read, and the next block's loads
+  // started, between the products of its first half, and the next block's first
+  // operands between the last quarter of the products of the second.  The barrier
+  // stands before that quarter: by then the next block has had most of a turn to
+  // arrive, and nobody reads the block before any more, whose place the
+  // loads of the following turn take.
+  constexpr int PRODUCTS = NN * NM, OPERANDS = NN + NM, JOIN = PRODUCTS * 3 / 4;
+  i32x8 f[2][OPERANDS];
+  const auto read = [&](int set, int o, int stage) {
+    const uint32_t at = base + stage * STAGE + (o < NN ? wn + 32 * o : TN + wm + 32 * (o - NN)) * BK;
+    f[set][o] = operand(at, row, 4 * set + 2 * half);
+  };
+  const auto product = [&](int set, int i) {
+    const int a = i / NM, b = i % NM;
+    acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f[set][a], f[set][NN + b], acc[a][b], 0, 0, 0, 0, 0, 0);
+  };
+  enum Next { FULL, TAIL, NONE };
+  const auto turn = [&](auto next_c, int k, int stage) {
+    constexpr int next = decltype(next_c)::value;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      i32x8 fw[NN], fx[NM];
+    for (int i = 0; i < PRODUCTS; ++i) {
 #pragma unroll
-      for (int a = 0; a < NN; ++a) fw[a] = operand(tw, 32 * a + row, 4 * ks + 2 * half);
+      for (int o = i * OPERANDS / PRODUCTS; o < (i + 1) * OPERANDS / PRODUCTS; ++o) read(1, o, stage);
+      if (next != NONE) {
 #pragma unroll
-      for (int b = 0; b < NM; ++b) fx[b] = operand(tx, 32 * b + row, 4 * ks + 2 * half);
-#pragma unroll
-      for (int a = 0; a < NN; ++a)
-#pragma unroll
-        for (int b = 0; b < NM; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[a], fx[b], acc[a][b], 0, 0, 0, 0, 0, 0);
+        for (int j = i * PIECES / PRODUCTS; j < (i + 1) * PIECES / PRODUCTS; ++j) load(j, k + BK, stage ^ 1, next == TAIL);
+      }
+      product(0, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int i = 0; i < PRODUCTS; ++i) {
+      if (next != NONE) {
+        if (i == JOIN) {
+          wy::wait_vm<0>();
+          __syncthreads();
+        }
+        if (i >= JOIN) {
+#pragma unroll
+          for (int o = (i - JOIN) * OPERANDS / (PRODUCTS - JOIN); o < (i - JOIN + 1) * OPERANDS / (PRODUCTS - JOIN); ++o)
+            read(0, o, stage ^ 1);
+        }
+      }
+      product(1, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  const int blocks = (p.K + BK - 1) / BK;
+  const bool ragged = p.K % BK != 0;
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) load(j, 0, 0, p.K < BK);
+  wy::wait_vm<0>();
+  __syncthreads();
+#pragma unroll
+  for (int o = 0; o < OPERANDS; ++o) read(0, o, 0);
+  int at = 0;
+  for (; at < blocks - 1 - ragged; ++at) turn(std::integral_constant<int, FULL>(), at * BK, at & 1);
+  if (at < blocks - 1) {
+    turn(std::integral_constant<int, TAIL>(), at * BK, at & 1);
+    ++at;
   }
+  turn(std::integral_constant<int, NONE>(), at * BK, at & 1);
 
   // Epilogue: 32 rows m at a time through the wave's own part of LDS, so that a
   // lane finishes and stores 8 neighbouring columns, and keeps their scales.
@@ -283,8 +326,8 @@ extern "C" dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, 
                                 const float *ws, const float *bias, const void *residual, int32_t act, void *y,
                                 hipStream_t stream) {
   if (M < 0 || N <= 0 || K <= 0 || act < ACT_NONE || act > ACT_GELU) return DN_EINVAL;
-  // the rows' 16-byte units, the tiles' count, and the byte offsets within a row
-  if (K % 16 != 0 || K > INT32_MAX - BK * FEW_WAVES * FEW_BATCH) return DN_EUNSUPPORTED;
+  // the rows' 16-byte units, a tile's 32-bit byte offsets, and the tiles' count
+  if (K % 16 != 0 || K > 1 << 23) return DN_EUNSUPPORTED;
   if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) > UINT32_MAX / 256 || N > INT32_MAX - 256 || M > INT32_MAX - 256)
     return DN_EUNSUPPORTED;
   if (M == 0) return DN_OK;

@@ -672,9 +672,9 @@ dn_status dn_norm8(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, co
  * fp32 (bias NULL: zero), residual, y [M,N] bf16 (residual NULL: zero; y may alias
  * it); act 0: none, 1: z sigmoid(z), 2: z Phi(z), Phi the normal distribution's
  * integral.  The sums are those of the matrix instructions (fp32 accumulators),
- * all else is fp32 and y is rounded once.  K a multiple of 16, K and N up to 2^31 - 4097
- * and - 257, fewer than 2^24 pieces of 64 x 64 values of y (DN_EUNSUPPORTED otherwise);
- * x, w, residual, y 16-byte aligned.
+ * all else is fp32 and y is rounded once.  K a multiple of 16 up to 2^23, fewer
+ * than 2^24 pieces of 64 x 64 values of y (DN_EUNSUPPORTED otherwise); x, w, residual,
+ * y 16-byte aligned.
  */
 dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, const float *xs, const void *w, const float *ws,
                      const float *bias, const void *residual, int32_t act, void *y, hipStream_t stream);

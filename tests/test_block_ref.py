@@ -179,7 +179,7 @@ def test_norm8_refuses(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(act=3), EINVAL), (dict(act=-1), EINVAL), (dict(K=24), EUNSUPPORTED),
-    (dict(K=TOP - 15), EUNSUPPORTED), (dict(M=TOP), EUNSUPPORTED), (dict(N=TOP), EUNSUPPORTED), (dict(M=1 << 20, N=1 << 20), EUNSUPPORTED),
+    (dict(K=TOP - 15), EUNSUPPORTED), (dict(K=(1 << 23) + 16), EUNSUPPORTED), (dict(M=TOP), EUNSUPPORTED), (dict(N=TOP), EUNSUPPORTED), (dict(M=1 << 20, N=1 << 20), EUNSUPPORTED),
     (dict(x=None), EINVAL), (dict(xs=None), EINVAL), (dict(w=None), EINVAL), (dict(ws=None), EINVAL), (dict(y=None), EINVAL),
     (dict(x=F + 8), EINVAL), (dict(w=F + 8), EINVAL), (dict(residual=F + 2), EINVAL), (dict(y=F + 2), EINVAL), (dict(M=0, x=None), OK)])
 def test_linear8_refuses(lib, kw, code):
