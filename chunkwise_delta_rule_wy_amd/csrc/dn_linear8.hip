@@ -109,6 +109,20 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
 
+  // What the epilogue needs: a lane's row there is `row` of each 32 until the
+  // transposition, and then 8 columns.
+  constexpr int LPR = WN / 8;
+  const int nw = n0 + wn, n8 = nw + (lane % LPR) * 8;
+  float ws[8], bias[8], xs[NM];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int n = min(n8 + e, p.N - 1);
+    ws[e] = p.ws[n];
+    bias[e] = p.bias ? p.bias[n] : 0.f;
+  }
+#pragma unroll
+  for (int b = 0; b < NM; ++b) xs[b] = p.xs[min(m0 + wm + 32 * b + row, p.M - 1)];
+
   // The loop over K, a block of 128 indices a turn.  One wave has a SIMD to itself
   // in the large tiles, so that whatever it waits for stops the matrix unit: the
   // operands of the block's second half are read, and the next block's loads
@@ -175,19 +189,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   turn(std::integral_constant<int, NONE>(), at * BK, at & 1);
 
   // Epilogue: 32 rows m at a time through the wave's own part of LDS, so that a
-  // lane finishes and stores 8 neighbouring columns, and keeps their scales.
+  // lane finishes and stores 8 neighbouring columns, BATCH rows at once, whose
+  // residuals it loads first.
   mfma_settle();
   __syncthreads();
   float *part = reinterpret_cast<float *>(lds) + wave * 32 * PITCH;
-  constexpr int LPR = WN / 8;
-  const int nw = n0 + wn, n8 = nw + (lane % LPR) * 8;
-  float ws[8], bias[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int n = min(n8 + e, p.N - 1);
-    ws[e] = p.ws[n];
-    bias[e] = p.bias ? p.bias[n] : 0.f;
-  }
+  constexpr int STEP = 64 / LPR, BATCH = 32 / STEP < 4 ? 32 / STEP : 4;
   const bool whole = (p.N & 7) == 0;  // rows of y start at 16-byte units
 #pragma unroll
   for (int b = 0; b < NM; ++b) {
@@ -197,37 +204,55 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<f32x4 *>(part + row * PITCH + 32 * a + 8 * i + 4 * half) =
-            (f32x4){acc[a][b][4 * i], acc[a][b][4 * i + 1], acc[a][b][4 * i + 2], acc[a][b][4 * i + 3]};
+            (f32x4){acc[a][b][4 * i] * xs[b], acc[a][b][4 * i + 1] * xs[b], acc[a][b][4 * i + 2] * xs[b],
+                    acc[a][b][4 * i + 3] * xs[b]};
     wave_lds_fence();
 #pragma unroll 1
-    for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-      if (mb + r >= p.M || n8 >= p.N) continue;
-      const float xs = p.xs[mb + r];
-      const f32x4 lo = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n8 - nw);
-      const f32x4 hi = *reinterpret_cast<const f32x4 *>(part + r * PITCH + n8 - nw + 4);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    for (int r0 = lane / LPR; r0 < 32; r0 += STEP * BATCH) {
+      bf16x8 res[BATCH] = {};
+      float v[BATCH][8];
+      if (whole && p.residual) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * xs * ws[e] + bias[e];
+        for (int k = 0; k < BATCH; ++k)
+          if (mb + r0 + k * STEP < p.M && n8 < p.N)
+            res[k] = *reinterpret_cast<const bf16x8 *>(p.residual + (size_t)(mb + r0 + k * STEP) * p.N + n8);
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const float *at = part + (r0 + k * STEP) * PITCH + n8 - nw;
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(at), hi = *reinterpret_cast<const f32x4 *>(at + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[k][e] = __builtin_fmaf(lo[e], ws[e], bias[e]);
+          v[k][4 + e] = __builtin_fmaf(hi[e], ws[4 + e], bias[4 + e]);
+        }
+      }
       if (p.act == ACT_SILU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = silu(v[e]);
+        for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] = silu(v[k][e]);
       } else if (p.act == ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = gelu(v[e]);
+        for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] = gelu(v[k][e]);
       }
-      const size_t at = (size_t)(mb + r) * p.N + n8;
-      if (whole) {
-        if (p.residual) {
-          const bf16x8 res = *reinterpret_cast<const bf16x8 *>(p.residual + at);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += to_f<bf16>(res[e]);
+      for (int k = 0; k < BATCH; ++k) {
+        const int m = mb + r0 + k * STEP;
+        if (m >= p.M || n8 >= p.N) continue;
+        const size_t at = (size_t)m * p.N + n8;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] += to_f<bf16>(res[k][e]);
+          *reinterpret_cast<u32x4 *>(p.y + at) = (u32x4){pk_bf16(v[k][0], v[k][1]), pk_bf16(v[k][2], v[k][3]),
+                                                         pk_bf16(v[k][4], v[k][5]), pk_bf16(v[k][6], v[k][7])};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n8 + e < p.N) p.y[at + e] = to_e<bf16>(p.residual ? v[k][e] + to_f<bf16>(p.residual[at + e]) : v[k][e]);
         }
-        *reinterpret_cast<u32x4 *>(p.y + at) =
-            (u32x4){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n8 + e < p.N) p.y[at + e] = to_e<bf16>(p.residual ? v[e] + to_f<bf16>(p.residual[at + e]) : v[e]);
       }
     }
     wave_lds_fence();
