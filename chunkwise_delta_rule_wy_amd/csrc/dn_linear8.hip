@@ -12,9 +12,10 @@
 // one row m.
 //
 // Many rows: tiles of x and w pass through LDS, a block of 128 indices at a time,
-// loaded directly (no registers) one block ahead.  A row of a tile is 128 bytes,
-// the span of the LDS banks; its 16-byte units are stored at unit ^ (row & 7), so
-// that eight lanes reading one unit of eight rows meet all banks.
+// loaded directly (no registers) one block ahead.  A row of a tile is 128 bytes, half
+// the span of the 64 banks; its 16-byte units are stored at unit ^ (row / 2 & 7), so
+// that sixteen lanes reading one unit of sixteen rows meet all banks (with unit ^
+// (row & 7), which only tells eight rows apart, every read took twice its time).
 //
 // Few rows: the weights are the traffic, and no tile of them is used twice, so
 // that they go from memory to registers; a workgroup takes 16 columns and its
@@ -64,8 +65,8 @@ __device__ __forceinline__ void tile_of(const Linear8Params &p, int &tm, int &tn
 
 // A 32-byte operand: the units `unit` (even) and unit + 1 of a row of a tile.
 __device__ __forceinline__ i32x8 operand(uint32_t tile, int row, int unit) {
-  const uint32_t at = tile + row * BK;
-  const i32x4 lo = wy::ld<i32x4>(at + ((unit ^ (row & 7)) << 4)), hi = wy::ld<i32x4>(at + (((unit + 1) ^ (row & 7)) << 4));
+  const uint32_t at = tile + row * BK, swz = row >> 1 & 7;
+  const i32x4 lo = wy::ld<i32x4>(at + ((unit ^ swz) << 4)), hi = wy::ld<i32x4>(at + (((unit + 1) ^ swz) << 4));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -85,18 +86,19 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   constexpr int PIECES = (TM + TN) / 8 / WAVES, OF_W = TN / 8 / WAVES;
   static_assert(PIECES * 8 * WAVES == TM + TN && OF_W * 8 * WAVES == TN, "the waves share the rows evenly");
   uint32_t src[PIECES];  // byte offsets from the tile's first row of w or x: K is below 2^23
-  const int unit = (lane & 7) ^ (lane >> 3);  // the unit that lands at lane % 8 of its row
+  // the unit that lands at lane % 8 of its row
+  const auto unit = [&](int j) { return (lane & 7) ^ ((4 * (j * WAVES + wave) + (lane >> 4)) & 7); };
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) {
     const int r = (j * WAVES + wave) * 8 + (lane >> 3);
-    src[j] = (uint32_t)(j < OF_W ? min(r, p.N - 1 - n0) : min(r - TN, p.M - 1 - m0)) * (uint32_t)p.K + unit * 16;
+    src[j] = (uint32_t)(j < OF_W ? min(r, p.N - 1 - n0) : min(r - TN, p.M - 1 - m0)) * (uint32_t)p.K + unit(j) * 16;
   }
   const uint8_t *w0 = p.w + (size_t)n0 * p.K, *x0 = p.x + (size_t)m0 * p.K;
   const auto load = [&](int j, int k, int stage, bool tail) {
     const uint8_t *from = (j < OF_W ? w0 : x0) + k;
     const uint32_t to = base + stage * STAGE + (j * WAVES + wave) * 1024;
     if (!tail) wy::dma16s(from, src[j], to);
-    else wy::dma16(k + unit * 16 < p.K ? (const void *)(from + src[j]) : (const void *)&g_zero16, to);
+    else wy::dma16(k + unit(j) * 16 < p.K ? (const void *)(from + src[j]) : (const void *)&g_zero16, to);
   };
 
   const int wm = (wave % (TM / WM)) * WM, wn = (wave / (TM / WM)) * WN;
