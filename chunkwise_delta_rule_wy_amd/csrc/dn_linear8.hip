@@ -126,13 +126,13 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   for (int b = 0; b < NM; ++b) xs[b] = p.xs[min(m0 + wm + 32 * b + row, p.M - 1)];
 
   // The loop over K, a block of 128 indices a turn.  One wave has a SIMD to itself
-  // in the large tiles, so that whatever it waits for stops the matrix unit: the
-  // operands of the block's second half are read, and the next block's loads
-  // started, between the products of its first half, and the next block's first
-  // operands between the last quarter of the products of the second.  The barrier
-  // stands before that quarter: by then the next block has had most of a turn to
-  // arrive, and nobody reads the block before any more, whose place the
-  // loads of the following turn take.
+  // in the large tiles, so that whatever it waits for stops the matrix unit.  Between
+  // the products of the block's first half it reads the operands of the second,
+  // whereupon the block's place is free (first barrier), and between those of the
+  // second half it starts the loads of the block after the next, evenly spaced, as
+  // bursts are slower.  The next block, whose loads were started a turn ago, is
+  // waited for (second barrier) before the last quarter of the products, between
+  // which its first operands are read.
   constexpr int PRODUCTS = NN * NM, OPERANDS = NN + NM, JOIN = PRODUCTS * 3 / 4;
   i32x8 f[2][OPERANDS];
   const auto read = [&](int set, int o, int stage) {
@@ -143,52 +143,62 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
     const int a = i / NM, b = i % NM;
     acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f[set][a], f[set][NN + b], acc[a][b], 0, 0, 0, 0, 0, 0);
   };
-  enum Next { FULL, TAIL, NONE };
-  const auto turn = [&](auto next_c, int k, int stage) {
-    constexpr int next = decltype(next_c)::value;
+  // what a turn loads: the block after the next, that as the ragged last one, or
+  // nothing, with or without a next block
+  enum Mode { FULL, TAIL, NEXT, LAST };
+  const auto turn = [&](auto mode_c, int k, int stage) {
+    constexpr int mode = decltype(mode_c)::value;
 #pragma unroll
     for (int i = 0; i < PRODUCTS; ++i) {
 #pragma unroll
       for (int o = i * OPERANDS / PRODUCTS; o < (i + 1) * OPERANDS / PRODUCTS; ++o) read(1, o, stage);
-      if (next != NONE) {
-#pragma unroll
-        for (int j = i * PIECES / PRODUCTS; j < (i + 1) * PIECES / PRODUCTS; ++j) load(j, k + BK, stage ^ 1, next == TAIL);
-      }
       product(0, i);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < PRODUCTS; ++i) {
-      if (next != NONE) {
-        if (i == JOIN) {
-          wy::wait_vm<0>();
-          __syncthreads();
-        }
-        if (i >= JOIN) {
+      if (mode <= TAIL && i == 0 && JOIN > 0) __syncthreads();
+      if (mode != LAST && i == JOIN) {
+        wy::wait_vm<mode == NEXT ? 0 : PIECES * JOIN / PRODUCTS>();
+        __syncthreads();
+      }
+      if (mode != LAST && i >= JOIN) {
 #pragma unroll
-          for (int o = (i - JOIN) * OPERANDS / (PRODUCTS - JOIN); o < (i - JOIN + 1) * OPERANDS / (PRODUCTS - JOIN); ++o)
-            read(0, o, stage ^ 1);
-        }
+        for (int o = (i - JOIN) * OPERANDS / (PRODUCTS - JOIN); o < (i - JOIN + 1) * OPERANDS / (PRODUCTS - JOIN); ++o)
+          read(0, o, stage ^ 1);
+      }
+      if (mode <= TAIL) {
+#pragma unroll
+        for (int j = i * PIECES / PRODUCTS; j < (i + 1) * PIECES / PRODUCTS; ++j) load(j, k + 2 * BK, stage, mode == TAIL);
       }
       product(1, i);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const int blocks = (p.K + BK - 1) / BK;
-  const bool ragged = p.K % BK != 0;
+  const int blocks = (p.K + BK - 1) / BK, ragged = p.K % BK != 0;
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) load(j, 0, 0, p.K < BK);
-  wy::wait_vm<0>();
+  if (blocks > 1) {
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) load(j, BK, 1, p.K < 2 * BK);
+    wy::wait_vm<PIECES>();
+  } else {
+    wy::wait_vm<0>();
+  }
   __syncthreads();
 #pragma unroll
   for (int o = 0; o < OPERANDS; ++o) read(0, o, 0);
   int at = 0;
-  for (; at < blocks - 1 - ragged; ++at) turn(std::integral_constant<int, FULL>(), at * BK, at & 1);
-  if (at < blocks - 1) {
+  for (; at + 2 < blocks - ragged; ++at) turn(std::integral_constant<int, FULL>(), at * BK, at & 1);
+  if (at + 2 < blocks) {
     turn(std::integral_constant<int, TAIL>(), at * BK, at & 1);
     ++at;
   }
-  turn(std::integral_constant<int, NONE>(), at * BK, at & 1);
+  if (at + 1 < blocks) {
+    turn(std::integral_constant<int, NEXT>(), at * BK, at & 1);
+    ++at;
+  }
+  turn(std::integral_constant<int, LAST>(), at * BK, at & 1);
 
   // Epilogue: 32 rows m at a time through the wave's own part of LDS, so that a
   // lane finishes and stores 8 neighbouring columns, BATCH rows at once, whose
