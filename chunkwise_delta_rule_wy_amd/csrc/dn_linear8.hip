@@ -51,9 +51,10 @@ __device__ const u128 g_zero16 = {{0, 0, 0, 0}};
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 __device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(0.70710678118654752440f * z)); }
 
-// Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD
-// gets a contiguous range of tiles, which run through bands of BAND rows of tiles, so
-// that the tiles which are side by side in time share rows of x and of w in one L2.
+// Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD gets a
+// contiguous range of tiles, which run through bands of BAND rows of tiles, so that
+// the tiles which are side by side in time share rows of x and of w in one L2
+// (16384 x 8192 x 4096: 458 us; bands of 2 and 8: 474 and 509 us).
 constexpr int BAND = 4;
 __device__ __forceinline__ void tile_of(const Linear8Params &p, int &tm, int &tn) {
   const int total = p.tm * p.tn, q = total >> 3, r = total & 7, xcd = blockIdx.x & 7;
@@ -70,14 +71,16 @@ __device__ __forceinline__ i32x8 operand(uint32_t tile, int row, int unit) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int TM, int TN, int WM, int WN>
+template <int TM, int TN, int WM, int WN, int ACT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kernel(Linear8Params p) {
   constexpr int WAVES = (TM / WM) * (TN / WN), STAGE = (TM + TN) * BK, NM = WM / 32, NN = WN / 32;
-  constexpr int PITCH = WN + 4;  // epilogue: fp32 rows, 16 bytes off the banks' span
-  constexpr int LDS = 2 * STAGE > WAVES * 32 * PITCH * 4 ? 2 * STAGE : WAVES * 32 * PITCH * 4;
-  __shared__ __attribute__((aligned(128))) char lds[LDS];
+  __shared__ __attribute__((aligned(256))) char lds[2 * STAGE];
+  __shared__ f32x2 cols[TN];  // (ws, bias) of a tile's columns
   const uint32_t base = (uint32_t)(size_t)(__attribute__((address_space(3))) char *)lds;
   const int lane = lane_id(), wave = wave_id();
+  const int wm = (wave % (TM / WM)) * WM, wn = (wave / (TM / WM)) * WN;
+  const int row = lane & 31, half = lane >> 5;
+  const int blocks = (p.K + BK - 1) / BK, ragged = p.K % BK != 0;
   int tm, tn;
   tile_of(p, tm, tn);
   const int m0 = tm * TM, n0 = tn * TN;
@@ -85,7 +88,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   // A wave's share of a tile's rows, eight at a time: rows of w first, then of x.
   constexpr int PIECES = (TM + TN) / 8 / WAVES, OF_W = TN / 8 / WAVES;
   static_assert(PIECES * 8 * WAVES == TM + TN && OF_W * 8 * WAVES == TN, "the waves share the rows evenly");
-  uint32_t src[PIECES];  // byte offsets from the tile's first row of w or x: K is below 2^23
+  uint32_t src[PIECES];  // byte offsets from the tile's first row of w or x: K is at most 2^23
   // the unit that lands at lane % 8 of its row
   const auto unit = [&](int j) { return (lane & 7) ^ ((4 * (j * WAVES + wave) + (lane >> 4)) & 7); };
 #pragma unroll
@@ -101,30 +104,6 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
     else wy::dma16(k + unit(j) * 16 < p.K ? (const void *)(from + src[j]) : (const void *)&g_zero16, to);
   };
 
-  const int wm = (wave % (TM / WM)) * WM, wn = (wave / (TM / WM)) * WN;
-  const int row = lane & 31, half = lane >> 5;
-  f32x16 acc[NN][NM];
-#pragma unroll
-  for (int a = 0; a < NN; ++a)
-#pragma unroll
-    for (int b = 0; b < NM; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
-
-  // What the epilogue needs: a lane's row there is `row` of each 32 until the
-  // transposition, and then 8 columns.
-  constexpr int LPR = WN / 8;
-  const int nw = n0 + wn, n8 = nw + (lane % LPR) * 8;
-  float ws[8], bias[8], xs[NM];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int n = min(n8 + e, p.N - 1);
-    ws[e] = p.ws[n];
-    bias[e] = p.bias ? p.bias[n] : 0.f;
-  }
-#pragma unroll
-  for (int b = 0; b < NM; ++b) xs[b] = p.xs[min(m0 + wm + 32 * b + row, p.M - 1)];
-
   // The loop over K, a block of 128 indices a turn.  One wave has a SIMD to itself
   // in the large tiles, so that whatever it waits for stops the matrix unit.  Between
   // the products of the block's first half it reads the operands of the second,
@@ -134,6 +113,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   // waited for (second barrier) before the last quarter of the products, between
   // which its first operands are read.
   constexpr int PRODUCTS = NN * NM, OPERANDS = NN + NM, JOIN = PRODUCTS * 3 / 4;
+  f32x16 acc[NN][NM];
   i32x8 f[2][OPERANDS];
   const auto read = [&](int set, int o, int stage) {
     const uint32_t at = base + stage * STAGE + (o < NN ? wn + 32 * o : TN + wm + 32 * (o - NN)) * BK;
@@ -144,7 +124,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
     acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f[set][a], f[set][NN + b], acc[a][b], 0, 0, 0, 0, 0, 0);
   };
   // what a turn loads: the block after the next, that as the ragged last one, or
-  // nothing, with or without a next block
+  // nothing; the last turn has no next block
   enum Mode { FULL, TAIL, NEXT, LAST };
   const auto turn = [&](auto mode_c, int k, int stage) {
     constexpr int mode = decltype(mode_c)::value;
@@ -169,23 +149,35 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
       }
       if (mode <= TAIL) {
 #pragma unroll
-        for (int j = i * PIECES / PRODUCTS; j < (i + 1) * PIECES / PRODUCTS; ++j) load(j, k + 2 * BK, stage, mode == TAIL);
+        for (int j = i * PIECES / PRODUCTS; j < (i + 1) * PIECES / PRODUCTS; ++j)
+          load(j, k + 2 * BK, stage, mode == TAIL);
       }
       product(1, i);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const int blocks = (p.K + BK - 1) / BK, ragged = p.K % BK != 0;
+
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) load(j, 0, 0, p.K < BK);
+  for (int n = threadIdx.x; n < TN; n += 64 * WAVES) {
+    const int c = min(n0 + n, p.N - 1);
+    cols[n] = (f32x2){p.ws[c], p.bias ? p.bias[c] : 0.f};
+  }
+  float xs[NM];
+#pragma unroll
+  for (int b = 0; b < NM; ++b) xs[b] = p.xs[min(m0 + wm + 32 * b + row, p.M - 1)];
+#pragma unroll
+  for (int a = 0; a < NN; ++a)
+#pragma unroll
+    for (int b = 0; b < NM; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+  wy::wait_vm<0>();
+  __syncthreads();
   if (blocks > 1) {
 #pragma unroll
     for (int j = 0; j < PIECES; ++j) load(j, BK, 1, p.K < 2 * BK);
-    wy::wait_vm<PIECES>();
-  } else {
-    wy::wait_vm<0>();
   }
-  __syncthreads();
 #pragma unroll
   for (int o = 0; o < OPERANDS; ++o) read(0, o, 0);
   int at = 0;
@@ -200,71 +192,88 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   }
   turn(std::integral_constant<int, LAST>(), at * BK, at & 1);
 
-  // Epilogue: 32 rows m at a time through the wave's own part of LDS, so that a
-  // lane finishes and stores 8 neighbouring columns, BATCH rows at once, whose
-  // residuals it loads first.
+  // Epilogue, in the place of the last block: ROUND times 32 rows m are finished
+  // in the registers, where a lane has four neighbouring columns of one row, and
+  // pass through the wave's own part of LDS as bf16, so that whole rows are
+  // stored.  A residual comes into that place first, by direct loads.  16-byte
+  // units of a row are stored at unit ^ swizzle(row).
+  constexpr int PITCH = 2 * WN, UNITS = PITCH / 16, PART = STAGE / WAVES;
+  constexpr int ROUND = PART / (32 * PITCH) < NM ? PART / (32 * PITCH) : NM;
+  static_assert(ROUND > 0 && NM % ROUND == 0, "a wave's part holds 32 rows at least");
+  const uint32_t part = base + (at & 1) * STAGE + wave * PART;
+  const auto swizzle = [](int r) { return r / (256 / PITCH) % UNITS; };
+  const int nw = n0 + wn;
+  const bool whole = (p.N & 7) == 0;  // rows of y start at 16-byte units
   mfma_settle();
   __syncthreads();
-  float *part = reinterpret_cast<float *>(lds) + wave * 32 * PITCH;
-  constexpr int STEP = 64 / LPR, BATCH = 32 / STEP < 4 ? 32 / STEP : 4;
-  const bool whole = (p.N & 7) == 0;  // rows of y start at 16-byte units
 #pragma unroll
-  for (int b = 0; b < NM; ++b) {
-    const int mb = m0 + wm + 32 * b;
+  for (int b0 = 0; b0 < NM; b0 += ROUND) {
+    const int mb = m0 + wm + 32 * b0;
+    constexpr int STEP = 64 / UNITS;  // rows a pass
+    const int u = lane % UNITS;
+    if (p.residual && whole) {
+#pragma unroll
+      for (int r0 = 0; r0 < 32 * ROUND; r0 += STEP) {
+        const int r = r0 + lane / UNITS, n = nw + 8 * (u ^ swizzle(r));
+        wy::dma16(n < p.N ? (const void *)(p.residual + (size_t)min(mb + r, p.M - 1) * p.N + n) : (const void *)&g_zero16,
+                  part + r0 * PITCH);
+      }
+      wy::wait_vm<0>();
+      asm volatile("" ::: "memory");  // no read of that place before the wait
+    }
 #pragma unroll
     for (int a = 0; a < NN; ++a)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4 *>(part + row * PITCH + 32 * a + 8 * i + 4 * half) =
-            (f32x4){acc[a][b][4 * i] * xs[b], acc[a][b][4 * i + 1] * xs[b], acc[a][b][4 * i + 2] * xs[b],
-                    acc[a][b][4 * i + 3] * xs[b]};
+      for (int i = 0; i < 4; ++i) {
+        const int n = 32 * a + 8 * i + 4 * half;
+        const f32x4 c01 = *reinterpret_cast<const f32x4 *>(&cols[wn + n]);
+        const f32x4 c23 = *reinterpret_cast<const f32x4 *>(&cols[wn + n + 2]);
+#pragma unroll
+        for (int b = b0; b < b0 + ROUND; ++b) {
+          const int r = 32 * (b - b0) + row;
+          const uint32_t to = part + r * PITCH + (((n >> 3) ^ swizzle(r)) << 4) + 8 * half;
+          float v[4];
+          v[0] = __builtin_fmaf(acc[a][b][4 * i] * xs[b], c01[0], c01[1]);
+          v[1] = __builtin_fmaf(acc[a][b][4 * i + 1] * xs[b], c01[2], c01[3]);
+          v[2] = __builtin_fmaf(acc[a][b][4 * i + 2] * xs[b], c23[0], c23[1]);
+          v[3] = __builtin_fmaf(acc[a][b][4 * i + 3] * xs[b], c23[2], c23[3]);
+          if (ACT == ACT_SILU) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = silu(v[e]);
+          } else if (ACT == ACT_GELU) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = gelu(v[e]);
+          }
+          if (p.residual) {
+            bf16x4 res;
+            if (whole) {
+              res = wy::ld<bf16x4>(to);
+            } else {
+              const bf16 *from = p.residual + (size_t)min(m0 + wm + 32 * b + row, p.M - 1) * p.N;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) res[e] = from[min(nw + n + e, p.N - 1)];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += to_f<bf16>(res[e]);
+          }
+          wy::st<u32x2>(to, (u32x2){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     wave_lds_fence();
-#pragma unroll 1
-    for (int r0 = lane / LPR; r0 < 32; r0 += STEP * BATCH) {
-      bf16x8 res[BATCH] = {};
-      float v[BATCH][8];
-      if (whole && p.residual) {
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32 * ROUND; r0 += STEP) {
+      const int r = r0 + lane / UNITS, m = mb + r, n = nw + 8 * u;
+      const u32x4 v = wy::ld<u32x4>(part + r * PITCH + ((u ^ swizzle(r)) << 4));
+      if (m >= p.M || n >= p.N) continue;
+      bf16 *out = p.y + (size_t)m * p.N + n;
+      if (whole) {
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out));
+      } else {
+        const bf16x8 h = __builtin_bit_cast(bf16x8, v);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-          if (mb + r0 + k * STEP < p.M && n8 < p.N)
-            res[k] = *reinterpret_cast<const bf16x8 *>(p.residual + (size_t)(mb + r0 + k * STEP) * p.N + n8);
-      }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const float *at = part + (r0 + k * STEP) * PITCH + n8 - nw;
-        const f32x4 lo = *reinterpret_cast<const f32x4 *>(at), hi = *reinterpret_cast<const f32x4 *>(at + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[k][e] = __builtin_fmaf(lo[e], ws[e], bias[e]);
-          v[k][4 + e] = __builtin_fmaf(hi[e], ws[4 + e], bias[4 + e]);
-        }
-      }
-      if (p.act == ACT_SILU) {
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][e] = silu(v[k][e]);
-      } else if (p.act == ACT_GELU) {
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][e] = gelu(v[k][e]);
-      }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int m = mb + r0 + k * STEP;
-        if (m >= p.M || n8 >= p.N) continue;
-        const size_t at = (size_t)m * p.N + n8;
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][e] += to_f<bf16>(res[k][e]);
-          *reinterpret_cast<u32x4 *>(p.y + at) = (u32x4){pk_bf16(v[k][0], v[k][1]), pk_bf16(v[k][2], v[k][3]),
-                                                         pk_bf16(v[k][4], v[k][5]), pk_bf16(v[k][6], v[k][7])};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n8 + e < p.N) p.y[at + e] = to_e<bf16>(p.residual ? v[k][e] + to_f<bf16>(p.residual[at + e]) : v[k][e]);
-        }
+        for (int e = 0; e < 8; ++e)
+          if (n + e < p.N) out[e] = h[e];
       }
     }
     wave_lds_fence();
@@ -331,8 +340,11 @@ template <int TM, int TN, int WM, int WN>
 hipError_t launch_tile(Linear8Params &p, hipStream_t st) {
   p.tm = (p.M + TM - 1) / TM;
   p.tn = (p.N + TN - 1) / TN;
-  hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN>), dim3((unsigned)(p.tm * p.tn)), dim3(64 * (TM / WM) * (TN / WN)),
-                     0, st, p);
+  const int64_t tiles = (int64_t)p.tm * p.tn;
+  const dim3 grid((unsigned)tiles), thr(64 * (TM / WM) * (TN / WN));
+  if (p.act == ACT_SILU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_SILU>), grid, thr, 0, st, p);
+  else if (p.act == ACT_GELU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_GELU>), grid, thr, 0, st, p);
+  else hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_NONE>), grid, thr, 0, st, p);
   return hipGetLastError();
 }
 
