@@ -109,22 +109,22 @@ __device__ __forceinline__ float glr_sigmoid(float z, float bias) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(__builtin_fmaf(z, -GLR_LOG2E, bias)));
 }
 
-// 1 - a^2 for a = 2^l2, l2 <= 0: with v = -2 log a, 1 - e^-v by its series below
-// 0.4, where the difference would lose digits (the rest is below 2^-24 of it).
+// 1 - a^2 for a = 2^l2, l2 <= 0: with v = -log a below 1/2, where the difference
+// would lose digits, 2 a sinh v by its series (the rest is below 2^-26 of it).
 __device__ __forceinline__ float glr_rest(float a, float l2) {
-  const float v = (-2.f * GLR_LN2) * l2;
-  float q = 1.f / 5040;
-  q = __builtin_fmaf(q, -v, 1.f / 720);
-  q = __builtin_fmaf(q, -v, 1.f / 120);
-  q = __builtin_fmaf(q, -v, 1.f / 24);
-  q = __builtin_fmaf(q, -v, 1.f / 6);
-  q = __builtin_fmaf(q, -v, 0.5f);
-  return v < 0.4f ? v * __builtin_fmaf(q, -v, 1.f) : __builtin_fmaf(-a, a, 1.f);
+  const float v = -GLR_LN2 * l2, w = v * v;
+  float q = __builtin_fmaf(w, 1.f / 5040, 1.f / 120);
+  q = __builtin_fmaf(w, q, 1.f / 6);
+  q = __builtin_fmaf(w, q, 1.f);
+  return v < 0.5f ? (v + v) * a * q : __builtin_fmaf(-a, a, 1.f);
 }
 
-// A c + B, where A = 0 drops c, whatever it is.
+// A c + B, where A = 0 drops c, whatever it is; DROP false where segments lie in
+// one sequence, and there is nothing to drop.
+template <bool DROP = true>
 __device__ __forceinline__ f32x2 glr_map(f32x2 A, f32x2 c, f32x2 B) {
-  return (f32x2){A[0] == 0.f ? B[0] : __builtin_fmaf(A[0], c[0], B[0]), A[1] == 0.f ? B[1] : __builtin_fmaf(A[1], c[1], B[1])};
+  const f32x2 r = {__builtin_fmaf(A[0], c[0], B[0]), __builtin_fmaf(A[1], c[1], B[1])};
+  return DROP ? (f32x2){A[0] == 0.f ? B[0] : r[0], A[1] == 0.f ? B[1] : r[1]} : r;
 }
 __device__ __forceinline__ f32x2 glr_fma(f32x2 a, f32x2 b, f32x2 c) {
   return (f32x2){__builtin_fmaf(a[0], b[0], c[0]), __builtin_fmaf(a[1], b[1], c[1])};
@@ -229,17 +229,23 @@ __device__ __forceinline__ bool glr_flags(const GlrParams &p, GlrSeq &q, int64_t
   return true;
 }
 
-// The ROWS rows of a run, two channels a lane; rows behind the segment's end
-// repeat its last one.
+// The ROWS rows of a run, two channels a lane.  `tile` (uniform) is the tile's first
+// row, `at` the run's first row in it, `left` the rows of the tile; rows behind them
+// repeat the last one.  A whole tile's addresses are uniform but for one offset.
 template <typename E, int ROWS>
-__device__ __forceinline__ void glr_load(const void *src, int64_t row, int64_t row1, int C, int c,
+__device__ __forceinline__ void glr_load(const void *src, int64_t tile, int at, int left, bool whole, int C, int c,
                                          typename Pair<E>::type (&v)[ROWS]) {
-  const int64_t left = row1 - 1 - row;
-  const int most = left < ROWS - 1 ? (int)left : ROWS - 1;
-  const E *at = static_cast<const E *>(src) + row * C + c;
+  const char *base = static_cast<const char *>(src) + tile * C * (int)sizeof(E);
+  const uint32_t pitch = C * (uint32_t)sizeof(E), col = c * (uint32_t)sizeof(E);
+  if (whole) {
+    const uint32_t off = at * pitch + col;
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j)
-    v[j] = *reinterpret_cast<const typename Pair<E>::type *>(at + (int64_t)min(j, most) * C);
+    for (int j = 0; j < ROWS; ++j) v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + j * (size_t)pitch + off);
+  } else {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+      v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + (min(at + j, left - 1) * pitch + col));
+  }
 }
 
 __device__ __forceinline__ f32x2 other_half(f32x2 v) {

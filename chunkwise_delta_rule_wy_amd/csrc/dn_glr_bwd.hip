@@ -9,7 +9,10 @@
 namespace dn {
 namespace {
 
-template <typename E, int ROWS>
+#ifndef BWD_ROWS
+#define BWD_ROWS 4
+#endif
+template <typename E, int ROWS, bool FLAT>
 __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   typedef typename Pair<E>::type P2;
   constexpr int TILE = GLR_RUNS * ROWS;
@@ -33,24 +36,28 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   f32x2 dlam = {0.f, 0.f}, dbr = {0.f, 0.f}, dbi = {0.f, 0.f};
   const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
   P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
-  const auto load = [&](int64_t row) {
-    glr_load<E>(p.x, row, s.row1, p.C, c, x);
-    glr_load<E>(p.r, row, s.row1, p.C, c, r);
-    glr_load<E>(p.i, row, s.row1, p.C, c, i);
-    glr_load<E>(p.dy, row, s.row1, p.C, c, dy);
+  const auto load = [&](int64_t tile) {
+    const int left = (int)min(s.row1 - tile, (int64_t)TILE);
+    glr_load<E>(p.x, tile, run * ROWS, left, left == TILE, p.C, c, x);
+    glr_load<E>(p.r, tile, run * ROWS, left, left == TILE, p.C, c, r);
+    glr_load<E>(p.i, tile, run * ROWS, left, left == TILE, p.C, c, i);
+    glr_load<E>(p.dy, tile, run * ROWS, left, left == TILE, p.C, c, dy);
   };
   GlrSeq q = {};
   if (tiles > 0) {
     q.find(p, s.row1 - 1);
-    load(s.row0 + (tiles - 1) * TILE + run * ROWS);
+    load(s.row0 + (tiles - 1) * TILE);
   }
   int turn = 0;
   for (int64_t t = tiles - 1; t >= 0; --t, turn ^= 1) {
-    const int64_t row = s.row0 + t * TILE + run * ROWS;
+    const int64_t tile = s.row0 + t * TILE, row = tile + run * ROWS;
     f32x2 state = *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
-    q.back(p, row);
-    GlrFlags f;
-    const bool slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
+    GlrFlags f = {0, 0, 0, ROWS};
+    bool slow = false;
+    if (FLAT || t == 0 || t == tiles - 1) {
+      q.back(p, row);
+      slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
+    }
     // a, 1 - sigmoid(r), m, sigmoid(i), x and dy stay until the gradients
     f32x2 a[ROWS], sr[ROWS], m[ROWS], si[ROWS], xv[ROWS], dv[ROWS];
 #pragma unroll
@@ -64,7 +71,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       a[j] = (f32x2){__builtin_amdgcn_exp2f(l0), __builtin_amdgcn_exp2f(l1)};
       m[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)), __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1))};
     }
-    if (t > 0) load(row - TILE);
+    if (t > 0) load(tile - TILE);
     const auto input = [&](int j) {
       return (f32x2){m[j][0] * si[j][0] * xv[j][0], m[j][1] * si[j][1] * xv[j][1]};
     };
@@ -117,26 +124,28 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     }
     const f32x2 oA = other_half(A), oB = other_half(B), oAr = other_half(Ar), oG = other_half(G);
     if (!upper) {
-      const f32x2 tB = glr_map(oA, B, oB);
+      const f32x2 tB = glr_map<FLAT>(oA, B, oB);
       fwd_maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
     } else {
-      const f32x2 tG = glr_map(oAr, G, oG);
+      const f32x2 tG = glr_map<FLAT>(oAr, G, oG);
       bwd_maps[turn][wave][lane] = (f32x4){Ar[0] * oAr[0], Ar[1] * oAr[1], tG[0], tG[1]};
     }
     __syncthreads();
     for (int k = 0; k < wave; ++k) {
       const f32x4 v = fwd_maps[turn][k][lane];
-      state = glr_map((f32x2){v[0], v[1]}, state, (f32x2){v[2], v[3]});
+      state = glr_map<FLAT>((f32x2){v[0], v[1]}, state, (f32x2){v[2], v[3]});
     }
-    if (upper) state = glr_map(oA, state, oB);
+    if (upper) state = glr_map<FLAT>(oA, state, oB);
     f32x2 g = {0.f, 0.f};
 #pragma unroll
     for (int k = GLR_WAVES - 1; k >= 0; --k) {
       if (k == wave) g = carry;
       const f32x4 v = bwd_maps[turn][k][lane];
-      carry = glr_map((f32x2){v[0], v[1]}, carry, (f32x2){v[2], v[3]});
+      carry = glr_map<FLAT>((f32x2){v[0], v[1]}, carry, (f32x2){v[2], v[3]});
     }
-    if (!upper) g = glr_map(oAr, g, oG);
+    if (!upper) g = glr_map<FLAT>(oAr, g, oG);
+    const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + ch * (uint32_t)sizeof(E);
+    const int64_t first = tile * p.C * (int)sizeof(E);
     // the state in front of every row
     f32x2 h[ROWS];
 #pragma unroll
@@ -180,10 +189,12 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
         dbi += di;
         if (!mine) continue;
       }
-      const int64_t o = (row + j) * p.C + ch;
-      *reinterpret_cast<P2 *>(static_cast<E *>(p.dx) + o) = to_e2<E>(dx);
-      *reinterpret_cast<P2 *>(static_cast<E *>(p.dr) + o) = to_e2<E>(dr);
-      *reinterpret_cast<P2 *>(static_cast<E *>(p.di) + o) = to_e2<E>(di);
+      const auto put = [&](void *out, f32x2 v) {
+        *reinterpret_cast<P2 *>(static_cast<char *>(out) + first + j * (size_t)pitch + off) = to_e2<E>(v);
+      };
+      put(p.dx, dx);
+      put(p.dr, dr);
+      put(p.di, di);
     }
   }
   *reinterpret_cast<f32x2 *>(&sums[0][run][2 * lane]) = dlam;
@@ -219,8 +230,13 @@ __global__ __launch_bounds__(ROW_THREADS) void glr_param_kernel(GlrParams p) {
 
 hipError_t launch_glr_bwd(const GlrParams &p, int dtype, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
-  if (dtype == 1) hipLaunchKernelGGL((glr_bwd_kernel<bf16, 4>), grid, thr, 0, st, p);
-  else hipLaunchKernelGGL((glr_bwd_kernel<float, 4>), grid, thr, 0, st, p);
+  if (dtype == 1) {
+    if (p.flat) hipLaunchKernelGGL((glr_bwd_kernel<bf16, BWD_ROWS, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_bwd_kernel<bf16, BWD_ROWS, false>), grid, thr, 0, st, p);
+  } else {
+    if (p.flat) hipLaunchKernelGGL((glr_bwd_kernel<float, BWD_ROWS, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_bwd_kernel<float, BWD_ROWS, false>), grid, thr, 0, st, p);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(glr_param_kernel, dim3((unsigned)((3 * (int64_t)p.C + SUM_COLS - 1) / SUM_COLS)), dim3(ROW_THREADS), 0,

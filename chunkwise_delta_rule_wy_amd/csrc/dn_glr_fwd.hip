@@ -26,9 +26,10 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
   // in row order: going back the maps are composed on the other side, c -> A (a c + b) + B
   for (int64_t row = beg; row < end; row += ROWS) {
     P2 r[ROWS], x[ROWS], i[ROWS];
-    glr_load<E>(p.r, row, end, p.C, c, r);
-    glr_load<E>(BACK ? p.dy : p.x, row, end, p.C, c, x);
-    if (!BACK) glr_load<E>(p.i, row, end, p.C, c, i);
+    const int left = (int)min(end - row, (int64_t)ROWS);
+    glr_load<E>(p.r, row, 0, left, left == ROWS, p.C, c, r);
+    glr_load<E>(BACK ? p.dy : p.x, row, 0, left, left == ROWS, p.C, c, x);
+    if (!BACK) glr_load<E>(p.i, row, 0, left, left == ROWS, p.C, c, i);
     GlrFlags f;
     const bool slow = glr_flags<ROWS>(p, q, row, end, f);
     GlrSeq w = q;
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
   *reinterpret_cast<f32x2 *>(out + p.C) = B;
 }
 
-template <typename E>
+template <typename E, bool FLAT>
 __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
   typedef typename Pair<E>::type P2;
   __shared__ f32x4 maps[2][GLR_WAVES][GLR_LANES];
@@ -105,18 +106,20 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
   GlrSeq q;
   q.find(p, s.row0);
   P2 x[ROWS], r[ROWS], i[ROWS];
-  const auto load = [&](int64_t row) {
-    glr_load<E>(p.x, row, s.row1, p.C, c, x);
-    glr_load<E>(p.r, row, s.row1, p.C, c, r);
-    glr_load<E>(p.i, row, s.row1, p.C, c, i);
+  const auto load = [&](int64_t tile) {
+    const int left = (int)min(s.row1 - tile, (int64_t)GLR_TILE);
+    glr_load<E>(p.x, tile, run * ROWS, left, left == GLR_TILE, p.C, c, x);
+    glr_load<E>(p.r, tile, run * ROWS, left, left == GLR_TILE, p.C, c, r);
+    glr_load<E>(p.i, tile, run * ROWS, left, left == GLR_TILE, p.C, c, i);
   };
-  load(s.row0 + run * ROWS);
+  load(s.row0);
   int turn = 0;
   int64_t block = s.state0;
   for (int64_t tile = s.row0; tile < s.row1; tile += GLR_TILE, turn ^= 1, block += GLR_TILE / GLR_STATE) {
     const int64_t row = tile + run * ROWS;
-    GlrFlags f;
-    const bool slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
+    GlrFlags f = {0, 0, 0, ROWS};
+    // in a segment of one sequence only its outer tiles have rows that need care
+    const bool slow = (FLAT || tile == s.row0 || tile + GLR_TILE >= s.row1) && __any(glr_flags<ROWS>(p, q, row, s.row1, f));
     f32x2 a[ROWS], b[ROWS], A = {1.f, 1.f}, B = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
       b[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
                      __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
     }
-    if (tile + GLR_TILE < s.row1) load(row + GLR_TILE);
+    if (tile + GLR_TILE < s.row1) load(tile + GLR_TILE);
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
     const f32x2 oA = other_half(A), oB = other_half(B);
     const bool upper = threadIdx.x & 32;
     if (!upper) {
-      const f32x2 tB = glr_map(oA, B, oB);
+      const f32x2 tB = glr_map<FLAT>(oA, B, oB);
       maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
     }
     __syncthreads();
@@ -167,17 +170,18 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
           tile + k * (GLR_TILE / GLR_WAVES) < s.row1)
         *reinterpret_cast<f32x2 *>(p.states + (block + k / (GLR_WAVES * GLR_STATE / GLR_TILE)) * p.C + ch) = carry;
       const f32x4 m = maps[turn][k][lane];
-      carry = glr_map((f32x2){m[0], m[1]}, carry, (f32x2){m[2], m[3]});
+      carry = glr_map<FLAT>((f32x2){m[0], m[1]}, carry, (f32x2){m[2], m[3]});
     }
-    if (upper) h = glr_map(oA, h, oB);
-    E *y = static_cast<E *>(p.y) + row * p.C + ch;
+    if (upper) h = glr_map<FLAT>(oA, h, oB);
+    char *y = static_cast<char *>(p.y) + tile * p.C * (int)sizeof(E);
+    const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + ch * (uint32_t)sizeof(E);
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_map(a[j], h, b[j]);
         if (j < f.live && mine) {
-          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<P2 *>(y + (int64_t)j * p.C) = to_e2<E>(h);
+          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<P2 *>(y + j * (size_t)pitch + off) = to_e2<E>(h);
           if (p.hT && f.ends >> j & 1) {
             w.walk(p, row + j);
             *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + ch) = h;
@@ -188,7 +192,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_fma(a[j], h, b[j]);
-        if (p.y && mine) *reinterpret_cast<P2 *>(y + (int64_t)j * p.C) = to_e2<E>(h);
+        if (p.y && mine) *reinterpret_cast<P2 *>(y + j * (size_t)pitch + off) = to_e2<E>(h);
       }
     }
   }
@@ -233,8 +237,13 @@ hipError_t launch_glr_sum(const GlrParams &p, int dtype, bool backward, hipStrea
 
 hipError_t launch_glr_fwd(const GlrParams &p, int dtype, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
-  if (dtype == 1) hipLaunchKernelGGL(glr_fwd_kernel<bf16>, grid, thr, 0, st, p);
-  else hipLaunchKernelGGL(glr_fwd_kernel<float>, grid, thr, 0, st, p);
+  if (dtype == 1) {
+    if (p.flat) hipLaunchKernelGGL((glr_fwd_kernel<bf16, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_fwd_kernel<bf16, false>), grid, thr, 0, st, p);
+  } else {
+    if (p.flat) hipLaunchKernelGGL((glr_fwd_kernel<float, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_fwd_kernel<float, false>), grid, thr, 0, st, p);
+  }
   return hipGetLastError();
 }
 
