@@ -20,7 +20,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   __shared__ f32x4 fwd_maps[2][GLR_WAVES][GLR_LANES], bwd_maps[2][GLR_WAVES][GLR_LANES];
   __shared__ float sums[3][GLR_RUNS][GLR_CH];
   const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
-  const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = wave_id();
+  const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
   const bool mine = ch < p.C, upper = threadIdx.x & 32;
   const GlrSegment s = glr_segment(p, seg);
@@ -131,17 +131,20 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       bwd_maps[turn][wave][lane] = (f32x4){Ar[0] * oAr[0], Ar[1] * oAr[1], tG[0], tG[1]};
     }
     __syncthreads();
-    for (int k = 0; k < wave; ++k) {
-      const f32x4 v = fwd_maps[turn][k][lane];
-      state = glr_map<FLAT>((f32x2){v[0], v[1]}, state, (f32x2){v[2], v[3]});
-    }
+    f32x4 mf[GLR_WAVES - 1], mb[GLR_WAVES];
+#pragma unroll
+    for (int k = 0; k < GLR_WAVES - 1; ++k) mf[k] = fwd_maps[turn][k][lane];
+#pragma unroll
+    for (int k = 0; k < GLR_WAVES; ++k) mb[k] = bwd_maps[turn][k][lane];
+#pragma unroll
+    for (int k = 0; k < GLR_WAVES - 1; ++k)
+      if (k < wave) state = glr_map<FLAT>((f32x2){mf[k][0], mf[k][1]}, state, (f32x2){mf[k][2], mf[k][3]});
     if (upper) state = glr_map<FLAT>(oA, state, oB);
     f32x2 g = {0.f, 0.f};
 #pragma unroll
     for (int k = GLR_WAVES - 1; k >= 0; --k) {
       if (k == wave) g = carry;
-      const f32x4 v = bwd_maps[turn][k][lane];
-      carry = glr_map<FLAT>((f32x2){v[0], v[1]}, carry, (f32x2){v[2], v[3]});
+      carry = glr_map<FLAT>((f32x2){mb[k][0], mb[k][1]}, carry, (f32x2){mb[k][2], mb[k][3]});
     }
     if (!upper) g = glr_map<FLAT>(oAr, g, oG);
     const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + ch * (uint32_t)sizeof(E);
