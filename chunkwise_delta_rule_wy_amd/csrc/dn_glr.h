@@ -109,6 +109,13 @@ __device__ __forceinline__ float glr_sigmoid(float z, float bias) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(__builtin_fmaf(z, -GLR_LOG2E, bias)));
 }
 
+// A choice that stays one: for a condition that differs between lanes the compiler
+// would branch around the side that costs more, and wait at each.
+__device__ __forceinline__ float glr_pick(bool first, float a, float b) {
+  asm("" : "+v"(a), "+v"(b));
+  return first ? a : b;
+}
+
 // 1 - a^2 for a = 2^l2, l2 <= 0: with v = -log a below 1/2, where the difference
 // would lose digits, 2 a sinh v by its series (the rest is below 2^-26 of it).
 __device__ __forceinline__ float glr_rest(float a, float l2) {
@@ -116,7 +123,7 @@ __device__ __forceinline__ float glr_rest(float a, float l2) {
   float q = __builtin_fmaf(w, 1.f / 5040, 1.f / 120);
   q = __builtin_fmaf(w, q, 1.f / 6);
   q = __builtin_fmaf(w, q, 1.f);
-  return v < 0.5f ? (v + v) * a * q : __builtin_fmaf(-a, a, 1.f);
+  return glr_pick(v < 0.5f, (v + v) * a * q, __builtin_fmaf(-a, a, 1.f));
 }
 
 // A c + B, where A = 0 drops c, whatever it is; DROP false where segments lie in

@@ -58,23 +58,28 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       q.back(p, row);
       slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
     }
-    // a, 1 - sigmoid(r), m, sigmoid(i), x and dy stay until the gradients
-    f32x2 a[ROWS], sr[ROWS], m[ROWS], si[ROWS], xv[ROWS], dv[ROWS];
+    // What stays until the gradients: a, the input b = m u, m sigmoid(i), u / m and the
+    // gates.  Below the fp32 range m counts as 0, and 1 / m as finite.
+    f32x2 a[ROWS], b[ROWS], ms[ROWS], um[ROWS], sr[ROWS], si[ROWS], dv[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const f32x2 rj = to_f2<E>(r[j]), ij = to_f2<E>(i[j]);
-      xv[j] = to_f2<E>(x[j]);
+      const f32x2 rj = to_f2<E>(r[j]), ij = to_f2<E>(i[j]), xj = to_f2<E>(x[j]);
       dv[j] = to_f2<E>(dy[j]);
-      sr[j] = (f32x2){glr_sigmoid(rj[0], k0.br), glr_sigmoid(rj[1], k1.br)};
-      si[j] = (f32x2){glr_sigmoid(ij[0], k0.bi), glr_sigmoid(ij[1], k1.bi)};
-      const float l0 = k0.k2 * sr[j][0], l1 = k1.k2 * sr[j][1];
-      a[j] = (f32x2){__builtin_amdgcn_exp2f(l0), __builtin_amdgcn_exp2f(l1)};
-      m[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)), __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1))};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const GlrChannel &k = e ? k1 : k0;
+        sr[j][e] = glr_sigmoid(rj[e], k.br);
+        si[j][e] = glr_sigmoid(ij[e], k.bi);
+        const float l2 = k.k2 * sr[j][e];
+        a[j][e] = __builtin_amdgcn_exp2f(l2);
+        const float mm = glr_rest(a[j][e], l2), over = __builtin_amdgcn_rsqf(fmaxf(mm, 1e-37f)), m = mm * over;
+        const float u = si[j][e] * xj[e];
+        b[j][e] = m * u;
+        ms[j][e] = m * si[j][e];
+        um[j][e] = u * over;
+      }
     }
     if (t > 0) load(tile - TILE);
-    const auto input = [&](int j) {
-      return (f32x2){m[j][0] * si[j][0] * xv[j][0], m[j][1] * si[j][1] * xv[j][1]};
-    };
     f32x2 A = {1.f, 1.f}, B = {0.f, 0.f}, Ar = {1.f, 1.f}, G = {0.f, 0.f};
     const auto at = [&](const float *st, int j) {  // row j's sequence of a state
       GlrSeq w = q;
@@ -84,38 +89,38 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     if (slow) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        f32x2 aj = a[j], b = input(j);
+        f32x2 aj = a[j], bj = b[j];
         if (j >= f.live) {
           aj = (f32x2){1.f, 1.f};
-          b = (f32x2){0.f, 0.f};
+          bj = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          aj = b = (f32x2){0.f, 0.f};
+          aj = bj = (f32x2){0.f, 0.f};
         } else if (f.starts >> j & 1) {
-          b = glr_fma(aj, at(p.h0, j), b);
+          bj = glr_fma(aj, at(p.h0, j), bj);
           aj = (f32x2){0.f, 0.f};
         }
-        B = glr_map(aj, B, b);
+        B = glr_map(aj, B, bj);
         A = (f32x2){A[0] * aj[0], A[1] * aj[1]};
       }
 #pragma unroll
       for (int j = ROWS - 1; j >= 0; --j) {
-        f32x2 aj = a[j], b = {a[j][0] * dv[j][0], a[j][1] * dv[j][1]};
+        f32x2 aj = a[j], gj = {a[j][0] * dv[j][0], a[j][1] * dv[j][1]};
         if (j >= f.live) {
           aj = (f32x2){1.f, 1.f};
-          b = (f32x2){0.f, 0.f};
+          gj = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          aj = b = (f32x2){0.f, 0.f};
+          aj = gj = (f32x2){0.f, 0.f};
         } else if (f.ends >> j & 1) {
-          b = glr_fma(aj, at(p.dhT, j), b);
+          gj = glr_fma(aj, at(p.dhT, j), gj);
           aj = (f32x2){0.f, 0.f};
         }
-        G = glr_map(aj, G, b);
+        G = glr_map(aj, G, gj);
         Ar = (f32x2){Ar[0] * aj[0], Ar[1] * aj[1]};
       }
     } else {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        B = glr_fma(a[j], B, input(j));
+        B = glr_fma(a[j], B, b[j]);
         A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
       }
 #pragma unroll
@@ -155,7 +160,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     for (int j = 0; j < ROWS; ++j) {
       if (slow && j < f.live && f.starts >> j & 1) state = at(p.h0, j);
       h[j] = state;
-      state = glr_fma(a[j], state, input(j));
+      state = glr_fma(a[j], state, b[j]);
     }
 #pragma unroll
     for (int j = ROWS - 1; j >= 0; --j) {
@@ -164,13 +169,12 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       f32x2 dx, dr, di, W;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ge = dv[j][e] + g[e], u = si[j][e] * xv[j][e], l = (e ? k1.k2 : k0.k2) * GLR_LN2 * sr[j][e];
-        // l / m is 0 where m is (also where 1 - a^2 fell below the fp32 range)
-        const float over = m[j][e] > 0.f ? l * __builtin_amdgcn_rcpf(m[j][e]) : 0.f;
-        W[e] = ge * (l * a[j][e] * h[j][e] - u * a[j][e] * a[j][e] * over);
-        dr[e] = (1.f - sr[j][e]) * W[e];
-        dx[e] = ge * m[j][e] * si[j][e];
-        di[e] = ge * m[j][e] * u * (1.f - si[j][e]);
+        // W = g log a (a h - u a^2 / m)
+        const float ge = dv[j][e] + g[e], la = (e ? k1.k2 : k0.k2) * GLR_LN2 * sr[j][e] * a[j][e], db = ge * b[j][e];
+        W[e] = ge * la * __builtin_fmaf(-a[j][e], um[j][e], h[j][e]);
+        dr[e] = __builtin_fmaf(-sr[j][e], W[e], W[e]);
+        dx[e] = ge * ms[j][e];
+        di[e] = __builtin_fmaf(-si[j][e], db, db);
         if (!(slow && j >= f.live)) g[e] = dead ? 0.f : a[j][e] * ge;
       }
       if (slow) {
