@@ -236,23 +236,32 @@ __device__ __forceinline__ bool glr_flags(const GlrParams &p, GlrSeq &q, int64_t
   return true;
 }
 
-// The ROWS rows of a run, two channels a lane.  `tile` (uniform) is the tile's first
-// row, `at` the run's first row in it, `left` the rows of the tile; rows behind them
-// repeat the last one.  A whole tile's addresses are uniform but for one offset.
+// A pointer that all lanes share, as the scalar base of an access with a 32-bit offset.
+#define GLR_GLOBAL __attribute__((address_space(1)))
+__device__ __forceinline__ GLR_GLOBAL char *glr_base(const void *src, int64_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(src) + bytes;
+  uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  uint64_t r = (uint64_t)hi << 32 | lo;
+  asm("" : "+s"(r));
+  return reinterpret_cast<GLR_GLOBAL char *>(r);
+}
+
+// The ROWS rows of a run, two channels a lane, from a row `tile` on that all lanes
+// share: row j of the run lies `off` and j rows behind it.
 template <typename E, int ROWS>
-__device__ __forceinline__ void glr_load(const void *src, int64_t tile, int at, int left, bool whole, int C, int c,
-                                         typename Pair<E>::type (&v)[ROWS]) {
-  const char *base = static_cast<const char *>(src) + tile * C * (int)sizeof(E);
-  const uint32_t pitch = C * (uint32_t)sizeof(E), col = c * (uint32_t)sizeof(E);
-  if (whole) {
-    const uint32_t off = at * pitch + col;
+__device__ __forceinline__ void glr_load(const void *src, int64_t tile, uint32_t off, int C, typename Pair<E>::type (&v)[ROWS]) {
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + j * (size_t)pitch + off);
-  } else {
+  for (int j = 0; j < ROWS; ++j)
+    v[j] = *reinterpret_cast<GLR_GLOBAL const typename Pair<E>::type *>(glr_base(src, (tile + j) * C * (int)sizeof(E)) + off);
+}
+// The same from row `at` on, of which `left` are there; those behind repeat the last one.
+template <typename E, int ROWS>
+__device__ __forceinline__ void glr_load_part(const void *src, int64_t tile, int at, int left, int C, int c,
+                                              typename Pair<E>::type (&v)[ROWS]) {
+  const E *base = static_cast<const E *>(src) + tile * C;
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j)
-      v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + (min(at + j, left - 1) * pitch + col));
-  }
+  for (int j = 0; j < ROWS; ++j)
+    v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + ((int64_t)min(at + j, left - 1) * C + c));
 }
 
 __device__ __forceinline__ f32x2 other_half(f32x2 v) {

@@ -36,17 +36,16 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   f32x2 dlam = {0.f, 0.f}, dbr = {0.f, 0.f}, dbi = {0.f, 0.f};
   const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
   P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
-  const auto load = [&](int64_t tile) {
-    const int left = (int)min(s.row1 - tile, (int64_t)TILE);
-    glr_load<E>(p.x, tile, run * ROWS, left, left == TILE, p.C, c, x);
-    glr_load<E>(p.r, tile, run * ROWS, left, left == TILE, p.C, c, r);
-    glr_load<E>(p.i, tile, run * ROWS, left, left == TILE, p.C, c, i);
-    glr_load<E>(p.dy, tile, run * ROWS, left, left == TILE, p.C, c, dy);
-  };
+  const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + c * (uint32_t)sizeof(E);
   GlrSeq q = {};
-  if (tiles > 0) {
+  if (tiles > 0) {  // the segment's last tile may be a part of one
     q.find(p, s.row1 - 1);
-    load(s.row0 + (tiles - 1) * TILE);
+    const int64_t tile = s.row0 + (tiles - 1) * TILE;
+    const int left = (int)(s.row1 - tile);
+    glr_load_part<E>(p.x, tile, run * ROWS, left, p.C, c, x);
+    glr_load_part<E>(p.r, tile, run * ROWS, left, p.C, c, r);
+    glr_load_part<E>(p.i, tile, run * ROWS, left, p.C, c, i);
+    glr_load_part<E>(p.dy, tile, run * ROWS, left, p.C, c, dy);
   }
   int turn = 0;
   for (int64_t t = tiles - 1; t >= 0; --t, turn ^= 1) {
@@ -79,7 +78,14 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
         um[j][e] = u * over;
       }
     }
-    if (t > 0) load(tile - TILE);
+    // the next tile; behind the last one a whole one again, if there is one
+    const int64_t ahead = t > 0 ? tile - TILE : s.row0;
+    if (tiles > 1) {
+      glr_load<E>(p.x, ahead, off, p.C, x);
+      glr_load<E>(p.r, ahead, off, p.C, r);
+      glr_load<E>(p.i, ahead, off, p.C, i);
+      glr_load<E>(p.dy, ahead, off, p.C, dy);
+    }
     f32x2 A = {1.f, 1.f}, B = {0.f, 0.f}, Ar = {1.f, 1.f}, G = {0.f, 0.f};
     const auto at = [&](const float *st, int j) {  // row j's sequence of a state
       GlrSeq w = q;
@@ -152,57 +158,55 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       carry = glr_map<FLAT>((f32x2){mb[k][0], mb[k][1]}, carry, (f32x2){mb[k][2], mb[k][3]});
     }
     if (!upper) g = glr_map<FLAT>(oAr, g, oG);
-    const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + ch * (uint32_t)sizeof(E);
-    const int64_t first = tile * p.C * (int)sizeof(E);
-    // the state in front of every row
-    f32x2 h[ROWS];
+    const auto finish = [&](auto slow_c) {
+      constexpr bool SLOW = decltype(slow_c)::value;
+      f32x2 h[ROWS];  // the state in front of every row
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      if (slow && j < f.live && f.starts >> j & 1) state = at(p.h0, j);
-      h[j] = state;
-      state = glr_fma(a[j], state, b[j]);
-    }
-#pragma unroll
-    for (int j = ROWS - 1; j >= 0; --j) {
-      const bool dead = slow && (j >= f.live || f.dead >> j & 1);
-      if (slow && !dead && f.ends >> j & 1) g = at(p.dhT, j);
-      f32x2 dx, dr, di, W;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // W = g log a (a h - u a^2 / m)
-        const float ge = dv[j][e] + g[e], la = (e ? k1.k2 : k0.k2) * GLR_LN2 * sr[j][e] * a[j][e], db = ge * b[j][e];
-        W[e] = ge * la * __builtin_fmaf(-a[j][e], um[j][e], h[j][e]);
-        dr[e] = __builtin_fmaf(-sr[j][e], W[e], W[e]);
-        dx[e] = ge * ms[j][e];
-        di[e] = __builtin_fmaf(-si[j][e], db, db);
-        if (!(slow && j >= f.live)) g[e] = dead ? 0.f : a[j][e] * ge;
+      for (int j = 0; j < ROWS; ++j) {
+        if (SLOW && j < f.live && f.starts >> j & 1) state = at(p.h0, j);
+        h[j] = state;
+        state = glr_fma(a[j], state, b[j]);
       }
-      if (slow) {
-        if (dead) dx = dr = di = (f32x2){0.f, 0.f};
-        else {
+#pragma unroll
+      for (int j = ROWS - 1; j >= 0; --j) {
+        if (SLOW && j >= f.live) continue;
+        const bool dead = SLOW && f.dead >> j & 1;
+        if (SLOW && f.ends >> j & 1) g = at(p.dhT, j);
+        f32x2 dx, dr, di, W;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // W = g log a (a h - u a^2 / m)
+          const float ge = dv[j][e] + g[e], la = (e ? k1.k2 : k0.k2) * GLR_LN2 * sr[j][e] * a[j][e], db = ge * b[j][e];
+          W[e] = ge * la * __builtin_fmaf(-a[j][e], um[j][e], h[j][e]);
+          dr[e] = __builtin_fmaf(-sr[j][e], W[e], W[e]);
+          dx[e] = ge * ms[j][e];
+          di[e] = __builtin_fmaf(-si[j][e], db, db);
+          g[e] = a[j][e] * ge;
+        }
+        if (SLOW && dead) {
+          g = dx = dr = di = (f32x2){0.f, 0.f};
+          if (!p.zero_tail) continue;
+        } else {
           dlam += W;
           dbr += dr;
           dbi += di;
-          if (p.dh0 && mine && f.starts >> j & 1) {
+          if (SLOW && p.dh0 && f.starts >> j & 1) {
             GlrSeq w = q;
             w.walk(p, row + j);
             *reinterpret_cast<f32x2 *>(p.dh0 + (size_t)w.n * p.C + ch) = g;
           }
         }
-        if (!mine || j >= f.live || (dead && !p.zero_tail)) continue;
-      } else {
-        dlam += W;
-        dbr += dr;
-        dbi += di;
-        if (!mine) continue;
+        const auto put = [&](void *out, f32x2 v) {
+          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, (tile + j) * pitch) + off) = to_e2<E>(v);
+        };
+        put(p.dx, dx);
+        put(p.dr, dr);
+        put(p.di, di);
       }
-      const auto put = [&](void *out, f32x2 v) {
-        *reinterpret_cast<P2 *>(static_cast<char *>(out) + first + j * (size_t)pitch + off) = to_e2<E>(v);
-      };
-      put(p.dx, dx);
-      put(p.dr, dr);
-      put(p.di, di);
-    }
+    };
+    if (!mine) continue;
+    if (slow) finish(std::true_type());
+    else finish(std::false_type());
   }
   *reinterpret_cast<f32x2 *>(&sums[0][run][2 * lane]) = dlam;
   *reinterpret_cast<f32x2 *>(&sums[1][run][2 * lane]) = dbr;

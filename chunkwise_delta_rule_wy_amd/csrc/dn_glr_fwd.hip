@@ -27,9 +27,9 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
   for (int64_t row = beg; row < end; row += ROWS) {
     P2 r[ROWS], x[ROWS], i[ROWS];
     const int left = (int)min(end - row, (int64_t)ROWS);
-    glr_load<E>(p.r, row, 0, left, left == ROWS, p.C, c, r);
-    glr_load<E>(BACK ? p.dy : p.x, row, 0, left, left == ROWS, p.C, c, x);
-    if (!BACK) glr_load<E>(p.i, row, 0, left, left == ROWS, p.C, c, i);
+    glr_load_part<E>(p.r, row, 0, left, p.C, c, r);
+    glr_load_part<E>(BACK ? p.dy : p.x, row, 0, left, p.C, c, x);
+    if (!BACK) glr_load_part<E>(p.i, row, 0, left, p.C, c, i);
     GlrFlags f;
     const bool slow = glr_flags<ROWS>(p, q, row, end, f);
     GlrSeq w = q;
@@ -106,11 +106,19 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
   GlrSeq q;
   q.find(p, s.row0);
   P2 x[ROWS], r[ROWS], i[ROWS];
+  // the tiles' loads; the last tile may be a part of one
+  const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + c * (uint32_t)sizeof(E);
   const auto load = [&](int64_t tile) {
     const int left = (int)min(s.row1 - tile, (int64_t)GLR_TILE);
-    glr_load<E>(p.x, tile, run * ROWS, left, left == GLR_TILE, p.C, c, x);
-    glr_load<E>(p.r, tile, run * ROWS, left, left == GLR_TILE, p.C, c, r);
-    glr_load<E>(p.i, tile, run * ROWS, left, left == GLR_TILE, p.C, c, i);
+    if (left == GLR_TILE) {
+      glr_load<E>(p.x, tile, off, p.C, x);
+      glr_load<E>(p.r, tile, off, p.C, r);
+      glr_load<E>(p.i, tile, off, p.C, i);
+    } else {
+      glr_load_part<E>(p.x, tile, run * ROWS, left, p.C, c, x);
+      glr_load_part<E>(p.r, tile, run * ROWS, left, p.C, c, r);
+      glr_load_part<E>(p.i, tile, run * ROWS, left, p.C, c, i);
+    }
   };
   load(s.row0);
   int turn = 0;
@@ -129,7 +137,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
       b[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
                      __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
     }
-    if (tile + GLR_TILE < s.row1) load(tile + GLR_TILE);
+    load(tile + GLR_TILE < s.row1 ? tile + GLR_TILE : s.row0);  // behind the last one the first again
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
@@ -173,15 +181,14 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
       carry = glr_map<FLAT>((f32x2){m[0], m[1]}, carry, (f32x2){m[2], m[3]});
     }
     if (upper) h = glr_map<FLAT>(oA, h, oB);
-    char *y = static_cast<char *>(p.y) + tile * p.C * (int)sizeof(E);
-    const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + ch * (uint32_t)sizeof(E);
+    if (!mine) continue;
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_map(a[j], h, b[j]);
-        if (j < f.live && mine) {
-          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<P2 *>(y + j * (size_t)pitch + off) = to_e2<E>(h);
+        if (j < f.live) {
+          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + off) = to_e2<E>(h);
           if (p.hT && f.ends >> j & 1) {
             w.walk(p, row + j);
             *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + ch) = h;
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_fma(a[j], h, b[j]);
-        if (p.y && mine) *reinterpret_cast<P2 *>(y + j * (size_t)pitch + off) = to_e2<E>(h);
+        if (p.y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + off) = to_e2<E>(h);
       }
     }
   }
