@@ -236,7 +236,8 @@ __device__ __forceinline__ bool glr_flags(const GlrParams &p, GlrSeq &q, int64_t
   return true;
 }
 
-// A pointer that all lanes share, as the scalar base of an access with a 32-bit offset.
+// A pointer that all lanes share, as the scalar base of an access with a 32-bit offset;
+// and the offset, kept from being widened to 64 bits far from the access.
 #define GLR_GLOBAL __attribute__((address_space(1)))
 __device__ __forceinline__ GLR_GLOBAL char *glr_base(const void *src, int64_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(src) + bytes;
@@ -246,10 +247,16 @@ __device__ __forceinline__ GLR_GLOBAL char *glr_base(const void *src, int64_t by
   return reinterpret_cast<GLR_GLOBAL char *>(r);
 }
 
+__device__ __forceinline__ uint32_t glr_offset(uint32_t off) {
+  asm volatile("" : "+v"(off));
+  return off;
+}
+
 // The ROWS rows of a run, two channels a lane, from a row `tile` on that all lanes
 // share: row j of the run lies `off` and j rows behind it.
 template <typename E, int ROWS>
 __device__ __forceinline__ void glr_load(const void *src, int64_t tile, uint32_t off, int C, typename Pair<E>::type (&v)[ROWS]) {
+  off = glr_offset(off);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j)
     v[j] = *reinterpret_cast<GLR_GLOBAL const typename Pair<E>::type *>(glr_base(src, (tile + j) * C * (int)sizeof(E)) + off);

@@ -37,11 +37,16 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
   P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
   const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + c * (uint32_t)sizeof(E);
+  const auto kept_state = [&](int64_t t) {
+    return *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
+  };
+  f32x2 kept = {0.f, 0.f};
   GlrSeq q = {};
   if (tiles > 0) {  // the segment's last tile may be a part of one
     q.find(p, s.row1 - 1);
     const int64_t tile = s.row0 + (tiles - 1) * TILE;
     const int left = (int)(s.row1 - tile);
+    kept = kept_state(tiles - 1);
     glr_load_part<E>(p.x, tile, run * ROWS, left, p.C, c, x);
     glr_load_part<E>(p.r, tile, run * ROWS, left, p.C, c, r);
     glr_load_part<E>(p.i, tile, run * ROWS, left, p.C, c, i);
@@ -50,7 +55,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   int turn = 0;
   for (int64_t t = tiles - 1; t >= 0; --t, turn ^= 1) {
     const int64_t tile = s.row0 + t * TILE, row = tile + run * ROWS;
-    f32x2 state = *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
+    f32x2 state = kept;
     GlrFlags f = {0, 0, 0, ROWS};
     bool slow = false;
     if (FLAT || t == 0 || t == tiles - 1) {
@@ -79,8 +84,10 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       }
     }
     // the next tile; behind the last one a whole one again, if there is one
+    // (its state too: a load that is waited for by itself would wait for the others)
     const int64_t ahead = t > 0 ? tile - TILE : s.row0;
     if (tiles > 1) {
+      kept = kept_state(t > 0 ? t - 1 : 0);
       glr_load<E>(p.x, ahead, off, p.C, x);
       glr_load<E>(p.r, ahead, off, p.C, r);
       glr_load<E>(p.i, ahead, off, p.C, i);
@@ -159,6 +166,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     }
     if (!upper) g = glr_map<FLAT>(oAr, g, oG);
     const auto finish = [&](auto slow_c) {
+      const uint32_t o = glr_offset(off);
       constexpr bool SLOW = decltype(slow_c)::value;
       f32x2 h[ROWS];  // the state in front of every row
 #pragma unroll
@@ -197,7 +205,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
           }
         }
         const auto put = [&](void *out, f32x2 v) {
-          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, (tile + j) * pitch) + off) = to_e2<E>(v);
+          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, (tile + j) * pitch) + o) = to_e2<E>(v);
         };
         put(p.dx, dx);
         put(p.dr, dr);

@@ -182,13 +182,14 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
     }
     if (upper) h = glr_map<FLAT>(oA, h, oB);
     if (!mine) continue;
+    const uint32_t o = glr_offset(off);
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_map(a[j], h, b[j]);
         if (j < f.live) {
-          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + off) = to_e2<E>(h);
+          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + o) = to_e2<E>(h);
           if (p.hT && f.ends >> j & 1) {
             w.walk(p, row + j);
             *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + ch) = h;
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_fma(a[j], h, b[j]);
-        if (p.y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + off) = to_e2<E>(h);
+        if (p.y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + o) = to_e2<E>(h);
       }
     }
   }
