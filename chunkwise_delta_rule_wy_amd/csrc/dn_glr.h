@@ -236,8 +236,7 @@ __device__ __forceinline__ bool glr_flags(const GlrParams &p, GlrSeq &q, int64_t
   return true;
 }
 
-// A pointer that all lanes share, as the scalar base of an access with a 32-bit offset;
-// and the offset, kept from being widened to 64 bits far from the access.
+// A pointer that all lanes share, as the scalar base of an access with a 32-bit offset.
 #define GLR_GLOBAL __attribute__((address_space(1)))
 __device__ __forceinline__ GLR_GLOBAL char *glr_base(const void *src, int64_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(src) + bytes;
@@ -247,29 +246,42 @@ __device__ __forceinline__ GLR_GLOBAL char *glr_base(const void *src, int64_t by
   return reinterpret_cast<GLR_GLOBAL char *>(r);
 }
 
-__device__ __forceinline__ uint32_t glr_offset(uint32_t off) {
-  asm volatile("" : "+v"(off));
-  return off;
+// Byte offsets of a run's ROWS rows from a tile's first, of which `left` are there;
+// those behind repeat the last one (an offset is the larger the later the row).
+// Opaque, as the compiler would widen them to 64 bits far from the accesses.
+template <int ROWS>
+__device__ __forceinline__ void glr_offsets(uint32_t (&o)[ROWS], int at, int left, uint32_t pitch, uint32_t col) {
+  const uint32_t last = (left - 1) * pitch + col;
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+    o[j] = min((at + j) * pitch + col, last);
+    asm volatile("" : "+v"(o[j]));
+  }
 }
 
-// The ROWS rows of a run, two channels a lane, from a row `tile` on that all lanes
-// share: row j of the run lies `off` and j rows behind it.
+// The rows of a run, two channels a lane, from a tile's first row on that all lanes share.
 template <typename E, int ROWS>
-__device__ __forceinline__ void glr_load(const void *src, int64_t tile, uint32_t off, int C, typename Pair<E>::type (&v)[ROWS]) {
-  off = glr_offset(off);
+__device__ __forceinline__ void glr_load(const void *src, int64_t tile, const uint32_t (&o)[ROWS], int C,
+                                         typename Pair<E>::type (&v)[ROWS]) {
+  GLR_GLOBAL char *base = glr_base(src, tile * C * (int)sizeof(E));
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) v[j] = *reinterpret_cast<GLR_GLOBAL const typename Pair<E>::type *>(base + o[j]);
+}
+// The same where lanes differ in the rows: row j of `left` from `row` on.
+template <typename E, int ROWS>
+__device__ __forceinline__ void glr_load_at(const void *src, int64_t row, int left, int C, int c,
+                                            typename Pair<E>::type (&v)[ROWS]) {
+  const E *base = static_cast<const E *>(src) + row * C + c;
 #pragma unroll
   for (int j = 0; j < ROWS; ++j)
-    v[j] = *reinterpret_cast<GLR_GLOBAL const typename Pair<E>::type *>(glr_base(src, (tile + j) * C * (int)sizeof(E)) + off);
+    v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + (int64_t)min(j, left - 1) * C);
 }
-// The same from row `at` on, of which `left` are there; those behind repeat the last one.
-template <typename E, int ROWS>
-__device__ __forceinline__ void glr_load_part(const void *src, int64_t tile, int at, int left, int C, int c,
-                                              typename Pair<E>::type (&v)[ROWS]) {
-  const E *base = static_cast<const E *>(src) + tile * C;
-#pragma unroll
-  for (int j = 0; j < ROWS; ++j)
-    v[j] = *reinterpret_cast<const typename Pair<E>::type *>(base + ((int64_t)min(at + j, left - 1) * C + c));
-}
+
+// All of the wave's loads and stores done.  The compiler counts the operations behind
+// a load to wait for it alone, and where ways meet it takes the fewest: the walks'
+// first tiles and careful rows end with this, so that the usual rows' loads do not
+// wait for the stores behind them.
+__device__ __forceinline__ void glr_settle() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
 __device__ __forceinline__ f32x2 other_half(f32x2 v) {
   return (f32x2){__shfl_xor(v[0], 32, 64), __shfl_xor(v[1], 32, 64)};

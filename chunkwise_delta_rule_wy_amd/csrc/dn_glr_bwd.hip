@@ -21,36 +21,42 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   __shared__ float sums[3][GLR_RUNS][GLR_CH];
   const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
   const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = __builtin_amdgcn_readfirstlane(wave_id());
-  const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
-  const bool mine = ch < p.C, upper = threadIdx.x & 32;
+  // lanes behind the last channels repeat them, stores included
+  const int c = min(grp * GLR_CH + 2 * lane, p.C - 2);
+  const bool upper = threadIdx.x & 32;
   const GlrSegment s = glr_segment(p, seg);
   const GlrChannel k0 = glr_channel(p.lam, p.br, p.bi, p.power, c), k1 = glr_channel(p.lam, p.br, p.bi, p.power, c + 1);
   // sequences without tokens pass dhT on
   if (p.dh0 && (p.cu || p.T == 0))
     for (int64_t n = (int64_t)seg * GLR_RUNS + run; n < p.N; n += (int64_t)p.nseg * GLR_RUNS)
-      if (mine && (!p.cu || p.cu[n] == p.cu[n + 1]))
-        *reinterpret_cast<f32x2 *>(p.dh0 + n * p.C + ch) =
-            p.dhT ? *reinterpret_cast<const f32x2 *>(p.dhT + n * p.C + ch) : (f32x2){0.f, 0.f};
+      if (!p.cu || p.cu[n] == p.cu[n + 1])
+        *reinterpret_cast<f32x2 *>(p.dh0 + n * p.C + c) =
+            p.dhT ? *reinterpret_cast<const f32x2 *>(p.dhT + n * p.C + c) : (f32x2){0.f, 0.f};
   f32x2 carry = {0.f, 0.f};  // the gradient that reaches the tile from behind
   if (p.cut) carry = glr_join<true>(p, p.sum_r, seg + 1, s.last + 1, c, &fwd_maps[0][0][0]);
   f32x2 dlam = {0.f, 0.f}, dbr = {0.f, 0.f}, dbi = {0.f, 0.f};
   const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
   P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
-  const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + c * (uint32_t)sizeof(E);
-  const auto kept_state = [&](int64_t t) {
-    return *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
-  };
+  const uint32_t pitch = p.C * (uint32_t)sizeof(E), col = c * (uint32_t)sizeof(E);
   f32x2 kept = {0.f, 0.f};
+  // tile t, and the state kept in front of it: a load that is waited for by itself
+  // would wait for the others.  No branch: registers that are loaded in one of two
+  // ways get copied where these meet, and the copies wait
+  const auto load = [&](int64_t t) {
+    const int64_t tile = s.row0 + t * TILE;
+    uint32_t o[ROWS];
+    glr_offsets<ROWS>(o, run * ROWS, (int)min(s.row1 - tile, (int64_t)TILE), pitch, col);
+    kept = *reinterpret_cast<const f32x2 *>(p.states + (s.state0 + t * (TILE / GLR_STATE)) * p.C + c);
+    glr_load<E>(p.x, tile, o, p.C, x);
+    glr_load<E>(p.r, tile, o, p.C, r);
+    glr_load<E>(p.i, tile, o, p.C, i);
+    glr_load<E>(p.dy, tile, o, p.C, dy);
+  };
   GlrSeq q = {};
-  if (tiles > 0) {  // the segment's last tile may be a part of one
+  if (tiles > 0) {
     q.find(p, s.row1 - 1);
-    const int64_t tile = s.row0 + (tiles - 1) * TILE;
-    const int left = (int)(s.row1 - tile);
-    kept = kept_state(tiles - 1);
-    glr_load_part<E>(p.x, tile, run * ROWS, left, p.C, c, x);
-    glr_load_part<E>(p.r, tile, run * ROWS, left, p.C, c, r);
-    glr_load_part<E>(p.i, tile, run * ROWS, left, p.C, c, i);
-    glr_load_part<E>(p.dy, tile, run * ROWS, left, p.C, c, dy);
+    load(tiles - 1);
+    glr_settle();
   }
   int turn = 0;
   for (int64_t t = tiles - 1; t >= 0; --t, turn ^= 1) {
@@ -83,16 +89,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
         um[j][e] = u * over;
       }
     }
-    // the next tile; behind the last one a whole one again, if there is one
-    // (its state too: a load that is waited for by itself would wait for the others)
-    const int64_t ahead = t > 0 ? tile - TILE : s.row0;
-    if (tiles > 1) {
-      kept = kept_state(t > 0 ? t - 1 : 0);
-      glr_load<E>(p.x, ahead, off, p.C, x);
-      glr_load<E>(p.r, ahead, off, p.C, r);
-      glr_load<E>(p.i, ahead, off, p.C, i);
-      glr_load<E>(p.dy, ahead, off, p.C, dy);
-    }
+    load(t > 0 ? t - 1 : 0);  // behind the last tile that one again
     f32x2 A = {1.f, 1.f}, B = {0.f, 0.f}, Ar = {1.f, 1.f}, G = {0.f, 0.f};
     const auto at = [&](const float *st, int j) {  // row j's sequence of a state
       GlrSeq w = q;
@@ -166,7 +163,8 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     }
     if (!upper) g = glr_map<FLAT>(oAr, g, oG);
     const auto finish = [&](auto slow_c) {
-      const uint32_t o = glr_offset(off);
+      uint32_t o[ROWS];
+      glr_offsets<ROWS>(o, run * ROWS, TILE, pitch, col);
       constexpr bool SLOW = decltype(slow_c)::value;
       f32x2 h[ROWS];  // the state in front of every row
 #pragma unroll
@@ -201,31 +199,32 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
           if (SLOW && p.dh0 && f.starts >> j & 1) {
             GlrSeq w = q;
             w.walk(p, row + j);
-            *reinterpret_cast<f32x2 *>(p.dh0 + (size_t)w.n * p.C + ch) = g;
+            *reinterpret_cast<f32x2 *>(p.dh0 + (size_t)w.n * p.C + c) = g;
           }
         }
         const auto put = [&](void *out, f32x2 v) {
-          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, (tile + j) * pitch) + o) = to_e2<E>(v);
+          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, tile * pitch) + o[j]) = to_e2<E>(v);
         };
         put(p.dx, dx);
         put(p.dr, dr);
         put(p.di, di);
       }
     };
-    if (!mine) continue;
-    if (slow) finish(std::true_type());
-    else finish(std::false_type());
+    if (slow) {
+      finish(std::true_type());
+      glr_settle();
+    } else finish(std::false_type());
   }
   *reinterpret_cast<f32x2 *>(&sums[0][run][2 * lane]) = dlam;
   *reinterpret_cast<f32x2 *>(&sums[1][run][2 * lane]) = dbr;
   *reinterpret_cast<f32x2 *>(&sums[2][run][2 * lane]) = dbi;
   __syncthreads();
-  const int which = threadIdx.x / GLR_CH, col = threadIdx.x % GLR_CH;
-  if (which >= 3 || grp * GLR_CH + col >= p.C) return;
+  const int which = threadIdx.x / GLR_CH, channel = threadIdx.x % GLR_CH;
+  if (which >= 3 || grp * GLR_CH + channel >= p.C) return;
   float sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < GLR_RUNS; ++k) sum += sums[which][k][col];
-  p.part[((size_t)seg * 3 + which) * p.C + grp * GLR_CH + col] = sum;
+  for (int k = 0; k < GLR_RUNS; ++k) sum += sums[which][k][channel];
+  p.part[((size_t)seg * 3 + which) * p.C + grp * GLR_CH + channel] = sum;
 }
 
 // The parameters' gradients from the segments' sums.

@@ -27,9 +27,9 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
   for (int64_t row = beg; row < end; row += ROWS) {
     P2 r[ROWS], x[ROWS], i[ROWS];
     const int left = (int)min(end - row, (int64_t)ROWS);
-    glr_load_part<E>(p.r, row, 0, left, p.C, c, r);
-    glr_load_part<E>(BACK ? p.dy : p.x, row, 0, left, p.C, c, x);
-    if (!BACK) glr_load_part<E>(p.i, row, 0, left, p.C, c, i);
+    glr_load_at<E>(p.r, row, left, p.C, c, r);
+    glr_load_at<E>(BACK ? p.dy : p.x, row, left, p.C, c, x);
+    if (!BACK) glr_load_at<E>(p.i, row, left, p.C, c, i);
     GlrFlags f;
     const bool slow = glr_flags<ROWS>(p, q, row, end, f);
     GlrSeq w = q;
@@ -84,43 +84,40 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
   *reinterpret_cast<f32x2 *>(out + p.C) = B;
 }
 
-template <typename E, bool FLAT>
+template <typename E, bool FLAT, bool Y>
 __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
   typedef typename Pair<E>::type P2;
   __shared__ f32x4 maps[2][GLR_WAVES][GLR_LANES];
   const int seg = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
   const int lane = threadIdx.x % GLR_LANES, run = threadIdx.x / GLR_LANES, wave = wave_id();
-  const int ch = grp * GLR_CH + 2 * lane, c = min(ch, p.C - 2);
-  const bool mine = ch < p.C;
+  // lanes behind the last channels repeat them, stores included
+  const int c = min(grp * GLR_CH + 2 * lane, p.C - 2);
   const GlrSegment s = glr_segment(p, seg);
   const GlrChannel k0 = glr_channel(p.lam, p.br, p.bi, p.power, c), k1 = glr_channel(p.lam, p.br, p.bi, p.power, c + 1);
   // sequences without tokens pass h0 on
   if (p.hT && (p.cu || p.T == 0))
     for (int64_t n = (int64_t)seg * GLR_RUNS + run; n < p.N; n += (int64_t)p.nseg * GLR_RUNS)
-      if (mine && (!p.cu || p.cu[n] == p.cu[n + 1]))
-        *reinterpret_cast<f32x2 *>(p.hT + n * p.C + ch) =
-            p.h0 ? *reinterpret_cast<const f32x2 *>(p.h0 + n * p.C + ch) : (f32x2){0.f, 0.f};
+      if (!p.cu || p.cu[n] == p.cu[n + 1])
+        *reinterpret_cast<f32x2 *>(p.hT + n * p.C + c) =
+            p.h0 ? *reinterpret_cast<const f32x2 *>(p.h0 + n * p.C + c) : (f32x2){0.f, 0.f};
   f32x2 carry = {0.f, 0.f};  // the state in front of the tile
   if (p.cut) carry = glr_join<false>(p, p.sum_f, s.first, seg, c, &maps[0][0][0]);
   if (s.row0 >= s.row1) return;
   GlrSeq q;
   q.find(p, s.row0);
   P2 x[ROWS], r[ROWS], i[ROWS];
-  // the tiles' loads; the last tile may be a part of one
-  const uint32_t pitch = p.C * (uint32_t)sizeof(E), off = run * ROWS * pitch + c * (uint32_t)sizeof(E);
+  // No branch in the loads: registers that are loaded in one of two ways get copied
+  // where these meet, and the copies wait.
+  const uint32_t pitch = p.C * (uint32_t)sizeof(E), col = c * (uint32_t)sizeof(E);
   const auto load = [&](int64_t tile) {
-    const int left = (int)min(s.row1 - tile, (int64_t)GLR_TILE);
-    if (left == GLR_TILE) {
-      glr_load<E>(p.x, tile, off, p.C, x);
-      glr_load<E>(p.r, tile, off, p.C, r);
-      glr_load<E>(p.i, tile, off, p.C, i);
-    } else {
-      glr_load_part<E>(p.x, tile, run * ROWS, left, p.C, c, x);
-      glr_load_part<E>(p.r, tile, run * ROWS, left, p.C, c, r);
-      glr_load_part<E>(p.i, tile, run * ROWS, left, p.C, c, i);
-    }
+    uint32_t o[ROWS];
+    glr_offsets<ROWS>(o, run * ROWS, (int)min(s.row1 - tile, (int64_t)GLR_TILE), pitch, col);
+    glr_load<E>(p.x, tile, o, p.C, x);
+    glr_load<E>(p.r, tile, o, p.C, r);
+    glr_load<E>(p.i, tile, o, p.C, i);
   };
   load(s.row0);
+  glr_settle();
   int turn = 0;
   int64_t block = s.state0;
   for (int64_t tile = s.row0; tile < s.row1; tile += GLR_TILE, turn ^= 1, block += GLR_TILE / GLR_STATE) {
@@ -174,33 +171,34 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
     for (int k = 0; k < GLR_WAVES; ++k) {
       if (k == wave) h = carry;
-      if (p.states && k % (GLR_WAVES * GLR_STATE / GLR_TILE) == 0 && k == wave && !upper && mine &&
+      if (p.states && k % (GLR_WAVES * GLR_STATE / GLR_TILE) == 0 && k == wave && !upper &&
           tile + k * (GLR_TILE / GLR_WAVES) < s.row1)
-        *reinterpret_cast<f32x2 *>(p.states + (block + k / (GLR_WAVES * GLR_STATE / GLR_TILE)) * p.C + ch) = carry;
+        *reinterpret_cast<f32x2 *>(p.states + (block + k / (GLR_WAVES * GLR_STATE / GLR_TILE)) * p.C + c) = carry;
       const f32x4 m = maps[turn][k][lane];
       carry = glr_map<FLAT>((f32x2){m[0], m[1]}, carry, (f32x2){m[2], m[3]});
     }
     if (upper) h = glr_map<FLAT>(oA, h, oB);
-    if (!mine) continue;
-    const uint32_t o = glr_offset(off);
+    uint32_t o[ROWS];
+    glr_offsets<ROWS>(o, run * ROWS, GLR_TILE, pitch, col);
     if (slow) {
       GlrSeq w = q;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_map(a[j], h, b[j]);
         if (j < f.live) {
-          if (p.y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + o) = to_e2<E>(h);
+          if (Y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, tile * pitch) + o[j]) = to_e2<E>(h);
           if (p.hT && f.ends >> j & 1) {
             w.walk(p, row + j);
-            *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + ch) = h;
+            *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + c) = h;
           }
         }
       }
+      glr_settle();
     } else {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_fma(a[j], h, b[j]);
-        if (p.y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, (tile + j) * pitch) + o) = to_e2<E>(h);
+        if (Y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, tile * pitch) + o[j]) = to_e2<E>(h);
       }
     }
   }
@@ -245,13 +243,14 @@ hipError_t launch_glr_sum(const GlrParams &p, int dtype, bool backward, hipStrea
 
 hipError_t launch_glr_fwd(const GlrParams &p, int dtype, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.nseg * p.groups)), thr(GLR_THREADS);
-  if (dtype == 1) {
-    if (p.flat) hipLaunchKernelGGL((glr_fwd_kernel<bf16, true>), grid, thr, 0, st, p);
-    else hipLaunchKernelGGL((glr_fwd_kernel<bf16, false>), grid, thr, 0, st, p);
-  } else {
-    if (p.flat) hipLaunchKernelGGL((glr_fwd_kernel<float, true>), grid, thr, 0, st, p);
-    else hipLaunchKernelGGL((glr_fwd_kernel<float, false>), grid, thr, 0, st, p);
-  }
+  const auto go = [&](auto e, auto y) {
+    typedef decltype(e) E;
+    constexpr bool Y = decltype(y)::value;
+    if (p.flat) hipLaunchKernelGGL((glr_fwd_kernel<E, true, Y>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_fwd_kernel<E, false, Y>), grid, thr, 0, st, p);
+  };
+  if (dtype == 1) p.y ? go(bf16(), std::true_type()) : go(bf16(), std::false_type());
+  else p.y ? go(0.f, std::true_type()) : go(0.f, std::false_type());
   return hipGetLastError();
 }
 
