@@ -23,11 +23,15 @@ dn_status check(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int3
   return DN_OK;
 }
 
-// Segments.  Sequences of FLAT rows and more are cut by themselves, and only
-// where they and the channels give fewer workgroups than FULL; packed and shorter
-// ones lie in one run of rows that is cut evenly, whatever the sequences'
-// lengths, into about WANT workgroups.
-constexpr int64_t FLAT = 512, FULL = 192, WANT = 512;
+// Segments.  Sequences of FLAT rows and more are cut by themselves, packed and
+// shorter ones lie in one run of rows that is cut evenly, whatever their lengths.
+// Cutting reads the inputs twice (the segments' maps first), so that it pays only
+// where sequences and channels give fewer than FULL workgroups (forwards and backwards
+// in us, uncut [cut]: 128 workgroups of 4 x 4096 rows in fp32, 143 + 235 [199 + 252]; 64
+// of 16384 packed rows, 419 + 695 [243 + 278]), and then up to about WANT, one for each
+// CU (the packed rows with 512: 238 + 286, with 1024: 243 + 302, with 128: 401 + 471; 16384
+// rows of 2048 channels with 256: 112 + 143, with 512: 116 + 150).
+constexpr int64_t FLAT = 512, FULL = 100, WANT = 256;
 
 struct Plan {
   bool flat, cut;
