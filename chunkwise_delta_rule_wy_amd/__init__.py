@@ -17,6 +17,7 @@ States are stored transposed, ``h = S^T`` with shape ``[N, H, Dk, Dv]``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -993,17 +994,34 @@ def _glr_args(x, r, i, lam, br, bi, state, cu_seqlens, dims):
     return dev, lead, H, D, N
 
 
+def _glr_fits(x, r, i, lam, br, bi, state, cu_seqlens):
+    """(whether the arguments are right, device index, sizes, sequences), in as few steps as possible."""
+    try:
+        E, dev, xs, f32 = x.dtype, x.get_device(), x.shape, torch.float32
+        B, _, H, D = xs
+        N, cs = B if cu_seqlens is None else cu_seqlens.shape[0] - 1, xs[2:]
+        return (E in _DTYPES and dev >= 0 and max(xs) <= _MAX_SIZE and x.is_contiguous() and _fits(r, E, xs, dev)
+                and _fits(i, E, xs, dev) and _fits(lam, f32, cs, dev) and (br is None or _fits(br, f32, cs, dev))
+                and (bi is None or _fits(bi, f32, cs, dev)) and (state is None or _fits(state, f32, (N, H, D), dev))
+                and (cu_seqlens is None or (B == 1 and N > 0 and _fits(cu_seqlens, torch.int32, (N + 1,), dev)))), dev, xs, N
+    except (AttributeError, ValueError, IndexError):  # not a tensor, not of four dimensions
+        return False, None, None, None
+
+
+@functools.lru_cache(maxsize=256)
+def _glr_sizes(B, T, H, D):
+    """Rows of states, bytes of workspace forwards, backwards with and without states."""
+    lib = load_library()
+    return (lib.dn_glr_states(B, T, H, D), lib.dn_glr_fwd_workspace(B, T, H, D), lib.dn_glr_bwd_workspace(B, T, H, D, 1),
+            lib.dn_glr_bwd_workspace(B, T, H, D, 0))
+
+
 def glr_states(x):
     """New memory for the states that ``glr_fwd`` keeps for ``glr_bwd`` (x
     ``[B,T,H,D]``): float32 ``[rows,H,D]``, about one row for 64 tokens."""
     dev = _gpu(x, "x", (4,), tuple(_DTYPES))
     B, T, H, D = x.shape
-    return torch.empty((load_library().dn_glr_states(B, T, H, D), H, D), dtype=torch.float32, device=dev)
-
-
-def _glr_states(states, B, T, H, D, dev):
-    if states is not None:
-        _is(states, "states", torch.float32, (load_library().dn_glr_states(B, T, H, D), H, D), dev)
+    return torch.empty((_glr_sizes(B, T, H, D)[0], H, D), dtype=torch.float32, device=dev)
 
 
 def glr_fwd(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: float = 8.0, states=None):
@@ -1017,14 +1035,18 @@ def glr_fwd(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: flo
     ``[H,D]`` float32 (br, bi None: zero); h0 ``[N,H,D]`` float32 or None;
     cu_seqlens as in ``ssm_fwd``; states from ``glr_states``, filled for
     ``glr_bwd``.  Returns ``(y, hT)``, y in x's dtype, hT ``[N,H,D]`` float32."""
-    dev, (B, T), H, D, N = _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
-    _glr_states(states, B, T, H, D, dev)
+    fits, dev, xs, N = _glr_fits(x, r, i, lam, br, bi, h0, cu_seqlens)
+    if not fits:
+        _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
+    B, T, H, D = xs
+    rows, wsb, _, _ = _glr_sizes(B, T, H, D)
+    _is(states, "states", torch.float32, (rows, H, D), x.device)
     y = torch.empty_like(x)
-    hT = torch.empty((N, H, D), dtype=torch.float32, device=dev)
-    wsb = load_library().dn_glr_fwd_workspace(B, T, H, D)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_glr_fwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(r), _adr(i), _adr(lam), _adr(br),
-          _adr(bi), float(power), _adr(h0), _adr(cu_seqlens), _adr(y), _adr(hT), _adr(states), _adr(ws), wsb)
+    hT = lam.new_empty((N, H, D))
+    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device) if wsb else None
+    _call("dn_glr_fwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, x.data_ptr(), r.data_ptr(), i.data_ptr(),
+          lam.data_ptr(), _adr(br), _adr(bi), power, _adr(h0), _adr(cu_seqlens), y.data_ptr(), hT.data_ptr(), _adr(states),
+          _adr(ws), wsb)
     return y, hT
 
 
@@ -1034,18 +1056,22 @@ def glr_bwd(x, r, i, lam, br, bi, h0, dy, dhT=None, cu_seqlens=None, power: floa
     filled (None: computed again).  Returns a dict: dx, dr, di in x's dtype,
     dlam, dbr, dbi (None without the bias) and dh0 in float32; rows behind the
     last packed sequence are zero."""
-    dev, (B, T), H, D, N = _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
+    fits, dev, xs, N = _glr_fits(x, r, i, lam, br, bi, h0, cu_seqlens)
+    if not fits:
+        _glr_args(x, r, i, lam, br, bi, h0, cu_seqlens, 4)
+    B, T, H, D = xs
     _given(dy=dy)
-    _is(dy, "dy", x.dtype, tuple(x.shape), dev)
-    _is(dhT, "dhT", torch.float32, (N, H, D), dev)
-    _glr_states(states, B, T, H, D, dev)
-    gr = dict(dx=torch.empty_like(x), dr=torch.empty_like(r), di=torch.empty_like(i), dlam=torch.empty_like(lam),
-              dbr=None if br is None else torch.empty_like(br), dbi=None if bi is None else torch.empty_like(bi),
-              dh0=torch.empty((N, H, D), dtype=torch.float32, device=dev))
-    wsb = load_library().dn_glr_bwd_workspace(B, T, H, D, states is not None)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_glr_bwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, _adr(x), _adr(r), _adr(i), _adr(lam), _adr(br),
-          _adr(bi), float(power), _adr(h0), _adr(cu_seqlens), _adr(states), _adr(dy), _adr(dhT),
+    _is(dy, "dy", x.dtype, xs, x.device)
+    _is(dhT, "dhT", torch.float32, (N, H, D), x.device)
+    rows, _, given, none = _glr_sizes(B, T, H, D)
+    _is(states, "states", torch.float32, (rows, H, D), x.device)
+    gr = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=torch.empty_like(x), dlam=torch.empty_like(lam),
+              dbr=None if br is None else torch.empty_like(lam), dbi=None if bi is None else torch.empty_like(lam),
+              dh0=lam.new_empty((N, H, D)))
+    wsb = none if states is None else given
+    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device) if wsb else None
+    _call("dn_glr_bwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, x.data_ptr(), r.data_ptr(), i.data_ptr(),
+          lam.data_ptr(), _adr(br), _adr(bi), power, _adr(h0), _adr(cu_seqlens), _adr(states), dy.data_ptr(), _adr(dhT),
           *[_adr(g) for g in gr.values()], _adr(ws), wsb)
     return gr
 
@@ -1127,6 +1153,19 @@ def _dropped(p, seed, dev):
     return round(p * 65536) > 0
 
 
+def _add_norm_fits(x, residual, w):
+    """(whether the arguments are right, device index, rows, D, residual's dtype), in as few steps as possible;
+    residual and w may be None."""
+    try:
+        E, dev, xs, f32 = x.dtype, x.get_device(), x.shape, torch.float32
+        R, D = E if residual is None else residual.dtype, xs[-1]
+        return (len(xs) < 9 and 0 < D <= _MAX_SIZE and E in _DTYPES and dev >= 0 and x.is_contiguous()
+                and (residual is None or ((R is E or R is f32) and _fits(residual, R, xs, dev)))
+                and (w is None or _fits(w, f32, xs[-1:], dev))), dev, x.numel() // (D or 1), D, R
+    except (AttributeError, IndexError):  # not a tensor, no dimensions
+        return False, None, None, None, None
+
+
 def add_norm(x, residual, w, eps: float = 1e-5, p: float = 0.0, seed=None):
     """The residual's addition with dropout and root-mean-square norm over the last
     dimension (``dn_add_norm``): ``h = residual + dropout(x)``, ``y = h /
@@ -1137,13 +1176,15 @@ def add_norm(x, residual, w, eps: float = 1e-5, p: float = 0.0, seed=None):
     depends on it and a value's place alone and is not stored.  Returns ``(y, h)``:
     y in x's dtype, h in the residual's (x itself where nothing is added or
     dropped)."""
-    dev, rows, D, R = _add_norm_args(x, residual, w)
     _given(w=w)
-    drop = _dropped(p, seed, dev)
+    fits, dev, rows, D, R = _add_norm_fits(x, residual, w)
+    if not fits:
+        _add_norm_args(x, residual, w)
+    drop = p != 0 and _dropped(p, seed, x.device)
     y = torch.empty_like(x)
-    h = torch.empty_like(x, dtype=R) if residual is not None or drop else None
-    _call("dn_add_norm", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], _adr(x), _adr(residual), _adr(w), eps, p,
-          _adr(seed) if drop else None, _adr(y), _adr(h))
+    h = torch.empty_like(x if residual is None else residual) if residual is not None or drop else None
+    _call("dn_add_norm", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], x.data_ptr(), _adr(residual), w.data_ptr(), eps, p,
+          seed.data_ptr() if drop else None, y.data_ptr(), _adr(h))
     return y, x if h is None else h
 
 
@@ -1152,17 +1193,19 @@ def add_norm_bwd(h, w, dy, dh=None, eps: float = 1e-5, p: float = 0.0, seed=None
     dh in h's (the gradient of h itself; None: 0), with the forward call's p and
     seed: ``(dx, dres, dw)``, dx in x's dtype (dres itself where nothing is dropped
     and the types agree), dres in h's, dw float32."""
-    _given(h=h)
-    dev, rows, D, R = _add_norm_args(dy, h, w)
-    _given(w=w)
-    drop = _dropped(p, seed, dev)
-    _is(dh, "dh", R, tuple(h.shape), dev)
+    _given(h=h, w=w)
+    fits, dev, rows, D, R = _add_norm_fits(dy, h, w)
+    if not fits:
+        _add_norm_args(dy, h, w)
+    drop = p != 0 and _dropped(p, seed, dy.device)
+    _is(dh, "dh", R, h.shape, dy.device)
     dres, dw = torch.empty_like(h), torch.empty_like(w)
     dx = torch.empty_like(dy) if drop or R is not dy.dtype else None
     wsb = load_library().dn_add_norm_bwd_workspace(rows, D)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _call("dn_add_norm_bwd", dev, rows, D, _DTYPES[dy.dtype], _DTYPES[R], _adr(h), _adr(w), eps, p,
-          _adr(seed) if drop else None, _adr(dy), _adr(dh), _adr(dx), _adr(dres), _adr(dw), _adr(ws), wsb)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dy.device)
+    _call("dn_add_norm_bwd", dev, rows, D, _DTYPES[dy.dtype], _DTYPES[R], h.data_ptr(), w.data_ptr(), eps, p,
+          seed.data_ptr() if drop else None, dy.data_ptr(), _adr(dh), _adr(dx), dres.data_ptr(), dw.data_ptr(), ws.data_ptr(),
+          wsb)
     return dres if dx is None else dx, dres, dw
 
 
@@ -1198,16 +1241,37 @@ def norm8(x, residual=None, w=None, eps: float = 1e-5):
     scale y8`` with ``scale = max |y| / 448``.  Without w the sum itself is
     rounded: ``norm8(weight)[:2]`` gives ``linear8`` its weights.  h as
     ``add_norm`` returns it."""
-    dev, rows, D, R = _add_norm_args(x, residual, w)
+    fits, dev, rows, D, R = _add_norm_fits(x, residual, w)
+    if not fits:
+        _add_norm_args(x, residual, w)
     y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    h = torch.empty_like(x, dtype=R) if residual is not None else None
-    _call("dn_norm8", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], _adr(x), _adr(residual), _adr(w), eps, _adr(y), _adr(scale),
-          _adr(h))
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    h = None if residual is None else torch.empty_like(residual)
+    _call("dn_norm8", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], x.data_ptr(), _adr(residual), _adr(w), eps, y.data_ptr(),
+          scale.data_ptr(), _adr(h))
     return y, scale, x if h is None else h
 
 
 _ACTS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _linear8_args(x, xs, w, ws, bias, residual, act):
+    """Says what is wrong with the arguments of ``linear8``."""
+    if act not in _ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(_ACTS))
+    E = torch.float8_e4m3fn
+    dev = _gpu(x, "x", tuple(range(1, 9)), (E,))
+    _gpu(w, "w", (2,), (E,))
+    _given(xs=xs, ws=ws)
+    lead, N = tuple(x.shape[:-1]), w.shape[0]
+    _is(x, "x", E, tuple(x.shape), dev)
+    _is(w, "w", E, (N, x.shape[-1]), dev)
+    _is(xs, "xs", torch.float32, lead, dev)
+    _is(ws, "ws", torch.float32, (N,), dev)
+    _is(bias, "bias", torch.float32, (N,), dev)
+    _is(residual, "residual", torch.bfloat16, lead + (N,), dev)
+    if xs.numel() > _MAX_SIZE:
+        raise ValueError("x has 2^31 rows or more")
 
 
 def linear8(x, xs, w, ws, bias=None, residual=None, act: str = "none"):
@@ -1217,23 +1281,18 @@ def linear8(x, xs, w, ws, bias=None, residual=None, act: str = "none"):
     16; bias ``[N]`` float32 or None; residual ``[..., N]`` bfloat16 or None; act
     "none", "silu" or "gelu" (with the normal distribution's integral).  Returns y
     ``[..., N]`` bfloat16."""
-    if act not in _ACTS:
-        raise ValueError("act must be one of %s" % ", ".join(_ACTS))
-    E = torch.float8_e4m3fn
-    dev = _gpu(x, "x", tuple(range(1, 9)), (E,))
-    _gpu(w, "w", (2,), (E,))
-    _given(xs=xs, ws=ws)
-    lead, K, N = tuple(x.shape[:-1]), x.shape[-1], w.shape[0]
-    _is(x, "x", E, tuple(x.shape), dev)
-    _is(w, "w", E, (N, K), dev)
-    _is(xs, "xs", torch.float32, lead, dev)
-    _is(ws, "ws", torch.float32, (N,), dev)
-    _is(bias, "bias", torch.float32, (N,), dev)
-    _is(residual, "residual", torch.bfloat16, lead + (N,), dev)
-    y = torch.empty(lead + (N,), dtype=torch.bfloat16, device=dev)
-    M = xs.numel()
-    if M > _MAX_SIZE:
-        raise ValueError("x has 2^31 rows or more")
-    _call("dn_linear8", dev, M, N, K, x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), _adr(bias), _adr(residual),
-          _ACTS[act], y.data_ptr())
+    try:  # the usual call in one expression; anything else goes through the checks that say what is wrong
+        xd, wd, dev, E, f32 = x.shape, w.shape, x.get_device(), torch.float8_e4m3fn, torch.float32
+        lead, N = xd[:-1], wd[0]
+        fits = (dev >= 0 and 0 < len(xd) < 9 and x.dtype is E and x.is_contiguous() and _fits(w, E, (N, xd[-1]), dev)
+                and _fits(xs, f32, lead, dev) and _fits(ws, f32, wd[:1], dev) and (bias is None or _fits(bias, f32, wd[:1], dev))
+                and (residual is None or _fits(residual, torch.bfloat16, lead + wd[:1], dev)) and act in _ACTS
+                and xs.numel() <= _MAX_SIZE and N <= _MAX_SIZE and xd[-1] <= _MAX_SIZE)
+    except (AttributeError, IndexError, TypeError):  # not a tensor
+        fits = False
+    if not fits:
+        _linear8_args(x, xs, w, ws, bias, residual, act)
+    y = torch.empty(lead + wd[:1], dtype=torch.bfloat16, device=x.device)
+    _call("dn_linear8", dev, xs.numel(), N, xd[-1], x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), _adr(bias),
+          _adr(residual), _ACTS[act], y.data_ptr())
     return y

@@ -29,6 +29,7 @@
 
 #include "dn_internal.h"
 #include "dn_rows.h"
+#include "dn_ssm.h"
 
 namespace dn {
 
@@ -69,8 +70,7 @@ struct GlrStepParams {
   const float *lam, *br, *bi;
   float *state;
   void *y;
-  int64_t n;  // B C
-  int C;
+  int B, C;
   float power;
 };
 hipError_t launch_glr_step(const GlrStepParams &p, int dtype, hipStream_t stream);
@@ -93,15 +93,13 @@ __device__ __forceinline__ typename Pair<E>::type to_e2(f32x2 v) {
   else return v;
 }
 
-__device__ __forceinline__ float glr_softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
 // What a channel's gates need: log2 of the decay at an open gate, and the biases
 // in units of -log2 e.
 struct GlrChannel {
   float k2, br, bi;
 };
 __device__ __forceinline__ GlrChannel glr_channel(const float *lam, const float *br, const float *bi, float power, int c) {
-  return {-power * GLR_LOG2E * glr_softplus(lam[c]), br ? -GLR_LOG2E * br[c] : 0.f, bi ? -GLR_LOG2E * bi[c] : 0.f};
+  return {-power * GLR_LOG2E * softplus(lam[c]), br ? -GLR_LOG2E * br[c] : 0.f, bi ? -GLR_LOG2E * bi[c] : 0.f};
 }
 
 // sigmoid(z + bias), bias in units of -log2 e

@@ -209,8 +209,8 @@ extern "C" dn_status dn_glr_step(int32_t B, int32_t H, int32_t D, int32_t dtype,
   if (st != DN_OK) return st;
   if (dtype & DN_ZERO_TAIL) return DN_EINVAL;
   if (!x || !r || !i || !lam || !state || !y || !all16({x, r, i, state, y})) return DN_EINVAL;
-  const int64_t n = (int64_t)B * H * D;
-  if (n / 4 > UINT32_MAX - 256) return DN_EUNSUPPORTED;
+  // a grid's rows, and fewer than 2^32 threads
+  if (B > 65535 * 4 || ((int64_t)H * D / 4 + 255) / 256 * B > UINT32_MAX / 256) return DN_EUNSUPPORTED;
   dn::GlrStepParams p = {};
   p.x = x;
   p.r = r;
@@ -220,7 +220,7 @@ extern "C" dn_status dn_glr_step(int32_t B, int32_t H, int32_t D, int32_t dtype,
   p.bi = bi;
   p.state = state;
   p.y = y;
-  p.n = n;
+  p.B = B;
   p.C = H * D;
   p.power = power;
   return dn::launch_glr_step(p, dtype, stream) == hipSuccess ? DN_OK : DN_EHIP;

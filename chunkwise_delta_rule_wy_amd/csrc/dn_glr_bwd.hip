@@ -236,7 +236,7 @@ __global__ __launch_bounds__(ROW_THREADS) void glr_param_kernel(GlrParams p) {
   if (which == 0) {
     // sigmoid(lam) / softplus(lam) is 1 to fp32's last digit where e^lam is below 2^-24
     const float lam = p.lam[c];
-    p.dlam[c] = lam < -20.f ? a : a / ((1.f + expf(-lam)) * glr_softplus(lam));
+    p.dlam[c] = lam < -20.f ? a : a / ((1.f + expf(-lam)) * softplus(lam));
   } else if (which == 1) {
     if (p.dbr) p.dbr[c] = a;
   } else if (p.dbi) {

@@ -204,27 +204,43 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
   }
 }
 
-template <typename E>
-__global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
-  constexpr int V = 4;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-  if (at >= p.n) return;
+// One token: a thread takes four channels of ROWS sequences, whose gates' constants
+// it computes once.
+constexpr int STEP_THREADS = 256;
+
+template <typename E, int ROWS>
+__global__ __launch_bounds__(STEP_THREADS) void glr_step_kernel(GlrStepParams p) {
   typedef typename four<E>::type E4;
-  const E4 x = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.x) + at);
-  const E4 r = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.r) + at);
-  const E4 i = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.i) + at);
-  f32x4 h = *reinterpret_cast<const f32x4 *>(p.state + at);
-  const int c = (int)(at % p.C);
-  E4 y;
+  const int c = (blockIdx.x * STEP_THREADS + threadIdx.x) * 4, b0 = blockIdx.y * ROWS;
+  if (c >= p.C) return;
+  E4 x[ROWS], r[ROWS], i[ROWS];
+  f32x4 h[ROWS];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const GlrChannel k = glr_channel(p.lam, p.br, p.bi, p.power, c + e);
-    const float l2 = k.k2 * glr_sigmoid(to_f<E>(r[e]), k.br), a = __builtin_amdgcn_exp2f(l2);
-    h[e] = __builtin_fmaf(a, h[e], __builtin_amdgcn_sqrtf(glr_rest(a, l2)) * glr_sigmoid(to_f<E>(i[e]), k.bi) * to_f<E>(x[e]));
-    y[e] = to_e<E>(h[e]);
+  for (int j = 0; j < ROWS; ++j) {
+    const size_t at = (size_t)min(b0 + j, p.B - 1) * p.C + c;
+    x[j] = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.x) + at);
+    r[j] = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.r) + at);
+    i[j] = *reinterpret_cast<const E4 *>(static_cast<const E *>(p.i) + at);
+    h[j] = *reinterpret_cast<const f32x4 *>(p.state + at);
   }
-  *reinterpret_cast<f32x4 *>(p.state + at) = h;
-  *reinterpret_cast<E4 *>(static_cast<E *>(p.y) + at) = y;
+  GlrChannel k[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) k[e] = glr_channel(p.lam, p.br, p.bi, p.power, c + e);
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+    if (b0 + j >= p.B) break;
+    const size_t at = (size_t)(b0 + j) * p.C + c;
+    E4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float l2 = k[e].k2 * glr_sigmoid(to_f<E>(r[j][e]), k[e].br), a = __builtin_amdgcn_exp2f(l2);
+      const float u = glr_sigmoid(to_f<E>(i[j][e]), k[e].bi) * to_f<E>(x[j][e]);
+      h[j][e] = __builtin_fmaf(a, h[j][e], __builtin_amdgcn_sqrtf(glr_rest(a, l2)) * u);
+      y[e] = to_e<E>(h[j][e]);
+    }
+    *reinterpret_cast<f32x4 *>(p.state + at) = h[j];
+    *reinterpret_cast<E4 *>(static_cast<E *>(p.y) + at) = y;
+  }
 }
 
 }  // namespace
@@ -254,10 +270,20 @@ hipError_t launch_glr_fwd(const GlrParams &p, int dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Four sequences a thread where single ones would give the CUs two workgroups and more
+// (4096 channels in bf16, 256 sequences: 6.0 us, single 8.2, eight 7.2; 64 sequences: 5.0 us,
+// single 4.1).
 hipError_t launch_glr_step(const GlrStepParams &p, int dtype, hipStream_t st) {
-  const dim3 grid((unsigned)((p.n / 4 + 255) / 256)), thr(256);
-  if (dtype == 1) hipLaunchKernelGGL(glr_step_kernel<bf16>, grid, thr, 0, st, p);
-  else hipLaunchKernelGGL(glr_step_kernel<float>, grid, thr, 0, st, p);
+  const int64_t cols = (p.C / 4 + STEP_THREADS - 1) / STEP_THREADS;
+  const bool many = cols * p.B >= 512;
+  const dim3 grid((unsigned)cols, (unsigned)(many ? (p.B + 3) / 4 : p.B)), thr(STEP_THREADS);
+  if (dtype == 1) {
+    if (many) hipLaunchKernelGGL((glr_step_kernel<bf16, 4>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_step_kernel<bf16, 1>), grid, thr, 0, st, p);
+  } else {
+    if (many) hipLaunchKernelGGL((glr_step_kernel<float, 4>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((glr_step_kernel<float, 1>), grid, thr, 0, st, p);
+  }
   return hipGetLastError();
 }
 
