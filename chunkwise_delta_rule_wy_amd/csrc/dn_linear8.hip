@@ -280,42 +280,65 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   }
 }
 
-// Few rows: 16 columns a workgroup, blocks of 128 indices dealt to the waves.
-constexpr int FEW_WAVES = 8, FEW_BATCH = 4;
+// Few rows: 16 columns a workgroup, whose waves take a contiguous part of the indices
+// each, in blocks of 128.  The blocks pass through the wave's own part of LDS, two
+// at a time and without barriers, as in the tiles: a load into registers would touch
+// 16 rows at once, which takes twice the time for the same bytes (64 x 4096 x 4096:
+// 12.3 us).
+constexpr int FEW_WAVES = 8;
 
 template <int MT>
 __global__ __launch_bounds__(64 * FEW_WAVES) void linear8_few_kernel(Linear8Params p) {
-  __shared__ float part[FEW_WAVES][16 * MT][20];
-  const int lane = lane_id(), wave = wave_id(), row = lane & 15, off = 32 * (lane >> 4);
+  constexpr int BLOCK = 16 * (1 + MT) * BK, PIECES = 2 * (1 + MT);
+  constexpr int PART = FEW_WAVES * 16 * MT * 20 * 4, LDS = 2 * FEW_WAVES * BLOCK > PART ? 2 * FEW_WAVES * BLOCK : PART;
+  __shared__ __attribute__((aligned(256))) char lds[LDS];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), row = lane & 15, unit = 2 * (lane >> 4);
+  const uint32_t base = (uint32_t)(size_t)(__attribute__((address_space(3))) char *)lds + wave * 2 * BLOCK;
   const int n0 = blockIdx.x * 16;
-  const uint8_t *w = p.w + (size_t)min(n0 + row, p.N - 1) * p.K + off;
-  const uint8_t *x[MT];
+  // eight rows a piece: two pieces of w, then those of x
+  uint32_t src[PIECES];
+  const uint8_t *w0 = p.w + (size_t)n0 * p.K;
+  const auto from = [&](int j) { return (lane & 7) ^ ((4 * j + (lane >> 4)) & 7); };  // the unit that lands at lane % 8
 #pragma unroll
-  for (int b = 0; b < MT; ++b) x[b] = p.x + (size_t)min(16 * b + row, p.M - 1) * p.K + off;
-  const auto get = [&](const uint8_t *src, int k) {
-    i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-    if (k + off < p.K) lo = *reinterpret_cast<const i32x4 *>(src + k);
-    if (k + off + 16 < p.K) hi = *reinterpret_cast<const i32x4 *>(src + k + 16);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  for (int j = 0; j < PIECES; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    src[j] = (uint32_t)(j < 2 ? min(r, p.N - 1 - n0) : min(r - 16, p.M - 1)) * (uint32_t)p.K + from(j) * 16;
+  }
+  const auto load = [&](int k, int stage) {
+    const bool whole = k + BK <= p.K;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const uint8_t *at = (j < 2 ? w0 : p.x) + k;
+      const uint32_t to = base + stage * BLOCK + j * 1024;
+      if (whole) wy::dma16s(at, src[j], to);
+      else wy::dma16(k + from(j) * 16 < p.K ? (const void *)(at + src[j]) : (const void *)&g_zero16, to);
+    }
   };
+  const int blocks = (p.K + BK - 1) / BK, per = (blocks + FEW_WAVES - 1) / FEW_WAVES;
+  const int first = wave * per, end = min(first + per, blocks);
   f32x4 acc[MT];
 #pragma unroll
   for (int b = 0; b < MT; ++b) acc[b] = zero4();
-  for (int k = wave * BK; k < p.K; k += FEW_BATCH * FEW_WAVES * BK) {
-    i32x8 fw[FEW_BATCH], fx[FEW_BATCH][MT];
+  if (first < end) load(first * BK, 0);
+  if (first + 1 < end) load((first + 1) * BK, 1);
+  for (int t = first; t < end; ++t) {
+    if (t + 1 < end) wy::wait_vm<PIECES>();
+    else wy::wait_vm<0>();
+    asm volatile("" ::: "memory");  // no read before the wait
+    const uint32_t at = base + ((t - first) & 1) * BLOCK;
+    const i32x8 fw = operand(at, row, unit);
+    i32x8 fx[MT];
 #pragma unroll
-    for (int j = 0; j < FEW_BATCH; ++j) {
-      fw[j] = get(w, k + j * FEW_WAVES * BK);
+    for (int b = 0; b < MT; ++b) fx[b] = operand(at + 16 * BK, 16 * b + row, unit);
+    wave_lds_fence();
+    if (t + 2 < end) load((t + 2) * BK, (t - first) & 1);
 #pragma unroll
-      for (int b = 0; b < MT; ++b) fx[j][b] = get(x[b], k + j * FEW_WAVES * BK);
-    }
-#pragma unroll
-    for (int j = 0; j < FEW_BATCH; ++j)
-#pragma unroll
-      for (int b = 0; b < MT; ++b)
-        acc[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fx[j][b], acc[b], 0, 0, 0, 0, 0, 0);
+    for (int b = 0; b < MT; ++b)
+      acc[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx[b], acc[b], 0, 0, 0, 0, 0, 0);
   }
   mfma_settle();
+  __syncthreads();
+  float (*part)[16 * MT][20] = reinterpret_cast<float (*)[16 * MT][20]>(lds);
 #pragma unroll
   for (int b = 0; b < MT; ++b) *reinterpret_cast<f32x4 *>(&part[wave][16 * b + row][4 * (lane >> 4)]) = acc[b];
   __syncthreads();
