@@ -71,10 +71,10 @@ __device__ __forceinline__ i32x8 operand(uint32_t tile, int row, int unit) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int TM, int TN, int WM, int WN, int ACT>
+template <int TM, int TN, int WM, int WN, int RING, int ACT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kernel(Linear8Params p) {
   constexpr int WAVES = (TM / WM) * (TN / WN), STAGE = (TM + TN) * BK, NM = WM / 32, NN = WN / 32;
-  __shared__ __attribute__((aligned(256))) char lds[2 * STAGE];
+  __shared__ __attribute__((aligned(256))) char lds[RING * STAGE];
   __shared__ f32x2 cols[TN];  // (ws, bias) of a tile's columns
   const uint32_t base = (uint32_t)(size_t)(__attribute__((address_space(3))) char *)lds;
   const int lane = lane_id(), wave = wave_id();
@@ -172,25 +172,64 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
     for (int b = 0; b < NM; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
-  wy::wait_vm<0>();
-  __syncthreads();
-  if (blocks > 1) {
+  int at = 0, last;  // the last block's place
+  if constexpr (RING == 2) {
+    wy::wait_vm<0>();
+    __syncthreads();
+    if (blocks > 1) {
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) load(j, BK, 1, p.K < 2 * BK);
-  }
+      for (int j = 0; j < PIECES; ++j) load(j, BK, 1, p.K < 2 * BK);
+    }
 #pragma unroll
-  for (int o = 0; o < OPERANDS; ++o) read(0, o, 0);
-  int at = 0;
-  for (; at + 2 < blocks - ragged; ++at) turn(std::integral_constant<int, FULL>(), at * BK, at & 1);
-  if (at + 2 < blocks) {
-    turn(std::integral_constant<int, TAIL>(), at * BK, at & 1);
-    ++at;
+    for (int o = 0; o < OPERANDS; ++o) read(0, o, 0);
+    for (; at + 2 < blocks - ragged; ++at) turn(std::integral_constant<int, FULL>(), at * BK, at & 1);
+    if (at + 2 < blocks) {
+      turn(std::integral_constant<int, TAIL>(), at * BK, at & 1);
+      ++at;
+    }
+    if (at + 1 < blocks) {
+      turn(std::integral_constant<int, NEXT>(), at * BK, at & 1);
+      ++at;
+    }
+    turn(std::integral_constant<int, LAST>(), at * BK, at & 1);
+    last = at & 1;
+  } else {
+    // Small tiles: a block's products take far less than its loads, which are started
+    // RING - 1 blocks ahead, and several workgroups of a CU fill each other's waits.
+#pragma unroll
+    for (int k = 1; k < RING - 1; ++k)
+      if (k < blocks) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) load(j, k * BK, k, (k + 1) * BK > p.K);
+      }
+    for (int stage = 0; at < blocks; ++at) {
+      if (at + RING - 2 < blocks) wy::wait_vm<(RING - 2) * PIECES>();
+      else wy::wait_vm<0>();
+      __syncthreads();
+#pragma unroll
+      for (int o = 0; o < OPERANDS; ++o) {
+        read(0, o, stage);
+        read(1, o, stage);
+      }
+      const int ahead = at + RING - 1, to = stage == 0 ? RING - 1 : stage - 1;  // the place of the block before
+      if (ahead < blocks) {
+        if ((ahead + 1) * BK <= p.K) {
+#pragma unroll
+          for (int j = 0; j < PIECES; ++j) load(j, ahead * BK, to, false);
+        } else {
+#pragma unroll
+          for (int j = 0; j < PIECES; ++j) load(j, ahead * BK, to, true);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PRODUCTS; ++i) {
+        product(0, i);
+        product(1, i);
+      }
+      last = stage;
+      stage = stage == RING - 1 ? 0 : stage + 1;
+    }
   }
-  if (at + 1 < blocks) {
-    turn(std::integral_constant<int, NEXT>(), at * BK, at & 1);
-    ++at;
-  }
-  turn(std::integral_constant<int, LAST>(), at * BK, at & 1);
 
   // Epilogue, in the place of the last block: ROUND times 32 rows m are finished
   // in the registers, where a lane has four neighbouring columns of one row, and
@@ -200,7 +239,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   constexpr int PITCH = 2 * WN, UNITS = PITCH / 16, PART = STAGE / WAVES;
   constexpr int ROUND = PART / (32 * PITCH) < NM ? PART / (32 * PITCH) : NM;
   static_assert(ROUND > 0 && NM % ROUND == 0, "a wave's part holds 32 rows at least");
-  const uint32_t part = base + (at & 1) * STAGE + wave * PART;
+  const uint32_t part = base + last * STAGE + wave * PART;
   const auto swizzle = [](int r) { return r / (256 / PITCH) % UNITS; };
   const int nw = n0 + wn;
   const bool whole = (p.N & 7) == 0;  // rows of y start at 16-byte units
@@ -261,19 +300,19 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
         __builtin_amdgcn_sched_barrier(0);
       }
     wave_lds_fence();
+    if (whole) {
 #pragma unroll 4
-    for (int r0 = 0; r0 < 32 * ROUND; r0 += STEP) {
-      const int r = r0 + lane / UNITS, m = mb + r, n = nw + 8 * u;
-      const u32x4 v = wy::ld<u32x4>(part + r * PITCH + ((u ^ swizzle(r)) << 4));
-      if (m >= p.M || n >= p.N) continue;
-      bf16 *out = p.y + (size_t)m * p.N + n;
-      if (whole) {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out));
-      } else {
-        const bf16x8 h = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < p.N) out[e] = h[e];
+      for (int r0 = 0; r0 < 32 * ROUND; r0 += STEP) {
+        const int r = r0 + lane / UNITS, m = mb + r, n = nw + 8 * u;
+        const u32x4 v = wy::ld<u32x4>(part + r * PITCH + ((u ^ swizzle(r)) << 4));
+        if (m < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p.y + (size_t)m * p.N + n));
+      }
+    } else {  // one column a lane
+#pragma unroll 4
+      for (int o = lane; o < 32 * ROUND * WN; o += 64) {
+        const int r = o / WN, n = o % WN;
+        const bf16 v = wy::ld<bf16>(part + r * PITCH + (((n >> 3) ^ swizzle(r)) << 4) + 2 * (n & 7));
+        if (mb + r < p.M && nw + n < p.N) p.y[(size_t)(mb + r) * p.N + nw + n] = v;
       }
     }
     wave_lds_fence();
@@ -359,15 +398,15 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void linear8_few_kernel(Linear8Para
 
 // ------------------------------------------------------------------- host
 
-template <int TM, int TN, int WM, int WN>
+template <int TM, int TN, int WM, int WN, int RING>
 hipError_t launch_tile(Linear8Params &p, hipStream_t st) {
   p.tm = (p.M + TM - 1) / TM;
   p.tn = (p.N + TN - 1) / TN;
   const int64_t tiles = (int64_t)p.tm * p.tn;
   const dim3 grid((unsigned)tiles), thr(64 * (TM / WM) * (TN / WN));
-  if (p.act == ACT_SILU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_SILU>), grid, thr, 0, st, p);
-  else if (p.act == ACT_GELU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_GELU>), grid, thr, 0, st, p);
-  else hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, ACT_NONE>), grid, thr, 0, st, p);
+  if (p.act == ACT_SILU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, RING, ACT_SILU>), grid, thr, 0, st, p);
+  else if (p.act == ACT_GELU) hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, RING, ACT_GELU>), grid, thr, 0, st, p);
+  else hipLaunchKernelGGL((linear8_tile_kernel<TM, TN, WM, WN, RING, ACT_NONE>), grid, thr, 0, st, p);
   return hipGetLastError();
 }
 
@@ -384,9 +423,9 @@ hipError_t launch(Linear8Params &p, hipStream_t st) {
   if (p.M <= 32) return launch_few<2>(p, st);
   if (p.M <= 64) return launch_few<4>(p, st);
   // the largest tiles that give the 256 CUs one each
-  if (tiles(p, 256) >= 256) return launch_tile<256, 256, 128, 128>(p, st);
-  if (tiles(p, 128) >= 256) return launch_tile<128, 128, 64, 64>(p, st);
-  return launch_tile<64, 64, 32, 32>(p, st);
+  if (tiles(p, 256) >= 256) return launch_tile<256, 256, 128, 128, 2>(p, st);
+  if (tiles(p, 128) >= 256) return launch_tile<128, 128, 64, 64, 2>(p, st);
+  return launch_tile<64, 64, 32, 32, 4>(p, st);
 }
 
 }  // namespace
