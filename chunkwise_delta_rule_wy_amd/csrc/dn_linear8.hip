@@ -237,7 +237,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
   // stored.  A residual comes into that place first, by direct loads.  16-byte
   // units of a row are stored at unit ^ swizzle(row).
   constexpr int PITCH = 2 * WN, UNITS = PITCH / 16, PART = STAGE / WAVES;
-  constexpr int ROUND = PART / (32 * PITCH) < NM ? PART / (32 * PITCH) : NM;
+  constexpr int FIT = PART / (32 * PITCH), ROUND = FIT >= NM ? NM : FIT >= 2 ? 2 : FIT;
   static_assert(ROUND > 0 && NM % ROUND == 0, "a wave's part holds 32 rows at least");
   const uint32_t part = base + last * STAGE + wave * PART;
   const auto swizzle = [](int r) { return r / (256 / PITCH) % UNITS; };
@@ -416,15 +416,23 @@ hipError_t launch_few(const Linear8Params &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-int64_t tiles(const Linear8Params &p, int t) { return (int64_t)((p.M + t - 1) / t) * ((p.N + t - 1) / t); }
+// The tiles by their measured times: `first` for up to 256 of them, one for each CU, and
+// `more` for every 256 beyond (tenths of us over 4096 indices).
+int64_t cost(const Linear8Params &p, int t, int first, int more) {
+  const int64_t n = (int64_t)((p.M + t - 1) / t) * ((p.N + t - 1) / t), rounds = (n + 255) / 256;
+  return rounds <= 1 ? first : more * rounds;
+}
 
 hipError_t launch(Linear8Params &p, hipStream_t st) {
   if (p.M <= 16) return launch_few<1>(p, st);
   if (p.M <= 32) return launch_few<2>(p, st);
   if (p.M <= 64) return launch_few<4>(p, st);
-  // the largest tiles that give the 256 CUs one each
-  if (tiles(p, 256) >= 256) return launch_tile<256, 256, 128, 128, 2>(p, st);
-  if (tiles(p, 128) >= 256) return launch_tile<128, 128, 64, 64, 2>(p, st);
+  // In us over 4096 indices with tiles of 64, 128 and 256: 256 x 4096 12.6, 17.9, 43.6; 768 x
+  // 4096 24.8, 20.2, 44.3; 3000 x 4096 81.8, 50.4, 52.1; 4096 x 4096 118, 65.6, 56.8; 4096 x 4097
+  // 126, 83.6, 126.
+  const int64_t small = cost(p, 64, 126, 70), medium = cost(p, 128, 190, 165), large = cost(p, 256, 560, 560);
+  if (large <= medium && large <= small) return launch_tile<256, 256, 128, 128, 2>(p, st);
+  if (medium <= small) return launch_tile<128, 128, 64, 64, 2>(p, st);
   return launch_tile<64, 64, 32, 32, 4>(p, st);
 }
 

@@ -56,6 +56,20 @@ def test_large_tiles(M, N, K, residual):
     run(M, N, K, "silu", True, residual, 2)
 
 
+# 256 tiles of 256 x 256 and fewer, which are taken whole by the largest kind; K of one to four blocks of 128 indices and parts
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 272, 400, 512])
+@pytest.mark.parametrize("M,N,residual", [(4090, 4000, True), (3999, 4091, True), (4096, 4096, False)])
+def test_largest_tiles(M, N, K, residual):
+    run(M, N, K, "gelu" if residual else "none", residual, residual, 3)
+
+
+# the middle kind and the smallest with the same parts
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 272, 400, 512, 528])
+@pytest.mark.parametrize("M,N", [(1030, 4090), (1030, 4088), (300, 1001), (300, 1000)])
+def test_smaller_tiles(M, N, K):
+    run(M, N, K, "none", False, True, 4)
+
+
 def test_whole_numbers_are_exact():
     # small whole numbers: the sums are whole, below 2^8 and so in bf16
     for M, N, K in ((3, 24, 160), (70, 72, 160), (2100, 2100, 144), (4200, 4200, 144)):
