@@ -169,12 +169,19 @@ def norm_bounds(h, w, eps, dtype, res_dtype, dy, dh, keep):
 
 
 def linear8(x, xs, w, ws, bias, residual, act):
-    """float64 y, and a bound: half a step of bf16, fp32's few roundings, and the matrix instructions' sums.  Those align
-    a block's products to the largest one; 2^-17 of the sum of absolute products covers a cut 20 bits below it."""
+    """float64 y, and a bound: half a step of bf16, fp32's few roundings, and what the matrix instructions cut.  These
+    align eight neighbouring products to the largest one and cut, towards zero, what lies 13 bits below its power of
+    two (test_gpu_linear8.py shows it), and add the eight to an fp32 sum.  So a group of eight is off by at most B = 7
+    x 2^-13 of its largest product, itself at most the product of the group's largest |x| and |w|.  The cuts take the
+    products' signs, which are as often one as the other: by Hoeffding's inequality groups that are independent are
+    off by 7.5 sqrt(sum B^2) together with a probability of 2 e^-28 at most."""
     p = x @ w.t()
     z = p * xs[:, None] * ws + (0 if bias is None else bias)
     y = z * torch.sigmoid(z) if act == "silu" else z * torch.special.ndtr(z) if act == "gelu" else z
     y = y if residual is None else y + residual
-    Ez = 2.0 ** -17 * (x.abs() @ w.abs().t()) * xs[:, None].abs() * ws.abs() + 4 * U * (z.abs() + (0 if bias is None else bias.abs()))
+    most = lambda t: t.abs().reshape(t.shape[0], -1, 8).amax(-1)  # noqa: E731
+    cut = 7 * 2.0 ** -13 * torch.minimum(most(x) @ most(w).t(), 7.5 * torch.sqrt(most(x) ** 2 @ (most(w) ** 2).t()))
+    Ez = (cut + U * (x.shape[1] // 8 + 2) * (x.abs() @ w.abs().t())) * xs[:, None].abs() * ws.abs() + 4 * U * (
+        z.abs() + (0 if bias is None else bias.abs()))
     # the activations' slope is at most 1.13, and their own error a few units of z
     return y, half(torch.bfloat16) * y.abs() + 1.2 * Ez + 24 * U * z.abs() * (1 + z.abs()) + 1e-37

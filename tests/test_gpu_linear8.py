@@ -80,6 +80,19 @@ def test_whole_numbers_are_exact():
         assert torch.equal(y.float().cpu(), x @ w.t())
 
 
+@pytest.mark.parametrize("M", [3, 80])
+def test_what_the_matrix_instructions_cut(M):
+    # 2^14 - 2^14 + 2^(14 - d): within eight neighbouring indices d = 13 is kept and d = 14 cut, beyond them 30 bits are kept
+    one = lambda n: torch.ones(n).cuda()  # noqa: E731
+    for place, d, want in ((2, 13, 2.0), (7, 13, 2.0), (2, 14, 0.0), (7, 14, 0.0), (16, 14, 1.0), (70, 22, 2.0 ** -8), (127, 30, 2.0 ** -16)):
+        x, w = torch.zeros(M, 128), torch.zeros(40, 128)
+        x[:, 0], x[:, 1], w[:, :2] = 128, -128, 128
+        e = 14 - d
+        x[:, place], w[:, place] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+        y = dn.linear8(x.to(E8).cuda(), one(M), w.to(E8).cuda(), one(40))
+        assert (y == want).all(), (place, d, y[0, 0].item())
+
+
 def test_padding_of_the_last_indices_is_not_read():
     # rows end inside a block of 128 indices; what lies behind them (the next row) is NaN
     for M in (4, 80):
