@@ -113,6 +113,46 @@ struct Row {
   }
 };
 
+// A row's units as they lie in memory, loaded ahead of their use.
+template <typename E, typename T, int LPR, int K>
+struct RawRow {
+  using RW = Row<E, LPR, K>;
+  static constexpr int U = Vec16<T>::N, PER = RW::V / U;
+  typename Vec16<T>::type v[K * PER];
+  // lanes behind the row's end repeat its first unit
+  __device__ __forceinline__ void load(const T *src, int lane, int D) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = RW::col(k, lane), at = c < D ? c : 0;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) v[k * PER + u] = *reinterpret_cast<const typename Vec16<T>::type *>(src + at + u * U);
+    }
+  }
+  __device__ __forceinline__ void get(int lane, int D, float (&x)[RW::N]) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < RW::V; ++e) x[k * RW::V + e] = RW::col(k, lane) < D ? to_f<T>(v[k * PER + e / U][e % U]) : 0.f;
+  }
+};
+
+// two sums over a row's lanes at once
+template <int LPR>
+__device__ __forceinline__ f32x2 lanes_sum2(f32x2 x, f32x2 (*buf)[ROW_THREADS / 64], int &turn) {
+  constexpr int L = LPR < 64 ? LPR : 64;
+  x = (f32x2){group_sum<L>(x[0]), group_sum<L>(x[1])};
+  if constexpr (LPR > 64) {
+    f32x2 *b = buf[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = (f32x2){0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < LPR / 64; ++i) x = (f32x2){x[0] + b[i][0], x[1] + b[i][1]};
+  }
+  return x;
+}
+
 // sum (or, with MAX, maximum) over a row's lanes; a row as wide as the workgroup
 // goes through LDS (two buffers taken in turn, one barrier a sum)
 template <int LPR, bool MAX = false>
