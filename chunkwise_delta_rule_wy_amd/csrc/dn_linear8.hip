@@ -448,9 +448,10 @@ extern "C" dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, 
                                 const float *ws, const float *bias, const void *residual, int32_t act, void *y,
                                 hipStream_t stream) {
   if (M < 0 || N <= 0 || K <= 0 || act < ACT_NONE || act > ACT_GELU) return DN_EINVAL;
-  // the rows' 16-byte units, a tile's 32-bit byte offsets, and the tiles' count
+  // the rows' 16-byte units, a tile's 32-bit byte offsets, and a grid's threads (fewer than
+  // 2^32), in tiles and in the few rows' 16 columns a workgroup
   if (K % 16 != 0 || K > 1 << 23) return DN_EUNSUPPORTED;
-  if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) > UINT32_MAX / 256 || N > INT32_MAX - 256 || M > INT32_MAX - 256)
+  if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) > UINT32_MAX / 256 || N > 1 << 26 || M > INT32_MAX - 256)
     return DN_EUNSUPPORTED;
   if (M == 0) return DN_OK;
   if (!x || !xs || !w || !ws || !y) return DN_EINVAL;

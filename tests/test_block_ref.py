@@ -187,6 +187,11 @@ def test_linear8_refuses(lib, kw, code):
     assert lib.dn_linear8(*{**a, **kw}.values()) == code
 
 
+@pytest.mark.parametrize("M", [1, 64, 65])
+def test_linear8_refuses_grids_of_too_many_threads(lib, M):
+    assert lib.dn_linear8(M, (1 << 26) + 1, 64, F, F, F, F, None, None, 0, F, None) == EUNSUPPORTED
+
+
 def test_python_refuses():
     x, w = torch.zeros(2, 3, 1, 8), torch.zeros(1, 8)
     for call in (lambda: dn.glr_fwd(x, x, x, w), lambda: dn.glr_bwd(x, x, x, w, None, None, None, x), lambda: dn.glr_scan(x, x, x, w),
