@@ -981,7 +981,7 @@ def gated_norm_fn(x, z, w, eps: float = 1e-5, gate_first: bool = False):
 
 
 def _glr_args(x, r, i, lam, br, bi, state, cu_seqlens, dims):
-    """(device, leading sizes, H, D, sequences), checked; state may be None."""
+    """Says what is wrong with the arguments of ``glr_fwd`` and its like."""
     dev = _gpu(x, "x", (dims,), tuple(_DTYPES))
     lead, (H, D) = tuple(x.shape[:-2]), x.shape[-2:]
     _given(r=r, i=i, lam=lam)
@@ -991,7 +991,6 @@ def _glr_args(x, r, i, lam, br, bi, state, cu_seqlens, dims):
     for t, name in ((lam, "lam"), (br, "br"), (bi, "bi")):
         _is(t, name, torch.float32, (H, D), dev)
     _is(state, "state", torch.float32, (N, H, D), dev)
-    return dev, lead, H, D, N
 
 
 def _glr_fits(x, r, i, lam, br, bi, state, cu_seqlens):
@@ -1130,16 +1129,17 @@ def glr_scan(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: fl
 
 
 def _add_norm_args(x, residual, w):
-    """(device, rows, D, residual's dtype), checked; residual may be None."""
+    """Says what is wrong with the arguments of ``add_norm`` and its like."""
     dev = _gpu(x, "x", tuple(range(1, 9)), tuple(_DTYPES))
     D = x.shape[-1]
+    if D == 0:
+        raise ValueError("x has rows of no values")
     _is(x, "x", x.dtype, tuple(x.shape), dev)
     R = x.dtype
     if residual is not None:
         R = residual.dtype if isinstance(residual, torch.Tensor) and residual.dtype is torch.float32 else x.dtype
         _is(residual, "residual", R, tuple(x.shape), dev)
     _is(w, "w", torch.float32, (D,), dev)
-    return dev, x.numel() // D if D else 0, D, R
 
 
 def _dropped(p, seed, dev):

@@ -99,7 +99,9 @@ struct GlrChannel {
   float k2, br, bi;
 };
 __device__ __forceinline__ GlrChannel glr_channel(const float *lam, const float *br, const float *bi, float power, int c) {
-  return {-power * GLR_LOG2E * softplus(lam[c]), br ? -GLR_LOG2E * br[c] : 0.f, bi ? -GLR_LOG2E * bi[c] : 0.f};
+  // finite, so that a closed gate's 0 times it is 0
+  const float k2 = -power * (GLR_LOG2E * softplus(lam[c]));
+  return {k2 < -3.4e38f ? -3.4e38f : k2, br ? -GLR_LOG2E * br[c] : 0.f, bi ? -GLR_LOG2E * bi[c] : 0.f};
 }
 
 // sigmoid(z + bias), bias in units of -log2 e

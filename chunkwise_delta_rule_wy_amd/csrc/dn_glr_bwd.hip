@@ -9,9 +9,10 @@
 namespace dn {
 namespace {
 
-#ifndef BWD_ROWS
-#define BWD_ROWS 4
-#endif
+// Rows of a run: what stays of eight until the gradients passes the registers (4 x 4096
+// tokens of 4096 channels in bf16: 211 us, with eight 468).
+constexpr int BWD_ROWS = 4;
+
 template <typename E, int ROWS, bool FLAT>
 __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
   typedef typename Pair<E>::type P2;
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
       slow = __any(glr_flags<ROWS>(p, q, row, s.row1, f));
     }
     // What stays until the gradients: a, the input b = m u, m sigmoid(i), u / m and the
-    // gates.  Below the fp32 range m counts as 0, and 1 / m as finite.
+    // gates.  Below the fp32 range m and 1 / m count as 0: u may be of any size there.
     f32x2 a[ROWS], b[ROWS], ms[ROWS], um[ROWS], sr[ROWS], si[ROWS], dv[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
         si[j][e] = glr_sigmoid(ij[e], k.bi);
         const float l2 = k.k2 * sr[j][e];
         a[j][e] = __builtin_amdgcn_exp2f(l2);
-        const float mm = glr_rest(a[j][e], l2), over = __builtin_amdgcn_rsqf(fmaxf(mm, 1e-37f)), m = mm * over;
+        const float mm = glr_rest(a[j][e], l2), over = mm < 1e-37f ? 0.f : __builtin_amdgcn_rsqf(mm), m = mm * over;
         const float u = si[j][e] * xj[e];
         b[j][e] = m * u;
         ms[j][e] = m * si[j][e];
