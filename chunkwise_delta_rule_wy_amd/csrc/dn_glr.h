@@ -116,14 +116,15 @@ __device__ __forceinline__ float glr_pick(bool first, float a, float b) {
   return first ? a : b;
 }
 
-// 1 - a^2 for a = 2^l2, l2 <= 0: with v = -log a below 1/2, where the difference
-// would lose digits, 2 a sinh v by its series (the rest is below 2^-26 of it).
+// 1 - a^2 for a = 2^l2, l2 <= 0: above l2 = -1/2, where the difference would lose
+// digits, 2 a sinh(-log a), its sinh by the series' terms up to the fifth power with the
+// seventh's best share added (the rest is below 2^-26 of it); the logarithm's ln 2 is in
+// the numbers.
 __device__ __forceinline__ float glr_rest(float a, float l2) {
-  const float v = -GLR_LN2 * l2, w = v * v;
-  float q = __builtin_fmaf(w, 1.f / 5040, 1.f / 120);
-  q = __builtin_fmaf(w, q, 1.f / 6);
-  q = __builtin_fmaf(w, q, 1.f);
-  return glr_pick(v < 0.5f, (v + v) * a * q, __builtin_fmaf(-a, a, 1.f));
+  const float w = l2 * l2;
+  float q = __builtin_fmaf(w, -0.00267815118f, -0.111007145f);
+  q = __builtin_fmaf(w, q, -1.38629438f);
+  return glr_pick(l2 > -0.5f, a * l2 * q, __builtin_fmaf(-a, a, 1.f));
 }
 
 // A c + B, where A = 0 drops c, whatever it is; DROP false where segments lie in

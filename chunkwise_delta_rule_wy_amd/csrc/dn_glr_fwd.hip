@@ -30,41 +30,45 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p) {
     glr_load_at<E>(p.r, row, left, p.C, c, r);
     glr_load_at<E>(BACK ? p.dy : p.x, row, left, p.C, c, x);
     if (!BACK) glr_load_at<E>(p.i, row, left, p.C, c, i);
-    GlrFlags f;
-    const bool slow = glr_flags<ROWS>(p, q, row, end, f);
-    GlrSeq w = q;
+    f32x2 a[ROWS], b[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       const f32x2 rj = to_f2<E>(r[j]), xj = to_f2<E>(x[j]);
-      const float s0 = glr_sigmoid(rj[0], k0.br), s1 = glr_sigmoid(rj[1], k1.br);
-      f32x2 a = {__builtin_amdgcn_exp2f(k0.k2 * s0), __builtin_amdgcn_exp2f(k1.k2 * s1)}, b;
+      const float l0 = k0.k2 * glr_sigmoid(rj[0], k0.br), l1 = k1.k2 * glr_sigmoid(rj[1], k1.br);
+      a[j] = (f32x2){__builtin_amdgcn_exp2f(l0), __builtin_amdgcn_exp2f(l1)};
       if (BACK) {
-        b = (f32x2){a[0] * xj[0], a[1] * xj[1]};
+        b[j] = (f32x2){a[j][0] * xj[0], a[j][1] * xj[1]};
       } else {
         const f32x2 ij = to_f2<E>(i[j]);
-        b = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[0], k0.k2 * s0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
-                    __builtin_amdgcn_sqrtf(glr_rest(a[1], k1.k2 * s1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
+        b[j] = (f32x2){__builtin_amdgcn_sqrtf(glr_rest(a[j][0], l0)) * glr_sigmoid(ij[0], k0.bi) * xj[0],
+                       __builtin_amdgcn_sqrtf(glr_rest(a[j][1], l1)) * glr_sigmoid(ij[1], k1.bi) * xj[1]};
       }
-      if (slow) {
+    }
+    GlrFlags f;
+    if (__any(glr_flags<ROWS>(p, q, row, end, f))) {
+      GlrSeq w = q;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
         if (j >= f.live) {
-          a = (f32x2){1.f, 1.f};
-          b = (f32x2){0.f, 0.f};
+          a[j] = (f32x2){1.f, 1.f};
+          b[j] = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          a = b = (f32x2){0.f, 0.f};
+          a[j] = b[j] = (f32x2){0.f, 0.f};
         } else if ((BACK ? f.ends : f.starts) >> j & 1) {
           // the state in front of the row, or the gradient behind it, is h0 or dhT
           w.walk(p, row + j);
           const float *st = BACK ? p.dhT : p.h0;
-          if (st) b = glr_fma(a, *reinterpret_cast<const f32x2 *>(st + (size_t)w.n * p.C + c), b);
-          a = (f32x2){0.f, 0.f};
+          if (st) b[j] = glr_fma(a[j], *reinterpret_cast<const f32x2 *>(st + (size_t)w.n * p.C + c), b[j]);
+          a[j] = (f32x2){0.f, 0.f};
         }
+        B = BACK ? glr_map(A, b[j], B) : glr_map(a[j], B, b[j]);
+        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
       }
-      if (BACK) {
-        B = glr_map(A, b, B);
-        A = (f32x2){A[0] * a[0], A[1] * a[1]};
-      } else {
-        B = glr_map(a, B, b);
-        A = (f32x2){a[0] * A[0], a[1] * A[1]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        B = BACK ? glr_map(A, b[j], B) : glr_fma(a[j], B, b[j]);
+        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
       }
     }
   }

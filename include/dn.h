@@ -570,7 +570,7 @@ dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32_t dtype, c
  *   in dn_ssm_fwd.  A sequence without tokens passes h0 through to hT.
  * - States are fp32 throughout; y and the gradients in the dtype are rounded once.
  * - A recurrence gate r of minus infinity gives a = 1 exactly: the token leaves
- *   the state as it is.  A value that is not finite reaches its own channel's
+ *   the state as it is, for any finite x and i.  A value that is not finite reaches its own channel's
  *   later tokens of its sequence (in the backward pass also the earlier ones);
  *   it does not cross sequences or channels.
  * - `states`, from the forward to the backward pass: the fp32 states that the
@@ -578,8 +578,8 @@ dn_status dn_gated_norm_bwd(int64_t rows, int32_t D, int32_t R, int32_t dtype, c
  *   computed again by the backward pass).  They belong to the call's inputs,
  *   sizes and cu_seqlens.
  * - D a multiple of 8, H D up to 2^23, B T below 2^31, segments of the rows times
- *   blocks of 64 channels below 2^23 (DN_EUNSUPPORTED otherwise).  No atomics:
- *   results repeat bit for bit.
+ *   blocks of 64 channels below 2^23 (DN_EUNSUPPORTED otherwise).  Outputs may not alias
+ *   inputs.  No atomics: results repeat bit for bit.
  */
 size_t dn_glr_states(int32_t B, int32_t T, int32_t H, int32_t D);
 
@@ -606,7 +606,8 @@ dn_status dn_glr_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs,
 
 /*
  * One token of B sequences: x, r, i, y [B,H,D]; state [B,H,D] fp32, read and
- * overwritten.
+ * overwritten.  B up to 262140, sequences times blocks of 1024 channels below 2^24
+ * (DN_EUNSUPPORTED otherwise).
  */
 dn_status dn_glr_step(int32_t B, int32_t H, int32_t D, int32_t dtype, const void *x, const void *r, const void *i,
                       const float *lam, const float *br, const float *bi, float power, float *state, void *y,
@@ -654,10 +655,10 @@ dn_status dn_add_norm_bwd(int64_t rows, int32_t D, int32_t dtype, int32_t res_dt
 /*
  * dn_add_norm for serving, without dropout and with the rows in 8 bits: y8
  * [rows, D] 8-bit floats (4 exponent and 3 mantissa bits, no infinities, largest
- * value 448) and scale [rows] fp32, scale = max |y| / 448 (of rows of zeros
- * 1e-30 / 448), y8 = y / scale rounded to nearest even.  w NULL: y = h, the sum
- * itself.  A row with a value that is not finite has NaN in its place, or as a
- * whole where it is normed.  Other arguments and errors as dn_add_norm; y8 16-byte
+ * value 448) and scale [rows] fp32, scale = max |y| / 448 (1e-30 / 448 where all
+ * are below 1e-30), y8 = y / scale rounded to nearest even.  w NULL: y = h, the sum
+ * itself.  A row with NaN has NaN in its place, and one with an infinity an infinite
+ * scale; rows that are normed are NaN as a whole.  Other arguments and errors as dn_add_norm; y8 16-byte
  * aligned.
  */
 dn_status dn_norm8(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, const void *x, const void *residual,
