@@ -203,9 +203,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
             *reinterpret_cast<f32x2 *>(p.dh0 + (size_t)w.n * p.C + c) = g;
           }
         }
-        const auto put = [&](void *out, f32x2 v) {
-          *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(out, tile * pitch) + o[j]) = to_e2<E>(v);
-        };
+        const auto put = [&](void *out, f32x2 v) { glr_store(glr_base(out, tile * pitch), o[j], to_e2<E>(v)); };
         put(p.dx, dx);
         put(p.dr, dr);
         put(p.di, di);

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
       for (int j = 0; j < ROWS; ++j) {
         h = glr_map(a[j], h, b[j]);
         if (j < f.live) {
-          if (Y && (!(f.dead >> j & 1) || p.zero_tail)) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, tile * pitch) + o[j]) = to_e2<E>(h);
+          if (Y && (!(f.dead >> j & 1) || p.zero_tail)) glr_store(glr_base(p.y, tile * pitch), o[j], to_e2<E>(h));
           if (p.hT && f.ends >> j & 1) {
             w.walk(p, row + j);
             *reinterpret_cast<f32x2 *>(p.hT + (size_t)w.n * p.C + c) = h;
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         h = glr_fma(a[j], h, b[j]);
-        if (Y) *reinterpret_cast<GLR_GLOBAL P2 *>(glr_base(p.y, tile * pitch) + o[j]) = to_e2<E>(h);
+        if (Y) glr_store(glr_base(p.y, tile * pitch), o[j], to_e2<E>(h));
       }
     }
   }
