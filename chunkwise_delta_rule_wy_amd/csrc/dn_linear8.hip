@@ -52,7 +52,22 @@ struct Linear8Params {
 __device__ const u128 g_zero16 = {{0, 0, 0, 0}};
 
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(0.70710678118654752440f * z)); }
+// z Phi(z), Phi(-|z|) = e^(-z^2 / 2) t Q(t) with t = 1 / (1 + 0.3677 |z|): Q is the
+// polynomial of degree 6 that fits e^(z^2 / 2) Phi(-|z|) / t best (1.1e-6 of it for |z| up
+// to 14), so that the value keeps its digits below zero too, where 1 + erf would lose them:
+// with fp32's roundings 8e-6 of it, where y's rounding to bf16 gives 2e-3.  (1357 x 1001 over
+// 2064 indices: 12.8 us, with erff 13.7, with no activation 11.6.)
+__device__ __forceinline__ float gelu(float z) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.36769554f, 1.f));
+  float q = __builtin_fmaf(t, 0.048311852f, -0.173576f);
+  q = __builtin_fmaf(t, q, 0.15546185f);
+  q = __builtin_fmaf(t, q, 0.040676955f);
+  q = __builtin_fmaf(t, q, 0.13678895f);
+  q = __builtin_fmaf(t, q, 0.14560027f);
+  q = __builtin_fmaf(t, q, 0.14673667f);
+  const float below = __builtin_amdgcn_exp2f(-0.7213475f * z * z) * t * q;
+  return z * (z < 0.f ? below : 1.f - below);
+}
 
 // Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD gets a
 // contiguous range of tiles, which run through bands of BAND rows of tiles, so that

@@ -217,3 +217,15 @@ def test_serving_block():
     y = hd.reshape(-1, W) + val["y"] @ (d(o8) * d(os_)[:, None]).t()
     rel = (d(want).reshape(-1, W) - y).norm() / (y - hd.reshape(-1, W)).norm()
     assert rel < 0.1, rel
+
+
+def test_gelu_keeps_its_digits():
+    # one product at a time, exact in fp32: the activation's own error, far below zero too (Phi of -12 is 2e-33)
+    z = torch.linspace(-12, 12, 4096)
+    one, x = lambda n: torch.ones(n).cuda(), torch.zeros(70, 16)  # noqa: E731
+    w = torch.zeros(4096, 16).to(E8).cuda()
+    for M in (3, 70):
+        y = dn.linear8(x[:M].to(E8).cuda(), one(M), w, one(4096), z.cuda(), None, "gelu").cpu().double()
+        want = z.double() * torch.special.erfc(-z.double() / 2 ** 0.5) / 2
+        # half a step of bf16, the exponent's rounding (72 * 1.45 halves of 2^-23 of it) and 20 digits' units
+        assert ((y - want).abs() <= (ref.half(BF) + 128 * ref.U) * want.abs() * 1.01 + 1e-37).all()
