@@ -1042,7 +1042,7 @@ def glr_fwd(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: flo
     _is(states, "states", torch.float32, (rows, H, D), x.device)
     y = torch.empty_like(x)
     hT = lam.new_empty((N, H, D))
-    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device) if wsb else None
+    ws = x.new_empty(wsb, dtype=torch.uint8) if wsb else None
     _call("dn_glr_fwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, x.data_ptr(), r.data_ptr(), i.data_ptr(),
           lam.data_ptr(), _adr(br), _adr(bi), power, _adr(h0), _adr(cu_seqlens), y.data_ptr(), hT.data_ptr(), _adr(states),
           _adr(ws), wsb)
@@ -1068,7 +1068,7 @@ def glr_bwd(x, r, i, lam, br, bi, h0, dy, dhT=None, cu_seqlens=None, power: floa
               dbr=None if br is None else torch.empty_like(lam), dbi=None if bi is None else torch.empty_like(lam),
               dh0=lam.new_empty((N, H, D)))
     wsb = none if states is None else given
-    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device) if wsb else None
+    ws = x.new_empty(wsb, dtype=torch.uint8) if wsb else None
     _call("dn_glr_bwd", dev, B, T, H, D, N, _DTYPES[x.dtype] | DN_ZERO_TAIL, x.data_ptr(), r.data_ptr(), i.data_ptr(),
           lam.data_ptr(), _adr(br), _adr(bi), power, _adr(h0), _adr(cu_seqlens), _adr(states), dy.data_ptr(), _adr(dhT),
           *[_adr(g) for g in gr.values()], _adr(ws), wsb)
@@ -1166,6 +1166,12 @@ def _add_norm_fits(x, residual, w):
         return False, None, None, None, None
 
 
+@functools.lru_cache(maxsize=256)
+def _add_norm_sizes(rows, D):
+    """Bytes of workspace backwards."""
+    return load_library().dn_add_norm_bwd_workspace(rows, D)
+
+
 def add_norm(x, residual, w, eps: float = 1e-5, p: float = 0.0, seed=None):
     """The residual's addition with dropout and root-mean-square norm over the last
     dimension (``dn_add_norm``): ``h = residual + dropout(x)``, ``y = h /
@@ -1201,8 +1207,8 @@ def add_norm_bwd(h, w, dy, dh=None, eps: float = 1e-5, p: float = 0.0, seed=None
     _is(dh, "dh", R, h.shape, dy.device)
     dres, dw = torch.empty_like(h), torch.empty_like(w)
     dx = torch.empty_like(dy) if drop or R is not dy.dtype else None
-    wsb = load_library().dn_add_norm_bwd_workspace(rows, D)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dy.device)
+    wsb = _add_norm_sizes(rows, D)
+    ws = dy.new_empty(wsb, dtype=torch.uint8)
     _call("dn_add_norm_bwd", dev, rows, D, _DTYPES[dy.dtype], _DTYPES[R], h.data_ptr(), w.data_ptr(), eps, p,
           seed.data_ptr() if drop else None, dy.data_ptr(), _adr(dh), _adr(dx), dres.data_ptr(), dw.data_ptr(), ws.data_ptr(),
           wsb)
@@ -1245,7 +1251,7 @@ def norm8(x, residual=None, w=None, eps: float = 1e-5):
     if not fits:
         _add_norm_args(x, residual, w)
     y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     h = None if residual is None else torch.empty_like(residual)
     _call("dn_norm8", dev, rows, D, _DTYPES[x.dtype], _DTYPES[R], x.data_ptr(), _adr(residual), _adr(w), eps, y.data_ptr(),
           scale.data_ptr(), _adr(h))
@@ -1292,7 +1298,7 @@ def linear8(x, xs, w, ws, bias=None, residual=None, act: str = "none"):
         fits = False
     if not fits:
         _linear8_args(x, xs, w, ws, bias, residual, act)
-    y = torch.empty(lead + wd[:1], dtype=torch.bfloat16, device=x.device)
+    y = xs.new_empty(lead + wd[:1], dtype=torch.bfloat16)
     _call("dn_linear8", dev, xs.numel(), N, xd[-1], x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), _adr(bias),
           _adr(residual), _ACTS[act], y.data_ptr())
     return y
