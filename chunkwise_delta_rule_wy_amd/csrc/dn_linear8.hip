@@ -72,7 +72,8 @@ __device__ __forceinline__ float gelu(float z) {
 // Tile of a workgroup.  Workgroups are dealt to the 8 XCDs round robin; each XCD gets a
 // contiguous range of tiles, which run through bands of BAND rows of tiles, so that
 // the tiles which are side by side in time share rows of x and of w in one L2
-// (16384 x 8192 x 4096: 458 us; bands of 2 and 8: 474 and 509 us).
+// (16384 x 8192 x 4096: 422 to 438 us; bands of 2 and 8 rows within that, and where the
+// loads still set the pace 3 and 11 % longer).
 constexpr int BAND = 4;
 __device__ __forceinline__ void tile_of(const Linear8Params &p, int &tm, int &tn) {
   const int total = p.tm * p.tn, q = total >> 3, r = total & 7, xcd = blockIdx.x & 7;
@@ -341,7 +342,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
 // each, in blocks of 128.  The blocks pass through the wave's own part of LDS, two
 // at a time and without barriers, as in the tiles: a load into registers would touch
 // 16 rows at once, which takes twice the time for the same bytes (64 x 4096 x 4096:
-// 12.3 us).
+// 12.3 us, so 8.3).  What is left is latency: the launch, four blocks a wave that
+// depend on nothing but arrive one after the other, and the exchange of the waves' sums.
 constexpr int FEW_WAVES = 8;
 
 template <int MT>

@@ -235,3 +235,17 @@ def test_refusals():
                  lambda: dn.linear8(z(3, 24).to(E8), z(3), z(8, 24).to(E8), z(8))):
         with pytest.raises(dn.DnError):
             call()
+
+
+@pytest.mark.parametrize("B,T,H,lens", [(2, 1024, 104, None), (1, 1500, 104, None), (1, 1500, 128, [700, 0, 790])])
+def test_directions_cut_in_different_ways(B, T, H, lens):
+    """Where the backward pass cuts sequences that the forward pass walks through, with and without kept states."""
+    d, dy, dhT, cu, ls = inputs(B, T, H, 64 if B == 1 else 32, lens)
+    got, again = both(d, dy, dhT, cu), both(d, dy, dhT, cu, keep=False)
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+    C = d["lam"].numel()
+    pick = [0, 63, 64, C - 1]
+    col = lambda v: v.reshape(*v.shape[:-2], -1)[..., pick][..., None, :]  # noqa: E731
+    val, bound = reference({k: v if v is None else col(v) for k, v in d.items()}, ls, col(dy), col(dhT))
+    check({k: col(v).cpu() for k, v in got.items()}, val, bound)
