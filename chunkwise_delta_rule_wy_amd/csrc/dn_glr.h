@@ -143,15 +143,21 @@ __device__ __forceinline__ f32x2 glr_fma(f32x2 a, f32x2 b, f32x2 c) {
 struct GlrSeq {
   int n;
   int64_t beg, end;
+  // for a row that all lanes of the wave share, and all of them active: every lane looks
+  // at one offset a step (up to 63 sequences one step, to 4095 two; a search by halves waits
+  // for each of its loads: 1357 rows of 60 sequences 53.5 us both ways, so 51.8, 8192 of 300
+  // 86 and 83)
   __device__ __forceinline__ void find(const GlrParams &p, int64_t row) {
     if (p.cu) {
-      int lo = 0, hi = p.N + 1;  // the first offset behind the row
+      uint32_t lo = 0, hi = (uint32_t)p.N + 1;  // the first offset behind the row is one of [lo, hi]
       while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu[mid] > row) hi = mid;
-        else lo = mid + 1;
+        const uint32_t step = (hi - lo + 63) / 64, at = lo + (lane_id() + 1) * step - 1;
+        const uint64_t behind = __ballot(at >= hi || p.cu[at] > row);
+        const uint32_t k = behind ? __builtin_ctzll(behind) : 64;
+        hi = min(hi, lo + (k + 1) * step - 1);
+        lo = min(hi, lo + k * step);
       }
-      n = lo < 1 ? 0 : lo - 1;
+      n = lo < 1 ? 0 : (int)lo - 1;
       beg = p.cu[n];
       end = n < p.N ? p.cu[n + 1] : INT64_MAX;
     } else {
@@ -178,11 +184,9 @@ struct GlrSeq {
   }
 };
 
-// A segment's rows [row0, row1), the number of its first block of states and
-// the range of segments that its first and last rows' sequences reach.
+// A segment's rows [row0, row1) and the number of its first block of states.
 struct GlrSegment {
   int64_t row0, row1, state0;
-  int first, last;
 };
 __device__ __forceinline__ GlrSegment glr_segment(const GlrParams &p, int seg) {
   GlrSegment s;
@@ -191,23 +195,29 @@ __device__ __forceinline__ GlrSegment glr_segment(const GlrParams &p, int seg) {
     s.row0 = seg * span;
     s.row1 = min(s.row0 + span, p.rows);
     s.state0 = s.row0 / GLR_STATE;
-    s.first = s.last = seg;
-    if (p.cut && s.row1 > s.row0) {
-      GlrSeq q;
-      q.find(p, s.row0);
-      if (q.n < p.N) s.first = (int)max((int64_t)0, q.beg / span);
-      q.find(p, s.row1 - 1);
-      if (q.n < p.N) s.last = (int)min((int64_t)p.nseg - 1, (q.end - 1) / span);
-    }
   } else {
     const int n = seg / p.NS, k = seg - n * p.NS;
     s.row0 = (int64_t)n * p.T + k * span;
     s.row1 = min(s.row0 + span, (int64_t)(n + 1) * p.T);
     s.state0 = (int64_t)n * ((p.T + GLR_STATE - 1) / GLR_STATE) + k * (span / GLR_STATE);
-    s.first = n * p.NS;
-    s.last = s.first + p.NS - 1;
   }
   return s;
+}
+// The sequence of its first row (BACK: its last one), and that sequence's first (last) segment.
+template <bool BACK>
+__device__ __forceinline__ int glr_reach(const GlrParams &p, const GlrSegment &s, int seg, GlrSeq &q) {
+  if (!p.flat) {
+    q.n = seg / p.NS;
+    q.beg = (int64_t)q.n * p.T;
+    q.end = q.beg + p.T;
+    return BACK ? q.n * p.NS + p.NS - 1 : q.n * p.NS;
+  }
+  q = {};
+  if (s.row0 >= s.row1) return seg;
+  q.find(p, BACK ? s.row1 - 1 : s.row0);
+  if (!p.cut || q.n >= p.N) return seg;
+  const int64_t span = (int64_t)p.segt * GLR_TILE;
+  return BACK ? (int)min((int64_t)p.nseg - 1, (q.end - 1) / span) : (int)max((int64_t)0, q.beg / span);
 }
 
 // The rows of a run that need care: bit j of `starts` (`ends`) where row j is its

@@ -36,7 +36,9 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
         *reinterpret_cast<f32x2 *>(p.dh0 + n * p.C + c) =
             p.dhT ? *reinterpret_cast<const f32x2 *>(p.dhT + n * p.C + c) : (f32x2){0.f, 0.f};
   f32x2 carry = {0.f, 0.f};  // the gradient that reaches the tile from behind
-  if (p.cut) carry = glr_join<true>(p, p.sum_r, seg + 1, s.last + 1, c, &fwd_maps[0][0][0]);
+  GlrSeq q;
+  const int last = glr_reach<true>(p, s, seg, q);
+  if (p.cut) carry = glr_join<true>(p, p.sum_r, seg + 1, last + 1, c, &fwd_maps[0][0][0]);
   f32x2 dlam = {0.f, 0.f}, dbr = {0.f, 0.f}, dbi = {0.f, 0.f};
   const int64_t tiles = (s.row1 - s.row0 + TILE - 1) / TILE;
   P2 x[ROWS], r[ROWS], i[ROWS], dy[ROWS];
@@ -55,9 +57,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     glr_load<E>(p.i, tile, o, p.C, i);
     glr_load<E>(p.dy, tile, o, p.C, dy);
   };
-  GlrSeq q = {};
   if (tiles > 0) {
-    q.find(p, s.row1 - 1);
     load(tiles - 1);
     glr_settle();
   }

@@ -30,8 +30,12 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p, int c
   const int per = p.segt * (GLR_TILE / GLR_RUNS);  // rows of a run, a multiple of ROWS
   const int64_t beg = s.row0 + (int64_t)run * per, end = min(beg + per, s.row1);
   f32x2 A = {1.f, 1.f}, B = {0.f, 0.f};
-  GlrSeq q;
-  if (beg < end) q.find(p, beg);
+  // the sequences of the first rows of the wave's two runs
+  GlrSeq q, upper;
+  const int64_t first = s.row0 + (int64_t)__builtin_amdgcn_readfirstlane(2 * wave_id()) * per;
+  q.find(p, min(first, s.row1 - 1));
+  upper.find(p, min(first + per, s.row1 - 1));
+  if (run & 1) q = upper;
   // in row order: going back the maps are composed on the other side, c -> A (a c + b) + B
   for (int64_t row = beg; row < end; row += ROWS) {
     P2 r[ROWS], x[ROWS], i[ROWS];
@@ -114,10 +118,10 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
         *reinterpret_cast<f32x2 *>(p.hT + n * p.C + c) =
             p.h0 ? *reinterpret_cast<const f32x2 *>(p.h0 + n * p.C + c) : (f32x2){0.f, 0.f};
   f32x2 carry = {0.f, 0.f};  // the state in front of the tile
-  if (p.cut) carry = glr_join<false>(p, p.sum_f, s.first, seg, c, &maps[0][0][0]);
-  if (s.row0 >= s.row1) return;
   GlrSeq q;
-  q.find(p, s.row0);
+  const int first = glr_reach<false>(p, s, seg, q);
+  if (p.cut) carry = glr_join<false>(p, p.sum_f, first, seg, c, &maps[0][0][0]);
+  if (s.row0 >= s.row1) return;
   P2 x[ROWS], r[ROWS], i[ROWS];
   // No branch in the loads: registers that are loaded in one of two ways get copied
   // where these meet, and the copies wait.
