@@ -15,14 +15,16 @@
 // one row m.
 //
 // Many rows: tiles of x and w pass through LDS, a block of 128 indices at a time,
-// loaded directly (no registers) one block ahead.  A row of a tile is 128 bytes, half
+// loaded directly (no registers) up to two blocks ahead.  A row of a tile is 128 bytes, half
 // the span of the 64 banks; its 16-byte units are stored at unit ^ (row / 2 & 7), so
 // that sixteen lanes reading one unit of sixteen rows meet all banks (with unit ^
 // (row & 7), which only tells eight rows apart, every read took twice its time).
 //
-// Few rows: the weights are the traffic, and no tile of them is used twice, so
-// that they go from memory to registers; a workgroup takes 16 columns and its
-// waves share the indices.
+// 16384 x 8192 over 4096 indices take 422 to 438 us, 2.5 to 2.6 PFLOP/s at a clock that
+// the power brings down to 1.9 GHz, with the matrix unit busy in 65 % of the cycles.
+//
+// Few rows: the weights are the traffic, and no tile of them is used twice; a
+// workgroup takes 16 columns, and its waves share the indices and nothing else.
 #include "dn.h"
 #include "dn_internal.h"
 #include "dn_wy.h"
@@ -444,9 +446,16 @@ int64_t cost(const Linear8Params &p, int t, int first, int more) {
 }
 
 hipError_t launch(Linear8Params &p, hipStream_t st) {
-  if (p.M <= 16) return launch_few<1>(p, st);
-  if (p.M <= 32) return launch_few<2>(p, st);
-  if (p.M <= 64) return launch_few<4>(p, st);
+  // Few rows, of which a CU holds two workgroups (up to 16 rows) or one: up to two rounds
+  // of these, or one where 64 rows make it longer, and tiles beyond.  In us, few [tiles]: over
+  // 4096 indices 64 rows of 4096 columns 8.4 [11.0], of 6144 15.0 [13.9], of 16384 26.8
+  // [15.7]; 32 of 4096 6.4 [10.9], of 8192 12.8 [13.6], of 12288 17.9 [16.0]; 1 of 4096 5.1
+  // [10.8], of 16384 13.7 [13.8], of 65536 45.0 [45.7]; over 1024, 1 of 16384 5.7 [6.0], of
+  // 65536 17.6 [15.0].
+  const int64_t few = ((int64_t)p.N + 15) / 16;
+  if (p.M <= 16 && few <= 1024) return launch_few<1>(p, st);
+  if (p.M > 16 && p.M <= 32 && few <= 512) return launch_few<2>(p, st);
+  if (p.M > 32 && p.M <= 64 && few <= 256) return launch_few<4>(p, st);
   // In us over 4096 indices with tiles of 64, 128 and 256: 256 x 4096 12.6, 17.9, 43.6; 768 x
   // 4096 24.8, 20.2, 44.3; 3000 x 4096 81.8, 50.4, 52.1; 4096 x 4096 118, 65.6, 56.8; 4096 x 4097
   // 126, 83.6, 126.
@@ -465,8 +474,7 @@ extern "C" dn_status dn_linear8(int32_t M, int32_t N, int32_t K, const void *x, 
                                 const float *ws, const float *bias, const void *residual, int32_t act, void *y,
                                 hipStream_t stream) {
   if (M < 0 || N <= 0 || K <= 0 || act < ACT_NONE || act > ACT_GELU) return DN_EINVAL;
-  // the rows' 16-byte units, a tile's 32-bit byte offsets, and a grid's threads (fewer than
-  // 2^32), in tiles and in the few rows' 16 columns a workgroup
+  // the rows' 16-byte units, a tile's 32-bit byte offsets, and a grid's threads (fewer than 2^32)
   if (K % 16 != 0 || K > 1 << 23) return DN_EUNSUPPORTED;
   if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) > UINT32_MAX / 256 || N > 1 << 26 || M > INT32_MAX - 256)
     return DN_EUNSUPPORTED;

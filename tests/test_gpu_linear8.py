@@ -50,7 +50,7 @@ def test_epilogue(M, N, act, bias, residual):
     run(M, N, 320, act, bias, residual, 1)
 
 
-# one size for each tile, with ragged edges in both directions
+# ragged edges in both directions
 @pytest.mark.parametrize("M,N,K,residual", [(2100, 2000, 272, True), (2047, 2049, 128, False), (4100, 4099, 400, True), (4352, 4096, 128, False)])
 def test_large_tiles(M, N, K, residual):
     run(M, N, K, "silu", True, residual, 2)
@@ -229,3 +229,9 @@ def test_gelu_keeps_its_digits():
         want = z.double() * torch.special.erfc(-z.double() / 2 ** 0.5) / 2
         # half a step of bf16, the exponent's rounding (72 * 1.45 halves of 2^-23 of it) and 20 digits' units
         assert ((y - want).abs() <= (ref.half(BF) + 128 * ref.U) * want.abs() * 1.01 + 1e-37).all()
+
+
+# few rows of many columns, on both sides of where tiles take them over, with edges in their tiles
+@pytest.mark.parametrize("M,N", [(1, 16384), (16, 16385), (2, 20000), (17, 8192), (32, 8200), (33, 4096), (64, 4097), (60, 5000)])
+def test_few_rows_of_many_columns(M, N):
+    run(M, N, 272, "silu", True, True, 12)
