@@ -25,6 +25,8 @@
 // a pass before.  Packed sequences are cut wherever they lie: the state in front
 // of a sequence's first row is h0, and whatever reaches that row from the rows
 // before is dropped, not multiplied by zero, so that nothing crosses sequences.
+// Such a cut is marked by A's sign: a product of decays that has fallen to 0 drops
+// nothing, and what is not finite reaches all of its sequence.
 #pragma once
 
 #include "dn_internal.h"
@@ -127,12 +129,29 @@ __device__ __forceinline__ float glr_rest(float a, float l2) {
   return glr_pick(l2 > -0.5f, a * l2 * q, __builtin_fmaf(-a, a, 1.f));
 }
 
-// A c + B, where A = 0 drops c, whatever it is; DROP false where segments lie in
-// one sequence, and there is nothing to drop.
+// A map that starts anew has A = GLR_CUT, and compositions with it a negative A;
+// decays are positive or 0.  (One that is not a number may have either sign: its B is not
+// a number either, and so is the result.)
+constexpr float GLR_CUT = -0.f;
+__device__ __forceinline__ uint32_t glr_sign(float a) { return __builtin_bit_cast(uint32_t, a) & 0x80000000u; }
+
+// A c + B, or B alone, whatever c is, behind a cut; DROP false where segments lie in one
+// sequence, and there is nothing to drop.
 template <bool DROP = true>
 __device__ __forceinline__ f32x2 glr_map(f32x2 A, f32x2 c, f32x2 B) {
   const f32x2 r = {__builtin_fmaf(A[0], c[0], B[0]), __builtin_fmaf(A[1], c[1], B[1])};
-  return DROP ? (f32x2){A[0] == 0.f ? B[0] : r[0], A[1] == 0.f ? B[1] : r[1]} : r;
+  return DROP ? (f32x2){glr_sign(A[0]) ? B[0] : r[0], glr_sign(A[1]) ? B[1] : r[1]} : r;
+}
+// The A of two maps' composition: their product, with a cut that no product undoes, be it
+// another cut's or NaN.
+__device__ __forceinline__ float glr_times(float a, float b) {
+  const float r = a * b;
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r) | glr_sign(a) | glr_sign(b));
+}
+template <bool DROP = true>
+__device__ __forceinline__ f32x2 glr_times(f32x2 a, f32x2 b) {
+  if (!DROP) return (f32x2){a[0] * b[0], a[1] * b[1]};
+  return (f32x2){glr_times(a[0], b[0]), glr_times(a[1], b[1])};
 }
 __device__ __forceinline__ f32x2 glr_fma(f32x2 a, f32x2 b, f32x2 c) {
   return (f32x2){__builtin_fmaf(a[0], b[0], c[0]), __builtin_fmaf(a[1], b[1], c[1])};
@@ -317,7 +336,7 @@ __device__ __forceinline__ f32x2 glr_join(const GlrParams &p, const float *sums,
   for (int k = 0; k < hi - lo; ++k) {
     const float *m = sums + (size_t)(BACK ? hi - 1 - k : lo + k) * 2 * p.C + c;
     const f32x2 a = *reinterpret_cast<const f32x2 *>(m), b = *reinterpret_cast<const f32x2 *>(m + p.C);
-    A = (f32x2){a[0] * A[0], a[1] * A[1]};
+    A = glr_times(a, A);
     B = glr_map(a, B, b);
   }
   if ((threadIdx.x & 32) == 0) lds[wave * GLR_LANES + lane] = (f32x4){A[0], A[1], B[0], B[1]};

@@ -107,13 +107,14 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
           aj = (f32x2){1.f, 1.f};
           bj = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          aj = bj = (f32x2){0.f, 0.f};
+          aj = (f32x2){GLR_CUT, GLR_CUT};
+          bj = (f32x2){0.f, 0.f};
         } else if (f.starts >> j & 1) {
           bj = glr_fma(aj, at(p.h0, j), bj);
-          aj = (f32x2){0.f, 0.f};
+          aj = (f32x2){GLR_CUT, GLR_CUT};
         }
         B = glr_map(aj, B, bj);
-        A = (f32x2){A[0] * aj[0], A[1] * aj[1]};
+        A = glr_times(A, aj);
       }
 #pragma unroll
       for (int j = ROWS - 1; j >= 0; --j) {
@@ -122,13 +123,14 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
           aj = (f32x2){1.f, 1.f};
           gj = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          aj = gj = (f32x2){0.f, 0.f};
+          aj = (f32x2){GLR_CUT, GLR_CUT};
+          gj = (f32x2){0.f, 0.f};
         } else if (f.ends >> j & 1) {
           gj = glr_fma(aj, at(p.dhT, j), gj);
-          aj = (f32x2){0.f, 0.f};
+          aj = (f32x2){GLR_CUT, GLR_CUT};
         }
         G = glr_map(aj, G, gj);
-        Ar = (f32x2){Ar[0] * aj[0], Ar[1] * aj[1]};
+        Ar = glr_times(Ar, aj);
       }
     } else {
 #pragma unroll
@@ -143,10 +145,12 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_bwd_kernel(GlrParams p) {
     const f32x2 oA = other_half(A), oB = other_half(B), oAr = other_half(Ar), oG = other_half(G);
     if (!upper) {
       const f32x2 tB = glr_map<FLAT>(oA, B, oB);
-      fwd_maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
+      const f32x2 tA = glr_times<FLAT>(A, oA);
+      fwd_maps[turn][wave][lane] = (f32x4){tA[0], tA[1], tB[0], tB[1]};
     } else {
       const f32x2 tG = glr_map<FLAT>(oAr, G, oG);
-      bwd_maps[turn][wave][lane] = (f32x4){Ar[0] * oAr[0], Ar[1] * oAr[1], tG[0], tG[1]};
+      const f32x2 tA = glr_times<FLAT>(Ar, oAr);
+      bwd_maps[turn][wave][lane] = (f32x4){tA[0], tA[1], tG[0], tG[1]};
     }
     __syncthreads();
     f32x4 mf[GLR_WAVES - 1], mb[GLR_WAVES];

@@ -30,6 +30,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p, int c
   const int per = p.segt * (GLR_TILE / GLR_RUNS);  // rows of a run, a multiple of ROWS
   const int64_t beg = s.row0 + (int64_t)run * per, end = min(beg + per, s.row1);
   f32x2 A = {1.f, 1.f}, B = {0.f, 0.f};
+  bool closed = false;  // going back: the rows from here on are behind a sequence's end
   // the sequences of the first rows of the wave's two runs
   GlrSeq q, upper;
   const int64_t first = s.row0 + (int64_t)__builtin_amdgcn_readfirstlane(2 * wave_id()) * per;
@@ -66,21 +67,23 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p, int c
           a[j] = (f32x2){1.f, 1.f};
           b[j] = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          a[j] = b[j] = (f32x2){0.f, 0.f};
+          a[j] = (f32x2){GLR_CUT, GLR_CUT};
+          b[j] = (f32x2){0.f, 0.f};
         } else if ((BACK ? f.ends : f.starts) >> j & 1) {
           // the state in front of the row, or the gradient behind it, is h0 or dhT
           w.walk(p, row + j);
           const float *st = BACK ? p.dhT : p.h0;
           if (st) b[j] = glr_fma(a[j], *reinterpret_cast<const f32x2 *>(st + (size_t)w.n * p.C + c), b[j]);
-          a[j] = (f32x2){0.f, 0.f};
+          a[j] = (f32x2){GLR_CUT, GLR_CUT};
         }
         B = BACK ? glr_map(A, b[j], B) : glr_map(a[j], B, b[j]);
-        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
+        A = glr_times(A, a[j]);
       }
-    } else {
+      closed |= (f.dead | f.ends) != 0;
+    } else if (!BACK || !closed) {
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        B = BACK ? glr_map(A, b[j], B) : glr_fma(a[j], B, b[j]);
+        B = BACK ? glr_fma(A, b[j], B) : glr_fma(a[j], B, b[j]);
         A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
       }
     }
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_sum_kernel(GlrParams p, int c
 #pragma unroll
   for (int k = 0; k < GLR_RUNS; ++k) {
     const f32x4 m = maps[BACK ? GLR_RUNS - 1 - k : k][lane];
-    A = (f32x2){A[0] * m[0], A[1] * m[1]};
+    A = glr_times(A, (f32x2){m[0], m[1]});
     B = glr_map((f32x2){m[0], m[1]}, B, (f32x2){m[2], m[3]});
   }
   float *out = (BACK ? p.sum_r : p.sum_f) + (size_t)seg * 2 * p.C + ch;
@@ -160,14 +163,15 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
           a[j] = (f32x2){1.f, 1.f};
           b[j] = (f32x2){0.f, 0.f};
         } else if (f.dead >> j & 1) {
-          a[j] = b[j] = (f32x2){0.f, 0.f};
+          a[j] = (f32x2){GLR_CUT, GLR_CUT};
+          b[j] = (f32x2){0.f, 0.f};
         } else if (f.starts >> j & 1) {
           w.walk(p, row + j);
           if (p.h0) b[j] = glr_fma(a[j], *reinterpret_cast<const f32x2 *>(p.h0 + (size_t)w.n * p.C + c), b[j]);
-          a[j] = (f32x2){0.f, 0.f};
+          a[j] = (f32x2){GLR_CUT, GLR_CUT};
         }
         B = glr_map(a[j], B, b[j]);
-        A = (f32x2){A[0] * a[j][0], A[1] * a[j][1]};
+        A = glr_times(A, a[j]);
       }
     } else {
 #pragma unroll
@@ -181,7 +185,8 @@ __global__ __launch_bounds__(GLR_THREADS) void glr_fwd_kernel(GlrParams p) {
     const bool upper = threadIdx.x & 32;
     if (!upper) {
       const f32x2 tB = glr_map<FLAT>(oA, B, oB);
-      maps[turn][wave][lane] = (f32x4){A[0] * oA[0], A[1] * oA[1], tB[0], tB[1]};
+      const f32x2 tA = glr_times<FLAT>(A, oA);
+      maps[turn][wave][lane] = (f32x4){tA[0], tA[1], tB[0], tB[1]};
     }
     __syncthreads();
     f32x2 h = {0.f, 0.f};

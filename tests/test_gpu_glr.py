@@ -293,3 +293,63 @@ def test_offsets_past_32_bits():
     want = torch.sqrt(1 - a * a) * s / (1 - a)
     assert ((hT - want).abs() <= 64 * ref.U * want).all()
     assert not y[0, : T - 200].any() and ((y[0, -1].double() - want).abs() <= ref.half(BF) * want * 1.01).all()
+
+
+# How a call is cut: one sequence in segments, a pack in segments, a pack and a batch in one walk each,
+# short sequences side by side
+PLANS = [(1, 4096, 1, 64, None), (1, 1500, 1, 72, [300, 0, 700, 1, 400]), (1, 700, 130, 64, [150, 500, 50]),
+         (2, 600, 130, 64, None), (6, 300, 1, 40, None)]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("power", [8.0, 1e4])
+@pytest.mark.parametrize("B,T,H,D,lens", PLANS)
+def test_what_is_not_finite_reaches_its_sequence_under_strong_decays(B, T, H, D, lens, power, bad):
+    """Decays whose products (at power 1e4 they themselves) fall below fp32: later tokens, and going back earlier ones,
+    still see it, and other sequences and channels do not."""
+    d, dy, dhT, cu, ls = inputs(B, T, H, D, lens)
+    d["lam"].zero_()
+    clean = both(d, dy, dhT, cu, power)
+    starts = torch.tensor([0] + ls).cumsum(0)
+    n = max(range(len(ls)), key=lambda k: ls[k])  # the longest sequence
+    s, e = int(starts[n]), int(starts[n + 1])
+    fwd, back = s + min(10, ls[n] // 4), e - 1 - min(7, ls[n] // 4)
+    d["x"].reshape(-1, H * D)[fwd, 5] = bad
+    dy.reshape(-1, H * D)[back, 9] = bad
+    got = both(d, dy, dhT, cu, power)
+    flat = lambda t: t.reshape(-1, H * D)  # noqa: E731
+    assert not torch.isfinite(flat(got["y"])[fwd:e, 5]).any() and not torch.isfinite(flat(got["hT"])[n, 5])
+    assert not torch.isfinite(flat(got["dx"])[s:back + 1, 9]).any() and not torch.isfinite(flat(got["dh0"])[n, 9])
+    other = torch.ones(H * D, dtype=torch.bool)
+    other[[5, 9]] = False
+    for k in ("y", "dx", "dr", "di"):
+        same = flat(got[k] == clean[k])
+        assert same[:, other].all() and same[:s].all() and same[e:].all(), k
+    for k in ("hT", "dh0"):
+        same = flat(got[k] == clean[k])
+        assert same[:, other].all() and same[:n].all() and same[n + 1:].all(), k
+    assert torch.equal(flat(got["y"])[s:fwd], flat(clean["y"])[s:fwd])
+    again = both(d, dy, dhT, cu, power, keep=False)
+    for k in got:
+        assert torch.equal(torch.isfinite(again[k]), torch.isfinite(got[k])), k
+
+
+@pytest.mark.parametrize("H,lens", [(1, [50, 3, 70, 300, 77]), (130, [50, 3, 70, 300, 77]), (1, [1] * 40 + [200, 0, 260])])
+def test_gates_that_are_not_numbers_stay_in_their_sequence(H, lens):
+    """A decay of NaN takes no sequence with it that starts, or ends, in the same run of rows."""
+    d, dy, dhT, cu, _ = inputs(1, sum(lens), H, 64, lens)
+    clean = both(d, dy, dhT, cu)
+    starts = [0] + torch.tensor(lens).cumsum(0).tolist()
+    hit = [k for k in (1, 2, len(lens) - 3) if lens[k]]
+    for n in hit:  # the sequence's first and last tokens
+        d["r"][0, [starts[n], starts[n + 1] - 1], 0, 5] = torch.nan
+    got = both(d, dy, dhT, cu)
+    rows = torch.ones(sum(lens), dtype=torch.bool)
+    for n in hit:
+        rows[starts[n]:starts[n + 1]] = False
+        assert torch.isnan(got["y"][0, starts[n]:starts[n + 1], 0, 5]).all() and torch.isnan(got["hT"][n, 0, 5])
+    for k in ("y", "dx", "dr", "di"):
+        assert torch.equal(got[k][0, rows.cuda()], clean[k][0, rows.cuda()]), k
+    keep = [n for n in range(len(lens)) if n not in hit]
+    for k in ("hT", "dh0"):
+        assert torch.equal(got[k][keep], clean[k][keep]), k
