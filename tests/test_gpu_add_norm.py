@@ -227,3 +227,22 @@ def test_graph_replays_follow_the_seed():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a.float(), b.float())
+
+
+@pytest.mark.parametrize("E", [BF, F32])
+@pytest.mark.parametrize("rows,D", [(4000, 64), (300, 520), (700, 1000), (200, 1032), (500, 4096), (60, 8192)])
+def test_eight_bits_are_the_rounded_quotient(rows, D, E):
+    """Without norm y8 is the fp32 quotient h / scale rounded to nearest even, bit for bit: scales that are no powers of
+    two put many quotients of bf16 values next to, and onto, the halves between 8-bit values."""
+    x, res, _, _, _ = inputs(rows, D, E, E, 77)
+    x[::7] *= 1e-30  # a row's values around the least scale, and below the fp32 range
+    x[1::7] *= 1e36
+    x[2::7] *= 1e-36
+    res[::7], res[1::7], res[2::7] = 0, 0, 0
+    for r in (None, res):
+        y8, scale, h = dn.norm8(x.cuda(), None if r is None else r.cuda())
+        h, scale = h.cpu().float(), scale.cpu()
+        assert torch.equal(scale, h.abs().amax(-1).clamp(min=1e-30) / 448)
+        want = (h / scale[:, None]).to(E8).float()
+        got = y8.cpu().float()
+        assert torch.equal(got, want), int((got != want).sum())
