@@ -136,7 +136,7 @@ __global__ __launch_bounds__(AN_THREADS) void add_norm_kernel(AddNormParams p) {
 // Rows of zeros have the scale 1e-30 / 448, whose inverse is still finite.
 //
 // The quotients are those of an fp32 division: a product with the rounded inverse takes
-// some bf16 values of a row that is not normed (0.05 % in rows of 64, 0.02 % in rows of 4096),
+// some bf16 values of a row that is not normed (0.05 % in rows of 64, 0.03 % in rows of 4096),
 // whose quotients lie on a half, to the other side of it.  1 / s = inv + low to some 46
 // bits, so that q is one of the two fp32 numbers around the quotient; its remainder v - q s
 // then is exact, and q + remainder inv, rounded, is the quotient rounded (Markstein,
@@ -158,12 +158,18 @@ __global__ __launch_bounds__(AN_THREADS) void norm8_kernel(AddNormParams p) {
        row += (int64_t)gridDim.x * (AN_THREADS / LPR)) {
     float h[RW::N];
     add_row<E, R, LPR, K, false>(p, 0, 0, row, lane, h);
+    float top = LEAST8;
     if (NORM) {
       const float r = row_rsqrt<LPR>(p, h, buf, turn);
+      // an infinity becomes NaN, which a maximum passes over, and all else 0: it is
+      // looked for itself
+      if (!(r > 0.f)) {
+#pragma unroll
+        for (int i = 0; i < RW::N; ++i) top = fabsf(h[i]) == __builtin_inff() ? __builtin_inff() : top;
+      }
 #pragma unroll
       for (int i = 0; i < RW::N; ++i) h[i] = h[i] * r * w[i];
     }
-    float top = LEAST8;
 #pragma unroll
     for (int i = 0; i < RW::N; ++i) top = fmaxf(top, fabsf(h[i]));
     const float scale = lanes_sum<LPR, true>(top, buf, turn) / TOP8;
@@ -174,8 +180,8 @@ __global__ __launch_bounds__(AN_THREADS) void norm8_kernel(AddNormParams p) {
       for (int i = 0; i < RW::N; ++i) h[i] *= 0x1p64f;
     }
     float inv = 1.f / s, low = __builtin_fmaf(-inv, s, 1.f) * inv;
-    if (s == __builtin_inff()) {  // v / s is 0, and NaN for an infinite v
-      inv = low = 0.f;
+    if (s == __builtin_inff()) {  // v / s is 0, and NaN for an infinite v; a normed row is NaN as a whole
+      inv = low = NORM ? __builtin_nanf("") : 0.f;
       s = 1.f;
     }
     const auto quotient = [&](float v) {

@@ -656,10 +656,11 @@ dn_status dn_add_norm_bwd(int64_t rows, int32_t D, int32_t dtype, int32_t res_dt
  * dn_add_norm for serving, without dropout and with the rows in 8 bits: y8
  * [rows, D] 8-bit floats (4 exponent and 3 mantissa bits, no infinities, largest
  * value 448) and scale [rows] fp32, scale = max |y| / 448 (1e-30 / 448 where all
- * are below 1e-30), y8 = y / scale, the fp32 quotient rounded to nearest even.  w NULL: y = h, the sum
- * itself.  A row with NaN has NaN in its place, and one with an infinity an infinite
- * scale; rows that are normed are NaN as a whole.  Other arguments and errors as dn_add_norm; y8 16-byte
- * aligned.
+ * are below 1e-30), y8 = y / scale, the fp32 quotient rounded to nearest even.  w
+ * NULL: y = h, the sum itself.  A row with NaN has NaN in its place, and one with an
+ * infinity an infinite scale, NaN in its place and 0 for what is finite.  Rows that are
+ * normed are NaN as a whole with either, and their scale is infinite with an infinity.  Other
+ * arguments and errors as dn_add_norm; y8 16-byte aligned.
  */
 dn_status dn_norm8(int64_t rows, int32_t D, int32_t dtype, int32_t res_dtype, const void *x, const void *residual,
                    const float *w, float eps, void *y8, float *scale, void *h, hipStream_t stream);

@@ -246,3 +246,18 @@ def test_eight_bits_are_the_rounded_quotient(rows, D, E):
         want = (h / scale[:, None]).to(E8).float()
         got = y8.cpu().float()
         assert torch.equal(got, want), int((got != want).sum())
+
+
+@pytest.mark.parametrize("E,R", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256, 520, 1032, 2048, 4096, 8192])
+def test_normed_rows_with_an_infinity_in_eight_bits(D, E, R):
+    """An infinite scale, and NaN as a whole; the other rows as without it."""
+    x, res, w, _, _ = inputs(9, D, E, R, D)
+    clean = dn.norm8(x.cuda(), res.cuda(), w.cuda())
+    x[2, D - 1], res[5, D // 2], x[7, 0] = torch.inf, -torch.inf, -torch.inf
+    y8, scale, h = dn.norm8(x.cuda(), res.cuda(), w.cuda())
+    bad = [2, 5, 7]
+    assert (scale[bad] == torch.inf).all() and torch.isnan(y8[bad].float()).all()
+    keep = [0, 1, 3, 4, 6, 8]
+    assert torch.equal(y8[keep].float(), clean[0][keep].float()) and torch.equal(scale[keep], clean[1][keep])
+    assert torch.equal(h[keep], clean[2][keep]) and torch.isinf(h[[2, 5, 7], [D - 1, D // 2, 0]]).all()
