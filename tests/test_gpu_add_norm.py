@@ -261,3 +261,20 @@ def test_normed_rows_with_an_infinity_in_eight_bits(D, E, R):
     keep = [0, 1, 3, 4, 6, 8]
     assert torch.equal(y8[keep].float(), clean[0][keep].float()) and torch.equal(scale[keep], clean[1][keep])
     assert torch.equal(h[keep], clean[2][keep]) and torch.isinf(h[[2, 5, 7], [D - 1, D // 2, 0]]).all()
+
+
+def test_mask_past_32_bits_of_blocks():
+    """2^32 blocks of eight values and some, whose numbers reach into the counter's upper word (2^21 rows of 4096 values
+    end at 2^30 of them).  64 GiB, dropped and normed in place."""
+    lib, rows, D, n = dn.load_library(), (1 << 22) + 3, 8192, 5
+    x = torch.ones(rows, D, dtype=BF, device="cuda")
+    seed, w = torch.tensor(SEED).cuda(), torch.ones(D, device="cuda")
+    a = lambda t: t.data_ptr()  # noqa: E731
+    assert lib.dn_add_norm(rows, D, 1, 1, a(x), None, a(w), 1e-5, 0.5, a(seed), a(x), None, torch.cuda.current_stream().cuda_stream) == 0
+    last, first = x[-n:].float().cpu(), x[:n].float().cpu()
+    del x
+    torch.cuda.empty_cache()
+    assert torch.equal(last > 0, ref.keep_factors(SEED, 0.5, n, D, rows - n) > 0)
+    assert torch.equal(first > 0, ref.keep_factors(SEED, 0.5, n, D) > 0)
+    # rows 0, 1, 2 and the last three have the same lower words
+    assert not torch.equal(last[-3:] > 0, first[:3] > 0)
