@@ -209,3 +209,13 @@ def test_python_refuses():
         dn.linear8(x, w, x, w, act="relu")
     with pytest.raises(ValueError, match="dimensions"):
         dn.glr_fwd(x[0], x, x, w)
+
+
+def test_random_bits_against_published_vectors():
+    # the known answers that the method's authors publish for 4 words and 7 rounds (Salmon et al., 2011): counters and
+    # keys of zeros, of ones, and of the digits of pi
+    cases = [(0, 0, 0, "5f6fb709 0d893f64 4f121f81 4f730a48"),
+             (2 ** 64 - 1, 2 ** 64 - 1, 2 ** 64 - 1, "5207ddc2 45165e59 4d8ee751 8c52f662"),
+             (0x299F31D0A4093822, 0x0370734413198A2E, 0x85A308D3243F6A88, "4dfccaba 190a87f0 c47362ba b6b5242a")]
+    for key, stream, block, want in cases:
+        assert ref.philox(key, stream, block) == [int(v, 16) for v in want.split()]
