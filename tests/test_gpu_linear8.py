@@ -235,3 +235,39 @@ def test_gelu_keeps_its_digits():
 @pytest.mark.parametrize("M,N", [(1, 16384), (16, 16385), (2, 20000), (17, 8192), (32, 8200), (33, 4096), (64, 4097), (60, 5000)])
 def test_few_rows_of_many_columns(M, N):
     run(M, N, 272, "silu", True, True, 12)
+
+
+# every kind of tile, with the loop over the indices as long as it is in use: 16 to 64 blocks of 128, whole and ragged
+LONG = [(4090, 4000), (3999, 4091), (1030, 4088), (1030, 4090), (300, 1000), (257, 1001), (64, 4096), (17, 1000), (3, 520)]
+
+
+@pytest.mark.parametrize("K", [2048, 2064, 4096, 4112, 8192])
+@pytest.mark.parametrize("M,N", LONG)
+def test_whole_numbers_over_many_indices(M, N, K):
+    # two values of fifteen are not 0, and so one product of 56: the sums (8192 indices: a deviation of 12) stay below
+    # 2^8, and are exact in the sums and in bf16
+    g = torch.Generator("cuda").manual_seed(13)
+    few = lambda n: (torch.randint(-1, 2, (n, K), generator=g, device="cuda") *  # noqa: E731
+                     (torch.randint(0, 5, (n, K), generator=g, device="cuda") == 0)).float()
+    x, w = few(M), few(N)
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    want = x @ w.t()
+    assert want.abs().max() < 256
+    assert torch.equal(dn.linear8(x.to(E8), one(M), w.to(E8), one(N)).float(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(4090, 4000, 4112), (4096, 4096, 8192), (1030, 4088, 4096), (300, 1001, 8192)])
+def test_long_products(M, N, K):
+    # a sample of rows and columns, the tiles' edges among them, by the reference
+    g = torch.Generator().manual_seed(14)
+    x, xs = rows8(M, K, g)
+    w, ws = rows8(N, K, g)
+    ws, b, r = ws / K ** 0.5, torch.randn(N, generator=g), torch.randn(M, N, generator=g).to(BF)
+    y = dn.linear8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), b.cuda(), r.cuda(), "gelu").cpu()
+    some = lambda n: torch.cat([torch.tensor([0, 63, 64, 127, 128, 255, n - 1]), torch.randint(0, n, (90,), generator=g)])  # noqa: E731
+    m, n = some(M), some(N)
+    d = lambda t: t.double()  # noqa: E731
+    val, bound = ref.linear8(d(x[m]), d(xs[m]), d(w[n]), d(ws[n]), d(b[n]), d(r[m][:, n]), "gelu")
+    assert torch.isfinite(y).all()
+    q = ref.worst(y[m][:, n], val, bound)
+    assert q <= 1, q
