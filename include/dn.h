@@ -630,7 +630,10 @@ dn_status dn_glr_step(int32_t B, int32_t H, int32_t D, int32_t dtype, const void
  *   16 (j % 8) and up of the 128 that Philox4x32 with 7 rounds (Salmon et al.,
  *   "Parallel random numbers: as easy as 1, 2, 3", 2011) gives for the counter
  *   (block, stream), block = (i D + j) / 8, both 64 bits with the lower word first.
- *   The mask depends on nothing else and is not stored.
+ *   The mask depends on nothing else and is not stored.  d = 0 is a factor like
+ *   others: a dropped value that is not finite gives NaN, and so does such a gradient.
+ * - The mean of the squares is fp32: where it passes the range (values above 1e19 or
+ *   so) finite values are normed to 0.
  * - D a multiple of 8 up to 8192, rows below 2^31 (DN_EUNSUPPORTED otherwise); x,
  *   residual, h, y and their gradients 16-byte aligned.
  */

@@ -278,3 +278,32 @@ def test_mask_past_32_bits_of_blocks():
     assert torch.equal(first > 0, ref.keep_factors(SEED, 0.5, n, D) > 0)
     # rows 0, 1, 2 and the last three have the same lower words
     assert not torch.equal(last[-3:] > 0, first[:3] > 0)
+
+
+@pytest.mark.parametrize("E,R", TYPES)
+def test_dropped_values_that_are_not_finite(E, R):
+    """A dropped value is multiplied by 0, which gives NaN for one that is not finite, forwards and backwards."""
+    x, res, w, dy, dh = inputs(6, 128, E, R, 1)
+    keep = ref.keep_factors(SEED, 0.5, 6, 128)
+    seed = torch.tensor(SEED).cuda()
+    r = 3
+    drop, kept = (int((keep[r] == v).nonzero()[0]) for v in (0.0, 2.0))
+    x[r, drop] = x[r, kept] = torch.inf
+    h = dn.add_norm(x.cuda(), res.cuda(), w.cuda(), p=0.5, seed=seed)[1]
+    assert torch.isnan(h[r, drop]) and h[r, kept] == torch.inf
+    other = [0, 1, 2, 4, 5]
+    assert torch.isfinite(h[other]).all()
+    dh[r, drop] = dh[r, kept] = torch.inf
+    dx, dres, _ = dn.add_norm_bwd(res.cuda(), w.cuda(), dy.cuda(), dh.cuda(), p=0.5, seed=seed)
+    assert torch.isnan(dx[r, drop]) and dx[r, kept] == torch.inf and (dres[r, [drop, kept]] == torch.inf).all()
+    assert torch.isfinite(dx[other]).all()
+
+
+@pytest.mark.parametrize("E,R", TYPES)
+def test_rows_whose_squares_pass_the_range(E, R):
+    x, res, w, _, _ = inputs(4, 128, E, R, 2)
+    x[1], res[1] = 1e25, 0
+    y, h = dn.add_norm(x.cuda(), res.cuda(), w.cuda())
+    y8, scale, _ = dn.norm8(x.cuda(), res.cuda(), w.cuda())
+    assert not y[1].any() and not y8[1].float().any() and scale[1] == torch.tensor(1e-30) / 448
+    assert torch.isfinite(h).all() and (scale[[0, 2, 3]] > 1e-4).all() and y[[0, 2, 3]].any(1).all()
