@@ -1030,7 +1030,7 @@ def glr_fwd(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: flo
         s_t = sigmoid(r_t + br),  a_t = exp(-power softplus(lam) s_t),
         h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + bi) x_t,  y_t = h_t.
 
-    x, r, i ``[B,T,H,D]`` float32 or bfloat16 (D a multiple of 8); lam, br, bi
+    x, r, i ``[B,T,H,D]`` float32 or bfloat16, contiguous (D a multiple of 8); lam, br, bi
     ``[H,D]`` float32 (br, bi None: zero); h0 ``[N,H,D]`` float32 or None;
     cu_seqlens as in ``ssm_fwd``; states from ``glr_states``, filled for
     ``glr_bwd``.  Returns ``(y, hT)``, y in x's dtype, hT ``[N,H,D]`` float32."""
@@ -1119,8 +1119,10 @@ class GlrScan(torch.autograd.Function):
 
 def glr_scan(x, r, i, lam, br=None, bi=None, h0=None, cu_seqlens=None, power: float = 8.0, save_states: bool = True):
     """Differentiable gated linear recurrence; returns (y, hT).  ``save_states``
-    keeps states from the forward pass for the backward pass (1/16 of x's bytes
-    and less) instead of computing them again.  Rows behind the last packed
+    keeps states from the forward pass for the backward pass instead of computing
+    them again: a float32 row for every 64 rows, rounded up (for sequences of 512
+    tokens and more each by itself), of long inputs 1/32 of x's bytes in bfloat16
+    and 1/64 in float32.  Rows behind the last packed
     sequence give zeros and get zero gradients."""
     return GlrScan.apply(x, r, i, lam, br, bi, h0, cu_seqlens, power, save_states)
 
@@ -1245,8 +1247,8 @@ def norm8(x, residual=None, w=None, eps: float = 1e-5):
     """``add_norm`` for serving with its rows in 8 bits (``dn_norm8``): ``(y8, scale,
     h)``, y8 float8_e4m3fn of x's shape, scale float32 of its leading sizes, ``y =
     scale y8`` with ``scale = max |y| / 448``.  Without w the sum itself is
-    rounded: ``norm8(weight)[:2]`` gives ``linear8`` its weights.  h as
-    ``add_norm`` returns it."""
+    rounded: ``norm8(weight)[:2]`` gives ``linear8`` its weights, and y8 is ``(h /
+    scale[..., None]).to(torch.float8_e4m3fn)``.  h as ``add_norm`` returns it."""
     fits, dev, rows, D, R = _add_norm_fits(x, residual, w)
     if not fits:
         _add_norm_args(x, residual, w)

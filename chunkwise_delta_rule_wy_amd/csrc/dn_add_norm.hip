@@ -28,8 +28,8 @@ constexpr int AN_MAX_D = 8192;
 // ahead and leave as many rows of partial sums (16384 rows of 4096 bf16 values with
 // dropout, before the stores went past the caches: 136 us, with four per CU 143; without
 // the row ahead 201 us), each going on to further rows.  Both are bound by memory: these
-// rows take 103 us forwards, 133 backwards and 98 in 8 bits, that is 5.2, 5.0 and 4.8
-// TB/s, where a copy reaches 5.1.
+// rows take 102 us forwards, 125 backwards and 97 in 8 bits at best (medians 103, 131 and
+// 99), that is 5.3, 5.4 and 4.8 TB/s, where a copy reaches 5.1.
 constexpr int AN_FWD_BLOCKS = 2048, AN_BWD_BLOCKS = 512;
 
 struct AddNormParams {

@@ -308,8 +308,9 @@ __device__ __forceinline__ void glr_load_at(const void *src, int64_t row, int le
 }
 
 // Stores of results, past the caches, where the inputs' maps were read and they are read
-// again (16384 rows of 2048 channels in bf16, backwards: 131 us, with ordinary stores 140;
-// 4 x 4096 rows of 4096 channels 125 + 210 and 126 + 214).
+// again (whole calls, forwards + backwards: 16384 rows of 2048 channels in bf16, backwards
+// alone, 131 us, with ordinary stores 140; 4 x 4096 rows of 4096 channels 125 + 210 and
+// 126 + 214).
 template <typename P2>
 __device__ __forceinline__ void glr_store(GLR_GLOBAL char *base, uint32_t at, P2 v) {
   __builtin_nontemporal_store(v, reinterpret_cast<GLR_GLOBAL P2 *>(base + at));

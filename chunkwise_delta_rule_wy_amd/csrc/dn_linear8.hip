@@ -344,8 +344,10 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void linear8_tile_kerne
 // each, in blocks of 128.  The blocks pass through the wave's own part of LDS, two
 // at a time and without barriers, as in the tiles: a load into registers would touch
 // 16 rows at once, which takes twice the time for the same bytes (64 x 4096 x 4096:
-// 12.3 us, so 8.3).  What is left is latency: the launch, four blocks a wave that
-// depend on nothing but arrive one after the other, and the exchange of the waves' sums.
+// 12.3 us, so 8.3).  What is left: the launch, four blocks a wave that depend on nothing
+// but arrive one after the other, the exchange of the waves' sums, and with many rows x,
+// which every workgroup reads whole (64 rows of 4096: 256 KB beside 64 KB of weights, from
+// the L2's).
 constexpr int FEW_WAVES = 8;
 
 template <int MT>

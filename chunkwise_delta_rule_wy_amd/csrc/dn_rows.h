@@ -95,9 +95,9 @@ struct Row {
       for (int e = 0; e < V; ++e) x[k * V + e] = c < D ? src[c + e] : 0.f;
     }
   }
-  // PAST: past the caches, where one instruction's units fill whole lines (residual
-  // addition and norm of 16384 x 4096 bf16 values 103 us forwards, with ordinary stores 108;
-  // fp32 beside bf16, whose units come by halves, 160 and 156).
+  // PAST: past the caches, where one instruction's units fill whole lines (medians of the
+  // residual addition and norm of 16384 x 4096 bf16 values forwards: 103 us, with ordinary
+  // stores 108; fp32 beside bf16, whose units come by halves, 160 and 156).
   template <bool PAST = false, typename T>
   __device__ static __forceinline__ void store(T *dst, int lane, int D, const float (&x)[N]) {
     constexpr int U = Vec16<T>::N;
